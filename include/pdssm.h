@@ -352,6 +352,113 @@ pdssm_status pdssm_scan_bwd(const pdssm_problem *pb, const void *logits, const i
 pdssm_status pdssm_read_device_check(const void *workspace, pdssm_stream_t stream);
 
 /*
+ * Query and key preparation: the norm of every head and the rotation by position,
+ * in one pass over q and k (the layers that stand beside the PD scan take queries
+ * and keys of a fixed length: the delta rule below in the hybrid of Flash PD-SSM and
+ * DeltaNet layers of the Flash PD-SSM page, Experimental Results; B and C of a scan
+ * are its keys and queries too).
+ * For every token and head, x the head's N values and w the weight (1 when NULL):
+ *   z = x * w / sqrt(m + eps),  m = mean(x^2) (PDSSM_NORM_RMS) or sum(x^2) (PDSSM_NORM_L2)
+ *   y = z with its first `rot` values turned pair by pair: pair i < rot / 2 is
+ *       (z_i, z_{i + rot/2}), or (z_{2i}, z_{2i+1}) when interleaved, and becomes
+ *       (a cos - b sin, b cos + a sin) of the angle position * inv_freq[i]
+ * Sums and products are fp32, angles are reduced in double; y is rounded once.
+ *   q, q_out   device io_t [batch][seqlen][q_heads][N]; q_out may be q
+ *   k, k_out   device io_t [batch][seqlen][k_heads][N]; k_out may be k
+ *   wq, wk     device float [N] or NULL
+ *   inv_freq   device float [rot / 2]; NULL only when rot is 0
+ *   positions  device int32 [batch][seqlen], or NULL: the token's place t in its sequence
+ * A head of zeros with eps = 0 gives what the formula gives, NaN.
+ */
+typedef enum { PDSSM_NORM_RMS = 0, PDSSM_NORM_L2 = 1 } pdssm_norm_mode;
+
+typedef struct {
+  int64_t batch, seqlen, q_heads, k_heads, N; /* 1 <= N <= PDSSM_MAX_N; the others >= 0 */
+  int32_t io_t;                               /* PDSSM_F32 or PDSSM_BF16 */
+  int32_t mode;                               /* pdssm_norm_mode */
+  int32_t rot;                                /* even, 0 <= rot <= N */
+  int32_t interleaved;                        /* 0 or 1 */
+  float eps;                                  /* finite, >= 0 */
+  uint32_t flags;                             /* 0 */
+} pdssm_norm_problem;
+
+pdssm_status pdssm_qk_norm(const pdssm_norm_problem *pb, const void *q, const void *k, const float *wq,
+                           const float *wk, const float *inv_freq, const int32_t *positions, void *q_out,
+                           void *k_out, pdssm_stream_t stream);
+
+/*
+ * Its gradients: from q, k (the forward's inputs) and dq_out, dk_out (the gradients of
+ * its outputs, io_t), dq and dk (io_t, the inputs' shapes; dq may be dq_out, dk may be
+ * dk_out) and dwq, dwk (device float [N], NULL where not wanted; each needs its
+ * weight). The weights' gradients are sums over all tokens and heads in a fixed order.
+ *   workspace  pdssm_qk_norm_bwd_workspace_size bytes, 16-byte aligned (only the
+ *              weights' gradients use it; may be NULL when both are NULL)
+ */
+pdssm_status pdssm_qk_norm_bwd_workspace_size(const pdssm_norm_problem *pb, size_t *bytes);
+pdssm_status pdssm_qk_norm_bwd(const pdssm_norm_problem *pb, const void *q, const void *k, const float *wq,
+                               const float *wk, const float *inv_freq, const int32_t *positions,
+                               const void *dq_out, const void *dk_out, void *dq, void *dk, float *dwq, float *dwk,
+                               void *workspace, size_t workspace_bytes, pdssm_stream_t stream);
+
+/*
+ * The gated delta rule: the other layer of the hybrid of Flash PD-SSM and DeltaNet
+ * layers (Flash PD-SSM page, Experimental Results). Per sequence b and value head h,
+ * with the queries and keys of key head h / (heads / qk_heads):
+ *   e_t = v_t - exp(g_t) H_{t-1}^T k_t
+ *   H_t = exp(g_t) H_{t-1} + beta_t k_t e_t^T,   H_{-1} = h0 (or 0)
+ *   y_t = scale H_t^T q_t
+ * that is H_t = exp(g_t) (I - beta_t k_t k_t^T) H_{t-1} + beta_t k_t v_t^T.
+ *   q, k     device in_t [batch][seqlen][qk_heads][N]
+ *   v, y     device in_t [batch][seqlen][heads][P]
+ *   g, beta  device gate_t [batch][seqlen][heads]; g is the log of the decay (<= 0 in
+ *            use; below -110 the decay is 0, so -inf drops the state)
+ *   lengths  device int32 [batch] or NULL: sequence b has lengths[b] steps (values are
+ *            clamped to [0, seqlen]); the inputs behind them are not read, y is 0 there
+ *            and h_final is the state after the last step (h0 for a length of 0)
+ *   h0       device float [batch][heads][N][P] or NULL (zeros)
+ *   y        output; h_final device float [batch][heads][N][P] output, or NULL.
+ *            h_final may be h0 (the state is updated in place); no other buffers may
+ *            overlap.
+ * The state is fp32. Decoding is the call with seqlen = 1 and the state in h0 / h_final.
+ *   workspace pdssm_delta_workspace_size bytes, 16-byte aligned; may be NULL for 0.
+ * Calls that may run at the same time need workspaces of their own (two captured
+ * graphs that may be replayed side by side too). pdssm_qk_norm, pdssm_delta_fwd and
+ * their backward calls may be captured; the stream's device is current then.
+ * PDSSM_FLAG_REFERENCE_PATH: the step-by-step kernel whatever the problem.
+ */
+typedef struct {
+  int64_t batch, seqlen, heads, qk_heads, N, P; /* batch, seqlen >= 0; heads a multiple of qk_heads,
+                                                   both >= 1; 1 <= N <= PDSSM_MAX_N, 1 <= P <= PDSSM_MAX_P */
+  int32_t in_t, gate_t;                         /* PDSSM_F32 or PDSSM_BF16 */
+  float scale;                                  /* finite */
+  uint32_t flags;
+} pdssm_delta_problem;
+
+pdssm_status pdssm_delta_workspace_size(const pdssm_delta_problem *pb, size_t *bytes);
+pdssm_status pdssm_delta_fwd(const pdssm_delta_problem *pb, const void *q, const void *k, const void *v,
+                             const void *g, const void *beta, const int32_t *lengths, const float *h0, void *y,
+                             float *h_final, void *workspace, size_t workspace_bytes, pdssm_stream_t stream);
+
+/*
+ * Gradients of sum_t <dy_t, y_t> + <dh_final, h_final> for the forward pass on the same
+ * arguments:
+ *   dy       in_t [batch][seqlen][heads][P]; dh_final float [batch][heads][N][P] or NULL (zeros)
+ *   dq, dk   in_t [batch][seqlen][qk_heads][N]: sums over the value heads that share a key head
+ *   dv       in_t [batch][seqlen][heads][P];  dg, dbeta  gate_t [batch][seqlen][heads]
+ *   dh0      float [batch][heads][N][P] or NULL
+ * Each gradient has the type of what it belongs to and is rounded once. Rows behind a
+ * sequence's length get zeros. No atomics: the same call gives the same bits.
+ *   workspace pdssm_delta_bwd_workspace_size bytes, 16-byte aligned: for each value head
+ *            the states and adjoints at the chunks' ends (2 * N * P floats every 32
+ *            steps) and two rows of P floats a step.
+ */
+pdssm_status pdssm_delta_bwd_workspace_size(const pdssm_delta_problem *pb, size_t *bytes);
+pdssm_status pdssm_delta_bwd(const pdssm_delta_problem *pb, const void *q, const void *k, const void *v,
+                             const void *g, const void *beta, const int32_t *lengths, const float *h0, const void *dy,
+                             const float *dh_final, void *dq, void *dk, void *dv, void *dg, void *dbeta, float *dh0,
+                             void *workspace, size_t workspace_bytes, pdssm_stream_t stream);
+
+/*
  * Kernel tracing (observability; the pages describe none).
  * Between pdssm_trace_begin and pdssm_trace_end, every kernel the calling
  * thread's pdssm_* calls enqueue is bracketed by cudaEventRecord of

@@ -16,7 +16,15 @@ The functions keep the C names:
     pdssm_scan_bwd(problem, logits, s, idx, d, B, C, x, h0, dy, dh_final, tau, dlogits, dd, dB, dC, dx, dh0,
                    workspace, stream=None)
 
-``forward(...)`` is a convenience wrapper that allocates the outputs and the
+    pdssm_qk_norm(problem, q, k, wq, wk, inv_freq, positions, q_out, k_out, stream=None)
+    pdssm_qk_norm_bwd(problem, q, k, wq, wk, inv_freq, positions, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
+                      stream=None)
+    pdssm_delta_fwd(problem, q, k, v, g, beta, lengths, h0, y, h_final, workspace, stream=None)
+    pdssm_delta_bwd(problem, q, k, v, g, beta, lengths, h0, dy, dh_final, dq, dk, dv, dg, dbeta, dh0, workspace,
+                    stream=None)
+
+``qk_norm``, ``qk_norm_backward``, ``delta_forward`` and ``delta_backward`` check their tensors against one
+another, allocate the results and call these. ``forward(...)`` is a convenience wrapper that allocates the outputs and the
 workspace with torch and calls ``pdssm_forward``; ``backward(...)`` does the
 same for ``pdssm_scan_bwd``.
 """
@@ -37,6 +45,9 @@ __all__ = [
     "backward", "pdssm_dict_hardmax", "pdssm_select_proj", "dict_hardmax", "select_proj",
     "pdssm_soft_select_workspace_size", "pdssm_soft_select", "pdssm_scan_fwd_steps", "soft_select",
     "forward_steps",
+    "NormProblem", "DeltaProblem", "pdssm_qk_norm", "pdssm_qk_norm_bwd_workspace_size", "pdssm_qk_norm_bwd",
+    "pdssm_delta_workspace_size", "pdssm_delta_fwd", "pdssm_delta_bwd_workspace_size", "pdssm_delta_bwd",
+    "qk_norm", "qk_norm_backward", "delta_forward", "delta_backward",
 ]
 
 F32, BF16, C64 = 0, 1, 2
@@ -52,6 +63,8 @@ EXPORTED_SYMBOLS = (
     "pdssm_trace_end", "pdssm_trace_kernel_name", "pdssm_forward_noalloc", "pdssm_bwd_workspace_size",
     "pdssm_scan_bwd", "pdssm_dict_hardmax", "pdssm_select_proj", "pdssm_soft_select_workspace_size",
     "pdssm_soft_select", "pdssm_scan_fwd_steps",
+    "pdssm_qk_norm", "pdssm_qk_norm_bwd_workspace_size", "pdssm_qk_norm_bwd", "pdssm_delta_workspace_size",
+    "pdssm_delta_fwd", "pdssm_delta_bwd_workspace_size", "pdssm_delta_bwd",
 )
 
 _DIR = os.path.dirname(os.path.abspath(__file__))
@@ -71,6 +84,26 @@ class Problem(ctypes.Structure):
         ("chunk", ctypes.c_int32), ("logits_t", ctypes.c_int32), ("in_t", ctypes.c_int32),
         ("d_t", ctypes.c_int32), ("state_t", ctypes.c_int32), ("out_t", ctypes.c_int32),
         ("flags", ctypes.c_uint32),
+    ]
+
+
+class NormProblem(ctypes.Structure):
+    """Mirror of ``pdssm_norm_problem``."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("q_heads", ctypes.c_int64),
+        ("k_heads", ctypes.c_int64), ("N", ctypes.c_int64), ("io_t", ctypes.c_int32), ("mode", ctypes.c_int32),
+        ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float), ("flags", ctypes.c_uint32),
+    ]
+
+
+class DeltaProblem(ctypes.Structure):
+    """Mirror of ``pdssm_delta_problem``."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("heads", ctypes.c_int64),
+        ("qk_heads", ctypes.c_int64), ("N", ctypes.c_int64), ("P", ctypes.c_int64), ("in_t", ctypes.c_int32),
+        ("gate_t", ctypes.c_int32), ("scale", ctypes.c_float), ("flags", ctypes.c_uint32),
     ]
 
 
@@ -115,6 +148,17 @@ def _load() -> ctypes.CDLL:
     lib.pdssm_soft_select.restype = ctypes.c_int
     lib.pdssm_scan_fwd_steps.argtypes = [pb, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.pdssm_scan_fwd_steps.restype = ctypes.c_int
+    npb, dpb = ctypes.POINTER(NormProblem), ctypes.POINTER(DeltaProblem)
+    for name, argtypes in (
+            ("pdssm_qk_norm", [npb] + [vp] * 9),
+            ("pdssm_qk_norm_bwd_workspace_size", [npb, ctypes.POINTER(sz)]),
+            ("pdssm_qk_norm_bwd", [npb] + [vp] * 13 + [sz, vp]),
+            ("pdssm_delta_workspace_size", [dpb, ctypes.POINTER(sz)]),
+            ("pdssm_delta_fwd", [dpb] + [vp] * 10 + [sz, vp]),
+            ("pdssm_delta_bwd_workspace_size", [dpb, ctypes.POINTER(sz)]),
+            ("pdssm_delta_bwd", [dpb] + [vp] * 16 + [sz, vp])):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = argtypes, ctypes.c_int
     lib.pdssm_read_device_check.argtypes = [vp, vp]
     lib.pdssm_read_device_check.restype = ctypes.c_int
     lib.pdssm_trace_begin.argtypes = [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int32]
@@ -442,4 +486,231 @@ def backward(logits: Optional[torch.Tensor], s: torch.Tensor, idx: torch.Tensor,
                                                               dtype=torch.uint8, device=dev)
     pdssm_scan_bwd(pb, logits, s, idx, d, B, C, x, h0, dy, dh_final, tau, out.get("dlogits"), out["dd"], out["dB"],
                    out["dC"], out["dx"], out.get("dh0"), ws, stream)
+    return out
+
+
+# ------------------------------------------- layers beside the scan: q / k preparation, gated delta rule
+
+_NORM_MODES = {"rms": 0, "l2": 1}
+
+
+def _addr(t: Optional[torch.Tensor], index: int):
+    """Device address of a contiguous tensor on CUDA device ``index`` (None -> NULL)."""
+    if t is None:
+        return None
+    if t.get_device() != index or not t.is_contiguous():
+        _ptr(t, torch.device("cuda", index))  # says what is wrong with it
+    return t.data_ptr()
+
+
+def _expect(name: str, t: Optional[torch.Tensor], shape, dtype) -> None:
+    if t is not None and (t.shape != shape or t.dtype is not dtype):
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def _handle(stream, index: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _used_on(stream, index: int, tensors) -> None:
+    """Tensors allocated here for a call on ``stream``: the allocator must not reuse them before it is done."""
+    if stream is None:
+        return
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_handle(stream, index), index)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(s)
+
+
+def _size(fn, pb, where: str) -> int:
+    n = ctypes.c_size_t(0)
+    _check(fn(ctypes.byref(pb), ctypes.byref(n)), where)
+    return int(n.value)
+
+
+def _index(t: torch.Tensor) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError("libpdssm takes device memory only; got a CPU tensor")
+    return t.get_device()
+
+
+def _nbytes(workspace: Optional[torch.Tensor]) -> int:
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def pdssm_qk_norm(pb: NormProblem, q, k, wq, wk, inv_freq, positions, q_out, k_out, stream=None) -> None:
+    i = _index(q)
+    _check(_lib.pdssm_qk_norm(pb, _addr(q, i), _addr(k, i), _addr(wq, i), _addr(wk, i), _addr(inv_freq, i),
+                              _addr(positions, i), _addr(q_out, i), _addr(k_out, i), _handle(stream, i)), "pdssm_qk_norm")
+
+
+def pdssm_qk_norm_bwd_workspace_size(pb: NormProblem) -> int:
+    return _size(_lib.pdssm_qk_norm_bwd_workspace_size, pb, "pdssm_qk_norm_bwd_workspace_size")
+
+
+def pdssm_qk_norm_bwd(pb: NormProblem, q, k, wq, wk, inv_freq, positions, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
+                      stream=None) -> None:
+    i = _index(q)
+    _check(_lib.pdssm_qk_norm_bwd(pb, _addr(q, i), _addr(k, i), _addr(wq, i), _addr(wk, i), _addr(inv_freq, i),
+                                  _addr(positions, i), _addr(dq_out, i), _addr(dk_out, i), _addr(dq, i), _addr(dk, i),
+                                  _addr(dwq, i), _addr(dwk, i), _addr(workspace, i), _nbytes(workspace),
+                                  _handle(stream, i)), "pdssm_qk_norm_bwd")
+
+
+def pdssm_delta_workspace_size(pb: DeltaProblem) -> int:
+    return _size(_lib.pdssm_delta_workspace_size, pb, "pdssm_delta_workspace_size")
+
+
+def pdssm_delta_fwd(pb: DeltaProblem, q, k, v, g, beta, lengths, h0, y, h_final, workspace, stream=None) -> None:
+    i = _index(q)
+    _check(_lib.pdssm_delta_fwd(pb, _addr(q, i), _addr(k, i), _addr(v, i), _addr(g, i), _addr(beta, i),
+                                _addr(lengths, i), _addr(h0, i), _addr(y, i), _addr(h_final, i), _addr(workspace, i),
+                                _nbytes(workspace), _handle(stream, i)), "pdssm_delta_fwd")
+
+
+def pdssm_delta_bwd_workspace_size(pb: DeltaProblem) -> int:
+    return _size(_lib.pdssm_delta_bwd_workspace_size, pb, "pdssm_delta_bwd_workspace_size")
+
+
+def pdssm_delta_bwd(pb: DeltaProblem, q, k, v, g, beta, lengths, h0, dy, dh_final, dq, dk, dv, dg, dbeta, dh0, workspace,
+                    stream=None) -> None:
+    i = _index(q)
+    _check(_lib.pdssm_delta_bwd(pb, _addr(q, i), _addr(k, i), _addr(v, i), _addr(g, i), _addr(beta, i),
+                                _addr(lengths, i), _addr(h0, i), _addr(dy, i), _addr(dh_final, i), _addr(dq, i),
+                                _addr(dk, i), _addr(dv, i), _addr(dg, i), _addr(dbeta, i), _addr(dh0, i),
+                                _addr(workspace, i), _nbytes(workspace), _handle(stream, i)), "pdssm_delta_bwd")
+
+
+def _norm_problem(q, k, wq, wk, inv_freq, positions, eps, mode, interleaved) -> NormProblem:
+    if mode not in _NORM_MODES:
+        raise ValueError(f"mode must be 'rms' or 'l2', got {mode!r}")
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"q and k must be float32 or bfloat16, got {q.dtype}")
+    Bt, L, Hq, N = q.shape
+    _expect("k", k, (Bt, L, k.shape[2], N), q.dtype)
+    _expect("wq", wq, (N,), torch.float32)
+    _expect("wk", wk, (N,), torch.float32)
+    _expect("positions", positions, (Bt, L), torch.int32)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _expect("inv_freq", inv_freq, (rot // 2,), torch.float32)
+    return NormProblem(Bt, L, Hq, k.shape[2], N, _DT[q.dtype], _NORM_MODES[mode], rot, int(interleaved), eps, 0)
+
+
+def qk_norm(q: torch.Tensor, k: torch.Tensor, wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None,
+            inv_freq: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None, eps: float = 1e-6,
+            mode: str = "rms", interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+            k_out: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
+    """Norm of every head of q [Bt, L, Hq, N] and k [Bt, L, Hk, N], then the rotation of its first
+    2 * len(inv_freq) values by position (``positions`` int32 [Bt, L]; None: the token's place in its
+    sequence). ``mode``: "rms" or "l2". Results: "q", "k", written to ``q_out`` / ``k_out`` where given
+    (which may be q and k themselves)."""
+    pb = _norm_problem(q, k, wq, wk, inv_freq, positions, eps, mode, interleaved)
+    _expect("q_out", q_out, q.shape, q.dtype)
+    _expect("k_out", k_out, k.shape, q.dtype)
+    new = [torch.empty_like(q) if q_out is None else None, torch.empty_like(k) if k_out is None else None]
+    q_out, k_out = q_out if new[0] is None else new[0], k_out if new[1] is None else new[1]
+    pdssm_qk_norm(pb, q, k, wq, wk, inv_freq, positions, q_out, k_out, stream)
+    _used_on(stream, q.get_device(), new)
+    return {"q": q_out, "k": k_out}
+
+
+def qk_norm_backward(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_out: torch.Tensor,
+                     wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None,
+                     inv_freq: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                     eps: float = 1e-6, mode: str = "rms", interleaved: bool = False,
+                     stream=None) -> Dict[str, torch.Tensor]:
+    """Gradients of ``qk_norm`` from its inputs and its outputs' gradients: "dq", "dk" and, for each weight
+    given, "dwq", "dwk" (float32)."""
+    pb = _norm_problem(q, k, wq, wk, inv_freq, positions, eps, mode, interleaved)
+    _expect("dq_out", dq_out, q.shape, q.dtype)
+    _expect("dk_out", dk_out, k.shape, q.dtype)
+    out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k)}
+    if wq is not None:
+        out["dwq"] = torch.empty_like(wq)
+    if wk is not None:
+        out["dwk"] = torch.empty_like(wk)
+    ws = None
+    if len(out) > 2:
+        ws = torch.empty(pdssm_qk_norm_bwd_workspace_size(pb), dtype=torch.uint8, device=q.device)
+    pdssm_qk_norm_bwd(pb, q, k, wq, wk, inv_freq, positions, dq_out, dk_out, out["dq"], out["dk"], out.get("dwq"),
+                      out.get("dwk"), ws, stream)
+    _used_on(stream, q.get_device(), [ws, *out.values()])
+    return out
+
+
+def _delta_problem(q, k, v, g, beta, h0, scale, lengths, flags) -> DeltaProblem:
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"q, k and v must be float32 or bfloat16, got {q.dtype}")
+    if g.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"g and beta must be float32 or bfloat16, got {g.dtype}")
+    Bt, L, Hk, N = q.shape
+    H, P = v.shape[2:]
+    _expect("k", k, q.shape, q.dtype)
+    _expect("v", v, (Bt, L, H, P), q.dtype)
+    _expect("g", g, (Bt, L, H), g.dtype)
+    _expect("beta", beta, g.shape, g.dtype)
+    _expect("h0", h0, (Bt, H, N, P), torch.float32)
+    _expect("lengths", lengths, (Bt,), torch.int32)
+    return DeltaProblem(Bt, L, H, Hk, N, P, _DT[q.dtype], _DT[g.dtype], N ** -0.5 if scale is None else scale, flags)
+
+
+def delta_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                  h0: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                  lengths: Optional[torch.Tensor] = None, h_final: Optional[torch.Tensor] = None,
+                  want_h_final: bool = True, flags: int = 0, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> Dict[str, torch.Tensor]:
+    """The gated delta rule over whole sequences, or one token of each (L = 1 with the state in ``h0``).
+
+    q, k [Bt, L, Hk, N]; v [Bt, L, H, P] (H a multiple of Hk: value head h goes with key head h // (H / Hk));
+    g (log decay), beta [Bt, L, H]; h0 [Bt, H, N, P] float32; lengths int32 [Bt]: steps of each sequence, the
+    rest is padding. scale: N ** -0.5 by default. Results: "y" like v and, unless ``want_h_final`` is false,
+    "h_final", written to ``h_final`` where given, which may be ``h0`` itself."""
+    pb = _delta_problem(q, k, v, g, beta, h0, scale, lengths, flags)
+    i = _index(q)
+    y = torch.empty_like(v)
+    new = [y]
+    if h_final is not None:
+        _expect("h_final", h_final, (pb.batch, pb.heads, pb.N, pb.P), torch.float32)
+    elif want_h_final:
+        h_final = torch.empty(pb.batch, pb.heads, pb.N, pb.P, dtype=torch.float32, device=q.device)
+        new.append(h_final)
+    if workspace is None:
+        n = pdssm_delta_workspace_size(pb)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+            new.append(workspace)
+    pdssm_delta_fwd(pb, q, k, v, g, beta, lengths, h0, y, h_final, workspace, stream)
+    _used_on(stream, i, new)
+    return {"y": y} if h_final is None else {"y": y, "h_final": h_final}
+
+
+def delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                   dy: torch.Tensor, h0: Optional[torch.Tensor] = None, dh_final: Optional[torch.Tensor] = None,
+                   scale: Optional[float] = None, lengths: Optional[torch.Tensor] = None,
+                   want_dh0: Optional[bool] = None, flags: int = 0, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> Dict[str, torch.Tensor]:
+    """Gradients of ``delta_forward`` for dy (like v) and dh_final (float32 [Bt, H, N, P] or None: zeros):
+    "dq", "dk" (summed over the value heads that share a key head), "dv", "dg", "dbeta", each in the type of what
+    it belongs to, and "dh0" (by default where an h0 is given)."""
+    pb = _delta_problem(q, k, v, g, beta, h0, scale, lengths, flags)
+    _expect("dy", dy, v.shape, v.dtype)
+    _expect("dh_final", dh_final, (pb.batch, pb.heads, pb.N, pb.P), torch.float32)
+    i = _index(q)
+    out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v), "dg": torch.empty_like(g),
+           "dbeta": torch.empty_like(beta)}
+    if h0 is not None if want_dh0 is None else want_dh0:
+        out["dh0"] = torch.empty(pb.batch, pb.heads, pb.N, pb.P, dtype=torch.float32, device=q.device)
+    new = list(out.values())
+    if workspace is None:
+        workspace = torch.empty(pdssm_delta_bwd_workspace_size(pb), dtype=torch.uint8, device=q.device)
+        new.append(workspace)
+    pdssm_delta_bwd(pb, q, k, v, g, beta, lengths, h0, dy, dh_final, out["dq"], out["dk"], out["dv"], out["dg"],
+                    out["dbeta"], out.get("dh0"), workspace, stream)
+    _used_on(stream, i, new)
     return out

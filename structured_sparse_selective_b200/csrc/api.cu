@@ -5,25 +5,13 @@
 #include <algorithm>
 #include <mutex>
 
+#include "api_util.h"
 #include "launch.h"
 #include "pdssm.h"
 
 using namespace pdssm;
 
 namespace {
-
-size_t dtype_size(int dt) {
-  switch (dt) {
-    case PDSSM_F32: return 4;
-    case PDSSM_BF16: return 2;
-    case PDSSM_C64: return 8;
-    default: return 0;
-  }
-}
-
-bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
-
-size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct Plan {
   int64_t Bt, L, H, N, P, K, T, nC, rows;
@@ -123,8 +111,6 @@ Workspace carve(const Plan &p, void *ws) {
   return w;
 }
 
-bool aligned(const void *ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
-
 // Makes the device that owns `stream` current for this library's runtime.
 pdssm_status bind_device(cudaStream_t stream) {
   if (stream == nullptr) return PDSSM_OK;
@@ -135,8 +121,6 @@ pdssm_status bind_device(cudaStream_t stream) {
   if (cur != dev && cudaSetDevice(dev) != cudaSuccess) return PDSSM_ERR_CUDA;
   return PDSSM_OK;
 }
-
-pdssm_status cuda_status(cudaError_t e) { return e == cudaSuccess ? PDSSM_OK : PDSSM_ERR_CUDA; }
 
 pdssm_status check_scan_args(const pdssm_problem *pb, const Plan &p, const int32_t *idx,
                              const void *d, const void *B, const void *C, const void *x,

@@ -1,0 +1,263 @@
+// C-ABI entry points of the layers beside the scan: the norm and rotation of queries and
+// keys, and the gated delta rule. Validation, workspace layout and dispatch; the
+// contract is in include/pdssm.h.
+#include <math.h>
+
+#include <algorithm>
+
+#include "api_util.h"
+#include "launch.h"
+#include "pdssm.h"
+
+using namespace pdssm;
+
+namespace {
+
+// Makes the stream's device current for the call and puts the caller's back after it.
+// A capturing stream may not be asked for its device (the question ends the capture):
+// there the caller has that device current, as the capture needs it anyway.
+class OnDevice {
+ public:
+  explicit OnDevice(cudaStream_t stream) {
+    if (stream == nullptr) return;
+    cudaStreamCaptureStatus capturing;
+    if (cudaStreamIsCapturing(stream, &capturing) != cudaSuccess) {
+      status_ = PDSSM_ERR_CUDA;
+      return;
+    }
+    if (capturing != cudaStreamCaptureStatusNone) return;
+    int dev = -1;
+    if (cudaStreamGetDevice(stream, &dev) != cudaSuccess || cudaGetDevice(&before_) != cudaSuccess) {
+      status_ = PDSSM_ERR_CUDA;
+      return;
+    }
+    if (before_ == dev) return;
+    if (cudaSetDevice(dev) == cudaSuccess) changed_ = true;
+    else status_ = PDSSM_ERR_CUDA;
+  }
+  ~OnDevice() {
+    if (changed_) cudaSetDevice(before_);
+  }
+  pdssm_status status() const { return status_; }
+
+ private:
+  int before_ = 0;
+  bool changed_ = false;
+  pdssm_status status_ = PDSSM_OK;
+};
+
+bool real_type(int t) { return t == PDSSM_F32 || t == PDSSM_BF16; }
+
+pdssm_status check_norm(const pdssm_norm_problem *pb, int64_t *rows) {
+  if (!pb) return PDSSM_ERR_INVALID_ARG;
+  if (pb->batch < 0 || pb->seqlen < 0 || pb->q_heads < 0 || pb->k_heads < 0 || pb->N < 1 || pb->rot < 0 ||
+      (pb->rot & 1) || pb->rot > pb->N || !(pb->eps >= 0.f) || !(pb->eps < INFINITY) || pb->flags != 0 ||
+      (pb->interleaved != 0 && pb->interleaved != 1) || (pb->mode != PDSSM_NORM_RMS && pb->mode != PDSSM_NORM_L2))
+    return PDSSM_ERR_INVALID_ARG;
+  if (pb->N > PDSSM_MAX_N || !real_type(pb->io_t) || pb->q_heads > 65535 || pb->k_heads > 65535 ||
+      pb->seqlen > INT32_MAX)
+    return PDSSM_ERR_UNSUPPORTED;
+  int64_t n;
+  if (!mul_ok(pb->batch, pb->seqlen, rows) || !mul_ok(*rows, 65535 * PDSSM_MAX_N * 4, &n)) return PDSSM_ERR_UNSUPPORTED;
+  return PDSSM_OK;
+}
+
+size_t norm_bwd_bytes(const pdssm_norm_problem *pb, int64_t rows) {
+  return rows ? align256((size_t)2 * qk_norm_blocks(rows) * pb->N * 4) : 0;
+}
+
+pdssm_status run_norm(const pdssm_norm_problem *pb, QkNormArgs &a, int64_t rows, bool bwd, cudaStream_t cs) {
+  a.rows = rows; a.seqlen = pb->seqlen; a.heads[0] = pb->q_heads; a.heads[1] = pb->k_heads; a.N = pb->N;
+  a.io_t = pb->io_t; a.rot = pb->rot; a.interleaved = pb->interleaved;
+  a.l2 = pb->mode == PDSSM_NORM_L2;
+  a.eps = pb->eps;
+  return cuda_status(launch_qk_norm(a, bwd, cs));
+}
+
+struct DeltaPlan {
+  int64_t rows, slices, Pp, C, nC;
+  size_t o_carry, o_xcarry, o_e, o_du, fwd_bytes, bwd_bytes;
+};
+
+pdssm_status plan_delta(const pdssm_delta_problem *pb, DeltaPlan *pl) {
+  if (!pb) return PDSSM_ERR_INVALID_ARG;
+  if (pb->batch < 0 || pb->seqlen < 0 || pb->heads < 1 || pb->qk_heads < 1 || pb->heads % pb->qk_heads ||
+      pb->N < 1 || pb->P < 1 || !isfinite(pb->scale) ||
+      (pb->flags & ~(PDSSM_FLAG_REFERENCE_PATH | PDSSM_FLAG_SHORT_WAITS)))
+    return PDSSM_ERR_INVALID_ARG;
+  if (pb->N > PDSSM_MAX_N || pb->P > PDSSM_MAX_P || pb->batch > 65535 || pb->heads > 65535 ||
+      !real_type(pb->in_t) || !real_type(pb->gate_t) || pb->seqlen > (int64_t)1 << 35)
+    return PDSSM_ERR_UNSUPPORTED;
+  DeltaPlan p;
+  p.Pp = (pb->P + 3) / 4 * 4;
+  p.C = delta_grad_chunk();
+  p.nC = (pb->seqlen + p.C - 1) / p.C;
+  int64_t bytes;
+  p.slices = pb->batch * pb->heads;
+  // the largest array: carries of N x Pp floats a chunk, or rows of Pp floats a step
+  if (!mul_ok(pb->batch, pb->seqlen, &p.rows) || !mul_ok(p.slices, (p.nC + 1) * 65536, &bytes) ||
+      !mul_ok(p.rows * 8, pb->heads * PDSSM_MAX_N, &bytes))
+    return PDSSM_ERR_UNSUPPORTED;
+  size_t o = 0;
+  const size_t carries = (size_t)(p.slices * p.nC * pb->N * p.Pp) * 4, steps = (size_t)(p.rows * pb->heads * p.Pp) * 4;
+  p.o_carry = o; o = align256(o + carries);
+  p.o_xcarry = o; o = align256(o + carries);
+  p.o_e = o; o = align256(o + steps);
+  p.o_du = o; o = align256(o + steps);
+  p.bwd_bytes = o;
+  p.fwd_bytes = 0;
+  *pl = p;
+  return PDSSM_OK;
+}
+
+DeltaArgs delta_args(const pdssm_delta_problem *pb, const DeltaPlan &p) {
+  DeltaArgs a{};
+  a.Bt = pb->batch; a.L = pb->seqlen; a.H = pb->heads; a.Hk = pb->qk_heads; a.N = pb->N; a.P = pb->P;
+  a.Pp = p.Pp; a.C = p.C; a.nC = p.nC;
+  a.in_t = pb->in_t; a.gate_t = pb->gate_t;
+  a.scale = pb->scale;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+pdssm_status pdssm_qk_norm(const pdssm_norm_problem *pb, const void *q, const void *k, const float *wq,
+                           const float *wk, const float *inv_freq, const int32_t *positions, void *q_out,
+                           void *k_out, pdssm_stream_t stream) {
+  int64_t rows;
+  pdssm_status st = check_norm(pb, &rows);
+  if (st != PDSSM_OK) return st;
+  if (rows == 0 || pb->q_heads + pb->k_heads == 0) return PDSSM_OK;
+  const size_t es = dtype_size(pb->io_t);
+  if ((pb->q_heads && (!q || !q_out)) || (pb->k_heads && (!k || !k_out)) || (pb->rot && !inv_freq))
+    return PDSSM_ERR_INVALID_ARG;
+  if (!aligned(q, es) || !aligned(k, es) || !aligned(q_out, es) || !aligned(k_out, es) || !aligned(wq, 4) ||
+      !aligned(wk, 4) || !aligned(inv_freq, 4) || !aligned(positions, 4))
+    return PDSSM_ERR_INVALID_ARG;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  OnDevice on(cs);
+  if (on.status() != PDSSM_OK) return on.status();
+  QkNormArgs a{};
+  a.x[0] = q; a.x[1] = k; a.out[0] = q_out; a.out[1] = k_out; a.w[0] = wq; a.w[1] = wk;
+  a.inv_freq = inv_freq; a.positions = positions;
+  return run_norm(pb, a, rows, false, cs);
+}
+
+pdssm_status pdssm_qk_norm_bwd_workspace_size(const pdssm_norm_problem *pb, size_t *bytes) {
+  if (!bytes) return PDSSM_ERR_INVALID_ARG;
+  int64_t rows;
+  pdssm_status st = check_norm(pb, &rows);
+  if (st != PDSSM_OK) return st;
+  *bytes = norm_bwd_bytes(pb, rows);
+  return PDSSM_OK;
+}
+
+pdssm_status pdssm_qk_norm_bwd(const pdssm_norm_problem *pb, const void *q, const void *k, const float *wq,
+                               const float *wk, const float *inv_freq, const int32_t *positions,
+                               const void *dq_out, const void *dk_out, void *dq, void *dk, float *dwq, float *dwk,
+                               void *workspace, size_t workspace_bytes, pdssm_stream_t stream) {
+  int64_t rows;
+  pdssm_status st = check_norm(pb, &rows);
+  if (st != PDSSM_OK) return st;
+  const size_t es = dtype_size(pb->io_t);
+  if ((dwq && !wq) || (dwk && !wk)) return PDSSM_ERR_INVALID_ARG;
+  if (rows && ((pb->q_heads && (!q || !dq_out || !dq)) || (pb->k_heads && (!k || !dk_out || !dk)) || (pb->rot && !inv_freq)))
+    return PDSSM_ERR_INVALID_ARG;
+  if (!aligned(q, es) || !aligned(k, es) || !aligned(dq_out, es) || !aligned(dk_out, es) || !aligned(dq, es) ||
+      !aligned(dk, es) || !aligned(wq, 4) || !aligned(wk, 4) || !aligned(inv_freq, 4) || !aligned(positions, 4) ||
+      !aligned(dwq, 4) || !aligned(dwk, 4) || !aligned(workspace, 16))
+    return PDSSM_ERR_INVALID_ARG;
+  if ((dwq || dwk) && rows && (!workspace || workspace_bytes < norm_bwd_bytes(pb, rows))) return PDSSM_ERR_WORKSPACE;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  OnDevice on(cs);
+  if (on.status() != PDSSM_OK) return on.status();
+  if (rows == 0 || pb->q_heads + pb->k_heads == 0) {  // no tokens: nothing reaches the weights
+    if (dwq && cudaMemsetAsync(dwq, 0, pb->N * 4, cs) != cudaSuccess) return PDSSM_ERR_CUDA;
+    if (dwk && cudaMemsetAsync(dwk, 0, pb->N * 4, cs) != cudaSuccess) return PDSSM_ERR_CUDA;
+    return PDSSM_OK;
+  }
+  QkNormArgs a{};
+  a.x[0] = q; a.x[1] = k; a.dy[0] = dq_out; a.dy[1] = dk_out; a.out[0] = dq; a.out[1] = dk;
+  a.w[0] = wq; a.w[1] = wk; a.dw[0] = dwq; a.dw[1] = dwk;
+  a.inv_freq = inv_freq; a.positions = positions;
+  a.part = static_cast<float *>(workspace);
+  return run_norm(pb, a, rows, true, cs);
+}
+
+pdssm_status pdssm_delta_workspace_size(const pdssm_delta_problem *pb, size_t *bytes) {
+  if (!bytes) return PDSSM_ERR_INVALID_ARG;
+  DeltaPlan p;
+  pdssm_status st = plan_delta(pb, &p);
+  if (st != PDSSM_OK) return st;
+  *bytes = p.fwd_bytes;
+  return PDSSM_OK;
+}
+
+pdssm_status pdssm_delta_fwd(const pdssm_delta_problem *pb, const void *q, const void *k, const void *v,
+                             const void *g, const void *beta, const int32_t *lengths, const float *h0, void *y,
+                             float *h_final, void *workspace, size_t workspace_bytes, pdssm_stream_t stream) {
+  DeltaPlan p;
+  pdssm_status st = plan_delta(pb, &p);
+  if (st != PDSSM_OK) return st;
+  const size_t es = dtype_size(pb->in_t), gs = dtype_size(pb->gate_t);
+  if (p.rows * pb->heads > 0 && (!q || !k || !v || !g || !beta || !y)) return PDSSM_ERR_INVALID_ARG;
+  if (!aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(y, es) || !aligned(g, gs) ||
+      !aligned(beta, gs) || !aligned(lengths, 4) || !aligned(h0, 4) || !aligned(h_final, 4) || !aligned(workspace, 16))
+    return PDSSM_ERR_INVALID_ARG;
+  if (p.fwd_bytes && (!workspace || workspace_bytes < p.fwd_bytes)) return PDSSM_ERR_WORKSPACE;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  OnDevice on(cs);
+  if (on.status() != PDSSM_OK) return on.status();
+  if (p.slices == 0) return PDSSM_OK;
+  DeltaArgs a = delta_args(pb, p);
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lengths = lengths; a.h0 = h0; a.y = y; a.h_final = h_final;
+  return cuda_status(launch_delta_steps(a, cs));
+}
+
+pdssm_status pdssm_delta_bwd_workspace_size(const pdssm_delta_problem *pb, size_t *bytes) {
+  if (!bytes) return PDSSM_ERR_INVALID_ARG;
+  DeltaPlan p;
+  pdssm_status st = plan_delta(pb, &p);
+  if (st != PDSSM_OK) return st;
+  *bytes = p.bwd_bytes;
+  return PDSSM_OK;
+}
+
+pdssm_status pdssm_delta_bwd(const pdssm_delta_problem *pb, const void *q, const void *k, const void *v,
+                             const void *g, const void *beta, const int32_t *lengths, const float *h0, const void *dy,
+                             const float *dh_final, void *dq, void *dk, void *dv, void *dg, void *dbeta, float *dh0,
+                             void *workspace, size_t workspace_bytes, pdssm_stream_t stream) {
+  DeltaPlan p;
+  pdssm_status st = plan_delta(pb, &p);
+  if (st != PDSSM_OK) return st;
+  const size_t es = dtype_size(pb->in_t), gs = dtype_size(pb->gate_t);
+  if (p.rows * pb->heads > 0 &&
+      (!q || !k || !v || !g || !beta || !dy || !dq || !dk || !dv || !dg || !dbeta))
+    return PDSSM_ERR_INVALID_ARG;
+  if (!aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(dy, es) || !aligned(dq, es) ||
+      !aligned(dk, es) || !aligned(dv, es) || !aligned(g, gs) || !aligned(beta, gs) || !aligned(dg, gs) ||
+      !aligned(dbeta, gs) || !aligned(lengths, 4) || !aligned(h0, 4) || !aligned(dh_final, 4) || !aligned(dh0, 4) ||
+      !aligned(workspace, 16))
+    return PDSSM_ERR_INVALID_ARG;
+  if (p.bwd_bytes && (!workspace || workspace_bytes < p.bwd_bytes)) return PDSSM_ERR_WORKSPACE;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  OnDevice on(cs);
+  if (on.status() != PDSSM_OK) return on.status();
+  if (p.slices == 0) return PDSSM_OK;
+  DeltaArgs a = delta_args(pb, p);
+  char *base = static_cast<char *>(workspace);
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lengths = lengths; a.h0 = h0; a.dy = dy; a.dh_final = dh_final;
+  a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dh0 = dh0;
+  a.carry = reinterpret_cast<float *>(base + p.o_carry);
+  a.xcarry = reinterpret_cast<float *>(base + p.o_xcarry);
+  a.e = reinterpret_cast<float *>(base + p.o_e);
+  a.du = reinterpret_cast<float *>(base + p.o_du);
+  if (p.rows > 0 && (st = cuda_status(launch_delta_steps_save(a, cs))) != PDSSM_OK) return st;
+  if ((st = cuda_status(launch_delta_steps_bwd(a, cs))) != PDSSM_OK) return st;
+  if (p.rows > 0) st = cuda_status(launch_delta_grad(a, cs));
+  return st;
+}
+
+}  // extern "C"

@@ -1,0 +1,56 @@
+// What the gated delta rule's kernels share.
+//
+// Per (sequence b, value head h), with key head h / (heads / qk_heads), a_t = exp(g_t):
+//   e_t = v_t - a_t H_{t-1}^T k_t           (what the faded memory lacks of the value)
+//   H_t = a_t H_{t-1} + beta_t k_t e_t^T    (N x P)
+//   y_t = scale H_t^T q_t
+// and backwards, with X_t = dLoss/dH_t before the step is undone:
+//   X_t = X'_t + scale q_t dy_t^T,  du_t = X_t^T k_t,  dv_t = beta_t du_t,
+//   X'_{t-1} = a_t (X_t - k_t dv_t^T)
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace pdssm {
+
+// A decay below exp(-110) is 0 in fp32; the clamp keeps sums of log decays finite,
+// so that -inf (the state is dropped) is an ordinary value. NaN stays NaN.
+__device__ __forceinline__ float clamp_gate(float g) { return g < -110.f ? -110.f : g; }
+
+// Steps of sequence b that count: its length clamped to [0, L], or L.
+__device__ __forceinline__ int64_t live_steps(const int32_t *lengths, int64_t b, int64_t L) {
+  if (!lengths) return L;
+  const int64_t n = lengths[b];
+  return n < 0 ? 0 : (n > L ? L : n);
+}
+
+__device__ __forceinline__ float load_any(const void *p, int64_t i, bool bf16) {
+  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]) : static_cast<const float *>(p)[i];
+}
+
+__device__ __forceinline__ void store_any(void *p, int64_t i, bool bf16, float v) {
+  if (bf16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+  else static_cast<float *>(p)[i] = v;
+}
+
+// Two fp32 values in one register pair; one instruction works on both.
+using pair2 = unsigned long long;
+__device__ __forceinline__ pair2 pack2(float a, float b) {
+  pair2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(pair2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ pair2 fma2(pair2 a, pair2 b, pair2 c) {
+  pair2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ pair2 mul2(pair2 a, pair2 b) {
+  pair2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+}  // namespace pdssm

@@ -94,4 +94,51 @@ int64_t scan_bwd_scratch_steps();
 int64_t scan_bwd_column_blocks(int64_t slices, int64_t P, bool cplx);
 cudaError_t launch_scan_bwd(const ScanBwdArgs &a, cudaStream_t st);
 
+// The norm and rotation of query and key heads (csrc/qk_norm.cu). Index 0 is q, 1 is k;
+// `out` is y forwards and dx backwards. part: qk_norm_blocks(rows) * 2 * N floats where a
+// weight's gradient is wanted.
+struct QkNormArgs {
+  int64_t rows, seqlen, heads[2], N;
+  int io_t, rot, interleaved;
+  bool l2;
+  float eps;
+  const void *x[2], *dy[2];
+  void *out[2];
+  const float *w[2], *inv_freq;
+  const int32_t *positions;
+  float *dw[2], *part;
+};
+int qk_norm_blocks(int64_t rows);
+cudaError_t launch_qk_norm(const QkNormArgs &a, bool bwd, cudaStream_t st);
+
+// The gated delta rule (csrc/delta.cuh); validated and laid out by the C-ABI layer.
+struct DeltaArgs {
+  int64_t Bt, L, H, Hk, N, P;
+  int64_t Pp;     // P rounded up to a multiple of 4: row length of the workspace's arrays
+  int64_t C, nC;  // steps a chunk (a power of two) and chunks a sequence
+  int in_t, gate_t;
+  float scale;
+  const void *q, *k, *v, *g, *beta;
+  const int32_t *lengths;
+  const float *h0;
+  void *y;
+  float *h_final;
+  // backward
+  const void *dy;
+  const float *dh_final;
+  void *dq, *dk, *dv, *dg, *dbeta;
+  float *dh0;
+  // workspace: states before each chunk and adjoints behind it [Bt][H][nC][N][Pp],
+  // e_t and du_t [Bt][L][H][Pp]
+  float *carry, *xcarry, *e, *du;
+};
+// Step by step, any size; the outputs y and h_final.
+cudaError_t launch_delta_steps(const DeltaArgs &a, cudaStream_t st);
+// The same steps, writing carry and e instead; and the adjoint's steps (dv, dh0, xcarry, du).
+cudaError_t launch_delta_steps_save(const DeltaArgs &a, cudaStream_t st);
+cudaError_t launch_delta_steps_bwd(const DeltaArgs &a, cudaStream_t st);
+// dq, dk, dg and dbeta of every chunk from its carries, e and du.
+int64_t delta_grad_chunk();
+cudaError_t launch_delta_grad(const DeltaArgs &a, cudaStream_t st);
+
 }  // namespace pdssm
