@@ -5,7 +5,7 @@
 // (rg, cl) = (lane / 4, lane % 4) holds columns 4 cl .. 4 cl + 3 and rows
 // 32 j + 4 rg .. + 3 in registers for the whole sequence, so the state moves once in
 // and once out. k^T H is a sum over the lane's rows and three shuffles over the eight
-// row groups; no barrier joins the warps but the one a tile of 16 steps has, whose
+// row groups; no barrier joins the warps but the one a tile of 8 steps has, whose
 // k, q, v, decay and beta a loader warp brings to shared memory in fp32 while the
 // others work on the tile before.
 // A step's products are in row pairs (fma.rn.f32x2), which halves the instructions.
@@ -20,7 +20,7 @@ namespace pdssm {
 
 namespace {
 
-constexpr int kTS = 16;       // steps a tile
+constexpr int kTS = 8;        // steps a tile
 constexpr int kWarpCols = 16;
 constexpr int kMaxWarps = PDSSM_MAX_P / kWarpCols;
 
@@ -42,53 +42,73 @@ struct Tile {
   static size_t bytes(int cols) { return (size_t)2 * kTS * (2 * kRow + cols + 2) * 4; }
 };
 
-// The loader warp: steps [t0, t0 + n) into `tile`; `src` is v forwards, dy backwards.
+// The loader warp. A tile's values wait in registers while the tile before is computed:
+// fetch() starts the loads of one tile, put() writes them to shared memory a tile later,
+// so HBM's latency is behind a whole tile's work. The loads are unconditional, from a
+// valid place where there is nothing to load: with a branch around each they ran one
+// after the other (LM layer: 1.9 ms).
 template <int J, typename T, typename G>
-__device__ __forceinline__ void load_tile(const DeltaArgs &a, const Tile<J> &tile, int64_t b, int64_t h, int64_t t0, int n,
-                                          int p0, int cols, const void *src_) {
-  const int lane = threadIdx.x & 31;
-  const int64_t hk = h / (a.H / a.Hk);
-  const T *src = static_cast<const T *>(src_);
-  constexpr int R = 4;  // steps whose loads are in flight together
-  const int N = (int)a.N, P = (int)a.P;
-  for (int s0 = 0; s0 < n; s0 += R) {
-    float kv[R][J], qv[R][J], cv[R][kMaxWarps / 2];
+struct Loader {
+  static constexpr int M = kMaxWarps / 2;
+  const DeltaArgs &a;
+  const T *k, *q, *c;
+  const G *g, *beta;
+  int lane, p0, cols, n;
+  int64_t rowk, rowc;
+  T kv[kTS][J], qv[kTS][J], cv[kTS][M];
+  G gv, bv;
+
+  // `src`: v forwards, dy backwards.
+  __device__ Loader(const DeltaArgs &a_, int64_t b, int64_t h, int p0_, int cols_, const void *src)
+      : a(a_), lane(threadIdx.x & 31), p0(p0_), cols(cols_), n(0), rowk(a_.Hk * a_.N), rowc(a_.H * a_.P) {
+    const int64_t hk = h / (a.H / a.Hk);
+    k = static_cast<const T *>(a.k) + b * a.L * rowk + hk * a.N;
+    q = static_cast<const T *>(a.q) + b * a.L * rowk + hk * a.N;
+    c = static_cast<const T *>(src) + b * a.L * rowc + h * a.P;
+    g = static_cast<const G *>(a.g) + b * a.L * a.H + h;
+    beta = static_cast<const G *>(a.beta) + b * a.L * a.H + h;
+  }
+
+  // Steps [t0, t0 + steps), steps <= kTS; nothing for steps <= 0.
+  __device__ __forceinline__ void fetch(int64_t t0, int64_t steps) {
+    n = (int)(steps < kTS ? steps : kTS);
+    if (n <= 0) return;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const bool on = s0 + r < n;
-      const int64_t row = b * a.L + t0 + s0 + r;
-      const T *kp = static_cast<const T *>(a.k) + (row * a.Hk + hk) * a.N;
-      const T *qp = static_cast<const T *>(a.q) + (row * a.Hk + hk) * a.N;
-      const T *cp = src + (row * a.H + h) * a.P + p0;
+    for (int s = 0; s < kTS; ++s) {
+      const int64_t t = t0 + min(s, n - 1);
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int i = min(lane + 32 * j, (int)a.N - 1);
+        kv[s][j] = k[t * rowk + i];
+        qv[s][j] = q[t * rowk + i];
+      }
+#pragma unroll
+      for (int j = 0; j < M; ++j) cv[s][j] = c[t * rowc + min(p0 + min(lane + 32 * j, cols - 1), (int)a.P - 1)];
+    }
+    const int64_t t = (t0 + min(lane, n - 1)) * a.H;
+    gv = g[t];
+    bv = beta[t];
+  }
+
+  __device__ __forceinline__ void put(const Tile<J> &tile) {
+    if (n <= 0) return;
+#pragma unroll
+    for (int s = 0; s < kTS; ++s) {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const int i = lane + 32 * j;
-        kv[r][j] = on && i < N ? ldf(kp + i) : 0.f;
-        qv[r][j] = on && i < N ? ldf(qp + i) : 0.f;
+        tile.k[s * 32 * J + i] = i < a.N ? to_f32(kv[s][j]) : 0.f;
+        tile.q[s * 32 * J + i] = i < a.N ? to_f32(qv[s][j]) * a.scale : 0.f;
       }
 #pragma unroll
-      for (int j = 0; j < kMaxWarps / 2; ++j) {
+      for (int j = 0; j < M; ++j) {
         const int i = lane + 32 * j;
-        cv[r][j] = on && i < cols && p0 + i < P ? ldf(cp + i) : 0.f;
+        if (i < cols) tile.c[s * cols + i] = p0 + i < a.P ? to_f32(cv[s][j]) : 0.f;
       }
     }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        tile.k[(s0 + r) * 32 * J + lane + 32 * j] = kv[r][j];
-        tile.q[(s0 + r) * 32 * J + lane + 32 * j] = qv[r][j] * a.scale;
-      }
-#pragma unroll
-      for (int j = 0; j < kMaxWarps / 2; ++j)
-        if (lane + 32 * j < cols) tile.c[(s0 + r) * cols + lane + 32 * j] = cv[r][j];
-    }
+    if (lane < kTS) tile.ab[lane] = make_float2(expf(clamp_gate(to_f32(gv))), to_f32(bv));
   }
-  if (lane < n) {
-    const int64_t i = (b * a.L + t0 + lane) * a.H + h;
-    tile.ab[lane] = make_float2(expf(clamp_gate(ldf(static_cast<const G *>(a.g) + i))), ldf(static_cast<const G *>(a.beta) + i));
-  }
-}
+};
 
 // The lane's part of a state [N][P] at `p` (null: zeros), in row pairs.
 template <int J>
@@ -201,54 +221,60 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1)) delta_steps_kernel(Delta
   const int64_t len = live_steps(a.lengths, b, a.L);
   const int col = p0 + warp * kWarpCols + 4 * (lane & 3);
   const bool loader = warp == warps;
+  if (loader) {
+    Loader<J, T, G> in(a, b, h, p0, cols, a.v);
+    in.fetch(0, len);
+    in.put(Tile<J>(smem, cols, 0));
+    in.fetch(kTS, len - kTS);
+    __syncthreads();
+    for (int64_t t0 = 0, i = 0; t0 < len; t0 += kTS, ++i) {
+      in.put(Tile<J>(smem, cols, (i + 1) & 1));
+      in.fetch(t0 + 2 * kTS, len - t0 - 2 * kTS);
+      __syncthreads();
+    }
+    return;
+  }
   pair2 st[2 * J][4];
-  if (!loader) load_state<J>(st, a.h0 ? a.h0 + bh * a.N * a.P : nullptr, a.N, a.P, a.P, rg, col);
-  else if (len > 0) load_tile<J, T, G>(a, Tile<J>(smem, cols, 0), b, h, 0, (int)min((int64_t)kTS, len), p0, cols, a.v);
+  load_state<J>(st, a.h0 ? a.h0 + bh * a.N * a.P : nullptr, a.N, a.P, a.P, rg, col);
   __syncthreads();
   const int yc = 2 * (lane >> 4) + ((lane >> 3) & 1);
   T *y = static_cast<T *>(a.y);
   for (int64_t t0 = 0, i = 0; t0 < len; t0 += kTS, ++i) {
-    if (loader) {
-      if (t0 + kTS < len)
-        load_tile<J, T, G>(a, Tile<J>(smem, cols, (i + 1) & 1), b, h, t0 + kTS, (int)min((int64_t)kTS, len - t0 - kTS), p0, cols, a.v);
-    } else {
-      const Tile<J> tile(smem, cols, i & 1);
-      const int n = (int)min((int64_t)kTS, len - t0);
-      for (int s = 0; s < n; ++s) {
-        if (SAVE && ((t0 + s) & (a.C - 1)) == 0)
-          store_state<J>(st, a.carry + (bh * a.nC + (t0 + s) / a.C) * a.N * a.Pp, a.N, a.Pp, a.Pp, rg, col);
-        pair2 k[2 * J], q[2 * J];
-        load_rows<J>(k, tile.k + s * 32 * J, rg);
-        load_rows<J>(q, tile.q + s * 32 * J, rg);
-        const float4 v4 = *reinterpret_cast<const float4 *>(tile.c + s * cols + warp * kWarpCols + 4 * (lane & 3));
-        const float2 ab = tile.ab[s];
-        float d[4], e[4];
-        dot_rows<J>(d, k, st);
-        sum_groups(d);
-        e[0] = fmaf(-ab.x, d[0], v4.x); e[1] = fmaf(-ab.x, d[1], v4.y);
-        e[2] = fmaf(-ab.x, d[2], v4.z); e[3] = fmaf(-ab.x, d[3], v4.w);
-        const int64_t row = (b * a.L + t0 + s) * a.H + h;
-        if (SAVE && lane < 4 && col < a.Pp)
-          *reinterpret_cast<float4 *>(a.e + row * a.Pp + col) = make_float4(e[0], e[1], e[2], e[3]);
-        const pair2 aa = pack2(ab.x, ab.x);
+    const Tile<J> tile(smem, cols, i & 1);
+    const int n = (int)min((int64_t)kTS, len - t0);
+    for (int s = 0; s < n; ++s) {
+      if (SAVE && ((t0 + s) & (a.C - 1)) == 0)
+        store_state<J>(st, a.carry + (bh * a.nC + (t0 + s) / a.C) * a.N * a.Pp, a.N, a.Pp, a.Pp, rg, col);
+      pair2 k[2 * J], q[2 * J];
+      load_rows<J>(k, tile.k + s * 32 * J, rg);
+      load_rows<J>(q, tile.q + s * 32 * J, rg);
+      const float4 v4 = *reinterpret_cast<const float4 *>(tile.c + s * cols + warp * kWarpCols + 4 * (lane & 3));
+      const float2 ab = tile.ab[s];
+      float d[4], e[4];
+      dot_rows<J>(d, k, st);
+      sum_groups(d);
+      e[0] = fmaf(-ab.x, d[0], v4.x); e[1] = fmaf(-ab.x, d[1], v4.y);
+      e[2] = fmaf(-ab.x, d[2], v4.z); e[3] = fmaf(-ab.x, d[3], v4.w);
+      const int64_t row = (b * a.L + t0 + s) * a.H + h;
+      if (SAVE && lane < 4 && col < a.Pp)
+        *reinterpret_cast<float4 *>(a.e + row * a.Pp + col) = make_float4(e[0], e[1], e[2], e[3]);
+      const pair2 aa = pack2(ab.x, ab.x);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float u = ab.y * e[c];
-          const pair2 uu = pack2(u, u);
+      for (int c = 0; c < 4; ++c) {
+        const float u = ab.y * e[c];
+        const pair2 uu = pack2(u, u);
 #pragma unroll
-          for (int r = 0; r < 2 * J; ++r) st[r][c] = fma2(k[r], uu, mul2(aa, st[r][c]));
-        }
-        if (!SAVE) {
-          float z[4];
-          dot_rows<J>(z, q, st);
-          const float out = sum_groups_one(z, lane);
-          if (!(lane & 4) && col + yc < a.P) st_out(y + row * a.P + col + yc, out);
-        }
+        for (int r = 0; r < 2 * J; ++r) st[r][c] = fma2(k[r], uu, mul2(aa, st[r][c]));
+      }
+      if (!SAVE) {
+        float z[4];
+        dot_rows<J>(z, q, st);
+        const float out = sum_groups_one(z, lane);
+        if (!(lane & 4) && col + yc < a.P) st_out(y + row * a.P + col + yc, out);
       }
     }
     __syncthreads();
   }
-  if (loader) return;
   if (!SAVE) {
     for (int64_t t = len + rg; t < a.L; t += 8)
       for (int c = 0; c < 4; ++c)
@@ -269,59 +295,68 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1)) delta_steps_bwd_kernel(D
   const int col = p0 + warp * kWarpCols + 4 * (lane & 3);
   const bool loader = warp == warps;
   const int64_t tiles = (len + kTS - 1) / kTS;
+  if (loader) {
+    Loader<J, T, G> in(a, b, h, p0, cols, a.dy);
+    const auto fetch = [&](int64_t i) {  // the i-th tile from the end; nothing behind the first
+      const int64_t t0 = (tiles - 1 - i) * kTS;
+      in.fetch(t0, i < tiles ? len - t0 : 0);
+    };
+    fetch(0);
+    in.put(Tile<J>(smem, cols, 0));
+    fetch(1);
+    __syncthreads();
+    for (int64_t i = 0; i < tiles; ++i) {
+      in.put(Tile<J>(smem, cols, (i + 1) & 1));
+      fetch(i + 2);
+      __syncthreads();
+    }
+    return;
+  }
   pair2 st[2 * J][4];
-  if (!loader)
-    load_state<J>(st, a.dh_final ? a.dh_final + bh * a.N * a.P : nullptr, a.N, a.P, a.P, rg, col);
-  else if (tiles > 0)
-    load_tile<J, T, G>(a, Tile<J>(smem, cols, 0), b, h, (tiles - 1) * kTS, (int)(len - (tiles - 1) * kTS), p0, cols, a.dy);
+  load_state<J>(st, a.dh_final ? a.dh_final + bh * a.N * a.P : nullptr, a.N, a.P, a.P, rg, col);
   __syncthreads();
   T *dv = static_cast<T *>(a.dv);
   for (int64_t i = 0; i < tiles; ++i) {
     const int64_t t0 = (tiles - 1 - i) * kTS;
-    if (loader) {
-      if (t0 > 0) load_tile<J, T, G>(a, Tile<J>(smem, cols, (i + 1) & 1), b, h, t0 - kTS, kTS, p0, cols, a.dy);
-    } else {
-      const Tile<J> tile(smem, cols, i & 1);
-      const int n = (int)min((int64_t)kTS, len - t0);
-      for (int s = n - 1; s >= 0; --s) {
-        const int64_t t = t0 + s;
-        if (t == len - 1 || ((t + 1) & (a.C - 1)) == 0)
-          store_state<J>(st, a.xcarry + (bh * a.nC + t / a.C) * a.N * a.Pp, a.N, a.Pp, a.Pp, rg, col);
-        pair2 k[2 * J], q[2 * J];
-        load_rows<J>(k, tile.k + s * 32 * J, rg);
-        load_rows<J>(q, tile.q + s * 32 * J, rg);
-        const float4 d4 = *reinterpret_cast<const float4 *>(tile.c + s * cols + warp * kWarpCols + 4 * (lane & 3));
-        const float2 ab = tile.ab[s];
-        const float dy[4] = {d4.x, d4.y, d4.z, d4.w};
+    const Tile<J> tile(smem, cols, i & 1);
+    const int n = (int)min((int64_t)kTS, len - t0);
+    for (int s = n - 1; s >= 0; --s) {
+      const int64_t t = t0 + s;
+      if (t == len - 1 || ((t + 1) & (a.C - 1)) == 0)
+        store_state<J>(st, a.xcarry + (bh * a.nC + t / a.C) * a.N * a.Pp, a.N, a.Pp, a.Pp, rg, col);
+      pair2 k[2 * J], q[2 * J];
+      load_rows<J>(k, tile.k + s * 32 * J, rg);
+      load_rows<J>(q, tile.q + s * 32 * J, rg);
+      const float4 d4 = *reinterpret_cast<const float4 *>(tile.c + s * cols + warp * kWarpCols + 4 * (lane & 3));
+      const float2 ab = tile.ab[s];
+      const float dy[4] = {d4.x, d4.y, d4.z, d4.w};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const pair2 dd = pack2(dy[c], dy[c]);
+      for (int c = 0; c < 4; ++c) {
+        const pair2 dd = pack2(dy[c], dy[c]);
 #pragma unroll
-          for (int r = 0; r < 2 * J; ++r) st[r][c] = fma2(q[r], dd, st[r][c]);
-        }
-        float du[4];
-        dot_rows<J>(du, k, st);
-        sum_groups(du);
-        const int64_t row = (b * a.L + t) * a.H + h;
-        const pair2 aa = pack2(ab.x, ab.x);
+        for (int r = 0; r < 2 * J; ++r) st[r][c] = fma2(q[r], dd, st[r][c]);
+      }
+      float du[4];
+      dot_rows<J>(du, k, st);
+      sum_groups(du);
+      const int64_t row = (b * a.L + t) * a.H + h;
+      const pair2 aa = pack2(ab.x, ab.x);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float w = -ab.y * du[c];
-          const pair2 ww = pack2(w, w);
+      for (int c = 0; c < 4; ++c) {
+        const float w = -ab.y * du[c];
+        const pair2 ww = pack2(w, w);
 #pragma unroll
-          for (int r = 0; r < 2 * J; ++r) st[r][c] = mul2(aa, fma2(k[r], ww, st[r][c]));
-        }
-        if (lane < 4 && col < a.Pp) {
-          *reinterpret_cast<float4 *>(a.du + row * a.Pp + col) = make_float4(du[0], du[1], du[2], du[3]);
+        for (int r = 0; r < 2 * J; ++r) st[r][c] = mul2(aa, fma2(k[r], ww, st[r][c]));
+      }
+      if (lane < 4 && col < a.Pp) {
+        *reinterpret_cast<float4 *>(a.du + row * a.Pp + col) = make_float4(du[0], du[1], du[2], du[3]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (col + c < a.P) st_out(dv + row * a.P + col + c, ab.y * du[c]);
-        }
+        for (int c = 0; c < 4; ++c)
+          if (col + c < a.P) st_out(dv + row * a.P + col + c, ab.y * du[c]);
       }
     }
     __syncthreads();
   }
-  if (loader) return;
   for (int64_t t = len + rg; t < a.L; t += 8)
     for (int c = 0; c < 4; ++c)
       if (col + c < a.P) st_out(dv + ((b * a.L + t) * a.H + h) * a.P + col + c, 0.f);
