@@ -6,6 +6,7 @@
 #include <algorithm>
 
 #include "api_util.h"
+#include "delta_chunk.cuh"
 #include "launch.h"
 #include "pdssm.h"
 
@@ -76,8 +77,17 @@ pdssm_status run_norm(const pdssm_norm_problem *pb, QkNormArgs &a, int64_t rows,
 
 struct DeltaPlan {
   int64_t rows, slices, Pp, C, nC;
+  bool chunked;  // forward on the tensor cores
+  int64_t nF;    // its chunks a sequence
   size_t o_carry, o_xcarry, o_e, o_du, fwd_bytes, bwd_bytes;
 };
+
+constexpr size_t kErrBytes = 256;
+
+// bf16 sequences of more than a chunk go by chunks.
+bool chunks_apply(const pdssm_delta_problem *pb) {
+  return pb->in_t == PDSSM_BF16 && pb->seqlen > kChunk && !(pb->flags & PDSSM_FLAG_REFERENCE_PATH);
+}
 
 pdssm_status plan_delta(const pdssm_delta_problem *pb, DeltaPlan *pl) {
   if (!pb) return PDSSM_ERR_INVALID_ARG;
@@ -105,7 +115,9 @@ pdssm_status plan_delta(const pdssm_delta_problem *pb, DeltaPlan *pl) {
   p.o_e = o; o = align256(o + steps);
   p.o_du = o; o = align256(o + steps);
   p.bwd_bytes = o;
-  p.fwd_bytes = 0;
+  p.chunked = chunks_apply(pb);
+  p.nF = (pb->seqlen + kChunk - 1) / kChunk;
+  p.fwd_bytes = p.chunked ? kErrBytes + (size_t)(p.slices * p.nF * delta_record_bytes(false)) : 0;
   *pl = p;
   return PDSSM_OK;
 }
@@ -213,7 +225,15 @@ pdssm_status pdssm_delta_fwd(const pdssm_delta_problem *pb, const void *q, const
   if (p.slices == 0) return PDSSM_OK;
   DeltaArgs a = delta_args(pb, p);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lengths = lengths; a.h0 = h0; a.y = y; a.h_final = h_final;
-  return cuda_status(launch_delta_steps(a, cs));
+  if (!p.chunked) return cuda_status(launch_delta_steps(a, cs));
+  a.err = static_cast<uint32_t *>(workspace);
+  a.records = static_cast<uint8_t *>(workspace) + kErrBytes;
+  a.rec_bytes = delta_record_bytes(false);
+  a.C = kChunk; a.nC = p.nF;
+  a.wait_ns = (pb->flags & PDSSM_FLAG_SHORT_WAITS) ? 1000ull : 2000000000ull;
+  if (cudaMemsetAsync(a.err, 0, 4, cs) != cudaSuccess) return PDSSM_ERR_CUDA;
+  if ((st = cuda_status(launch_delta_prep(a, false, cs))) != PDSSM_OK) return st;
+  return cuda_status(launch_delta_chunk(a, cs));
 }
 
 pdssm_status pdssm_delta_bwd_workspace_size(const pdssm_delta_problem *pb, size_t *bytes) {

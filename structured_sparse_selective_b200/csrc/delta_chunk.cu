@@ -1,0 +1,422 @@
+// The gated delta rule by chunks of 64 steps, second part: the state from chunk to
+// chunk and the outputs, one block per (sequence, head) (bf16 inputs; the records of
+// csrc/delta_prep.cu; formulas in delta.cuh).
+//
+// For one chunk that starts from H, in the transposed form the tensor cores work on
+// (rows are the value's columns p, M = 64 or 128 of them):
+//   S = H^T K^T                       E = (V^T - S diag(exp G)) Te^T      u = beta e
+//   H'^T = exp(G_64) H^T + (u exp(G_64 - G))^T K
+//   Y^T = scale (H^T Q^T) diag(exp G) + U^T A^T
+// Everything left of a product comes from tensor memory, where a thread has one row p
+// (or a piece of it) and writes what it just computed; everything right of it is K, Q,
+// Te or A in shared memory, K and Q read as [steps][n] for the first products and as
+// [n][steps] for the update from the same bytes.
+//
+// Precision. K, Q, V are bf16 and exact. What is fp32 (H, R, u) is split into bf16 parts
+// that are multiplied one by one and summed in fp32: three parts (24 bits) on the way to
+// the state, so that it is an fp32 state; two parts (16 bits) where only y is
+// reached, which is rounded to bf16 itself.
+// SAVE (the forward of a backward pass) keeps three everywhere, since gradients of the
+// gates are differences of fp32 sums over y.
+//
+// The chain K H -> Te -> K^T u is what a sequence waits for; it runs once a chunk, and the
+// other products fill the pipe in its pauses. Roles (12 warps): 8 keep the state (fp32, in
+// registers: a row's n-range each) and do all elementwise work, a ninth issues the
+// products, two bring K, Q (16-byte cp.async into the operand order), V and the record
+// (one bulk copy) a chunk ahead into two stages, and one writes y from shared memory.
+// Every wait is bounded; after a timeout a role goes on without waiting, on data inside
+// its buffers, and the last one waits for the tensor core before tensor memory is freed.
+#include <algorithm>
+
+#include "delta.cuh"
+#include "delta_chunk.cuh"
+#include "sm100.cuh"
+
+namespace pdssm {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kStateWarps = 8, kIssuer = 8, kLoader0 = 9, kLoaders = 2, kWriter = 11;
+constexpr int kThreads = 32 * (kWriter + 1);
+constexpr int kGroup = kChunk * 16 + 16;  // bytes of eight columns of K or Q; 16 more spread the banks
+
+enum Bar { kFull0, kFull1, kFree0, kFree1, kH, kR, kU1, kU2, kDoneS, kDoneU, kDoneD, kDoneY, kOut, kOutFree, kEnd, kBars };
+
+template <int NP, int PM, bool SAVE>
+struct Layout {
+  // tensor memory, 32-bit columns: X holds the state's parts (K H and Q H read them), then
+  // u's parts; D the parts of R, then the update; Z first S, then E.
+  static constexpr int kX = 0, kXn = 3 * NP / 2;
+  static constexpr int kD = kXn, kDn = NP > 96 ? NP : 96;
+  static constexpr int kYh = kD + kDn, kYa = kYh + 64, kZ = kYa + 64;
+  static constexpr int kUd = kX;                                 // u exp(G_64 - G), three parts
+  static constexpr int kUy = NP == 128 ? kX + 96 : kZ + 64;      // u, two or three parts
+  static constexpr int kUyn = SAVE ? 96 : 64;
+  static constexpr int kCols = 512;
+  static_assert(kZ + 64 <= kCols && (NP == 128 || kUy + kUyn <= kCols) && (NP < 128 || 96 + kUyn <= kXn), "columns");
+  // shared memory of a stage
+  static constexpr int kRec = (3 + delta_a_parts(SAVE)) * kSquare + kScalars;
+  static constexpr int kQ = (NP / 8) * kGroup, kV = kChunk * PM * 2;  // V and Y: [step][p]
+  static constexpr int kVOff = 2 * kQ, kRecOff = kVOff + kV, kStage = kRecOff + kRec;
+  static constexpr int kYOff = 2 * kStage, kBarOff = kYOff + (SAVE ? 0 : kV), kBytes = kBarOff + 8 * kBars + 16;
+  // a thread's share of a row: W of 64 steps, WN of NP state values
+  static constexpr int kParts = 256 / PM, W = kChunk / kParts, WN = NP / kParts;
+};
+
+// `n` fp32 values as packed bf16 parts 0 .. PARTS - 1 into columns col, col + stride, ...
+// of the thread's row (col already at the thread's or the warp's part).
+template <int PM, int W, int PARTS>
+__device__ __forceinline__ void store_parts(uint32_t taddr, int stride, const float (&v)[W]) {
+  uint32_t p[3][W / 2];
+#pragma unroll
+  for (int i = 0; i < W / 2; ++i) {
+    if (PARTS == 3) split3(v[2 * i], v[2 * i + 1], p[0][i], p[1][i], p[2][i]);
+    else split2(v[2 * i], v[2 * i + 1], p[0][i], p[1][i]);
+  }
+#pragma unroll
+  for (int q = 0; q < PARTS; ++q) TmemIo<PM, W / 2>::st(taddr + q * stride, p[q]);
+}
+
+template <int PM, int W>
+__device__ __forceinline__ void load_cols(uint32_t taddr, float (&v)[W]) {
+  uint32_t r[W];
+  TmemIo<PM, W>::ld(taddr, r);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <int W>
+__device__ __forceinline__ void load_scalars(float (&v)[W], const float *p) {
+#pragma unroll
+  for (int c = 0; c < W; c += 4) {
+    const float4 x = *reinterpret_cast<const float4 *>(p + c);
+    v[c] = x.x; v[c + 1] = x.y; v[c + 2] = x.z; v[c + 3] = x.w;
+  }
+}
+
+template <int NP, int PM, bool SAVE>
+__global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, bool wide, bool wide_v) {
+  using Lay = Layout<NP, PM, SAVE>;
+  constexpr int W = Lay::W, WN = Lay::WN;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::kBarOff);
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + kBars);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.H + h, hk = h / (a.H / a.Hk);
+  const int p0 = blockIdx.x * PM;
+  const int64_t len = live_steps(a.lengths, b, a.L);
+  const int chunks = __shfl_sync(0xffffffffu, (int)((len + kChunk - 1) / kChunk), 0);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kBars; ++i) {
+      const bool state = i == kFree0 || i == kFree1 || i == kH || i == kR || i == kU1 || i == kU2 || i == kOut;
+      mbar_init(&bars[i], state ? kStateWarps : (i == kFull0 || i == kFull1) ? 32 * kLoaders + 1 : 1);
+    }
+    mbar_fence_init();
+  }
+  if (warp == kIssuer) {
+    tmem_alloc(tslot, Lay::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = __shfl_sync(0xffffffffu, *tslot, 0);
+
+  if (warp == kWriter) {
+    if (!SAVE) {
+      // y of a chunk: from [step][p] in shared memory, 16 bytes a lane
+      __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + (b * a.L * a.H + h) * a.P + p0;
+      const int64_t step = a.H * a.P;
+      const uint8_t *tile = smem + Lay::kYOff;
+      const int P = (int)min((int64_t)PM, a.P - p0);
+      for (int i = 0; i < chunks; ++i) {
+        wait_bar(&bars[kOut], i & 1, a.err, a.wait_ns);
+        const int live = (int)min((int64_t)kChunk, len - (int64_t)i * kChunk);
+        __nv_bfloat16 *dst = y + (int64_t)i * kChunk * step;
+        constexpr int G = PM / 8, kRows = 32 / G;
+        const int g = lane % G;
+#pragma unroll 4
+        for (int c = lane / G; c < kChunk; c += kRows) {
+          if (c >= live) continue;
+          if (wide_v) {
+            if (8 * g < P) *reinterpret_cast<uint4 *>(dst + c * step + 8 * g) = *reinterpret_cast<const uint4 *>(tile + (c * PM + 8 * g) * 2);
+          } else {
+            for (int k = 8 * g; k < min(P, 8 * g + 8); ++k) dst[c * step + k] = reinterpret_cast<const __nv_bfloat16 *>(tile)[c * PM + k];
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kOutFree]);
+      }
+      for (int64_t t = len; t < a.L; ++t)
+        for (int k = lane; k < P; k += 32) y[t * step + k] = __float2bfloat16_rn(0.f);
+    }
+  } else if (warp >= kLoader0) {
+    const int tid = threadIdx.x - 32 * kLoader0;
+    constexpr int NG = NP / 8;
+    const __nv_bfloat16 *kq[2] = {static_cast<const __nv_bfloat16 *>(a.k), static_cast<const __nv_bfloat16 *>(a.q)};
+    const int N = (int)a.N, P = (int)min((int64_t)PM, a.P - p0);
+    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + (b * a.L * a.H + h) * a.P + p0;
+    for (int i = 0; i < chunks; ++i) {
+      const int s = i & 1;
+      if (i >= 2) wait_bar(&bars[kFree0 + s], ((i >> 1) - 1) & 1, a.err, a.wait_ns);
+      uint8_t *st = smem + s * Lay::kStage;
+      if (tid == 0) {
+        const uint8_t *rec = a.records + (bh * a.nC + i) * a.rec_bytes;
+        uint64_t *full = &bars[kFull0 + s];
+        mbar_expect_tx(full, Lay::kRec);
+        if (SAVE) {  // the record has Tb between Te and A
+          bulk_load(st + Lay::kRecOff, rec, 3 * kSquare, full);
+          bulk_load(st + Lay::kRecOff + 3 * kSquare, rec + 6 * kSquare, 3 * kSquare + kScalars, full);
+        } else {
+          bulk_load(st + Lay::kRecOff, rec, Lay::kRec, full);
+        }
+      }
+      const int live = (int)min((int64_t)kChunk, len - (int64_t)i * kChunk);
+      const int64_t row0 = b * a.L + (int64_t)i * kChunk;
+      for (int k = tid; k < 2 * kChunk * NG; k += 32 * kLoaders) {
+        const int which = k / (kChunk * NG), c = (k / NG) & (kChunk - 1), g = k % NG;
+        const __nv_bfloat16 *src = kq[which] + ((row0 + c) * a.Hk + hk) * a.N + 8 * g;
+        uint8_t *dst = st + which * Lay::kQ + g * kGroup + c * 16;
+        if (wide && c < live && 8 * g < N) cp_async16(dst, src);
+        else *reinterpret_cast<uint4 *>(dst) = c < live ? gather8(src, N - 8 * g) : make_uint4(0, 0, 0, 0);
+      }
+      for (int k = tid; k < kChunk * (PM / 8); k += 32 * kLoaders) {
+        const int c = k / (PM / 8), g = k % (PM / 8);
+        const __nv_bfloat16 *src = v + ((int64_t)i * kChunk + c) * a.H * a.P + 8 * g;
+        uint8_t *dst = st + Lay::kVOff + (c * PM + 8 * g) * 2;
+        if (wide_v && c < live && 8 * g < P) cp_async16(dst, src);
+        else *reinterpret_cast<uint4 *>(dst) = c < live ? gather8(src, P - 8 * g) : make_uint4(0, 0, 0, 0);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      mbar_arrive(&bars[kFull0 + s]);
+    }
+  } else if (warp == kIssuer) {
+    // The whole warp goes through the loop and one lane issues: descriptors and addresses
+    // are then uniform (computed by one lane alone they cost about 70 cycles a product,
+    // twice the product itself).
+    constexpr uint32_t idS = idesc_bf16_f32(PM, kChunk, false, false), idD = idesc_bf16_f32(PM, NP, false, true);
+    const uint32_t base = smem_u32(smem);
+    for (int i = 0; i < chunks; ++i) {
+      const int s = i & 1;
+      const uint32_t ph = i & 1, sk = base + s * Lay::kStage, sq = sk + Lay::kQ, te = sk + Lay::kRecOff, sa = te + 3 * kSquare;
+      const uint64_t dk = smem_desc(sk, kGroup, 128), dq = smem_desc(sq, kGroup, 128), dkt = smem_desc(sk, 128, kGroup),
+                     dte = smem_desc(te, 1024, 128), da = smem_desc(sa, 1024, 128);
+      wait_bar(&bars[kFull0 + s], (i >> 1) & 1, a.err, a.wait_ns);
+      wait_bar(&bars[kH], ph, a.err, a.wait_ns);
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+#pragma unroll
+          for (int ks = 0; ks < NP / 16; ++ks)
+            mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kX + q * (NP / 2) + 8 * ks, dk + (2 * kGroup * ks >> 4), idS, q + ks > 0);
+        mma_commit(&bars[kDoneS]);
+      }
+      __syncwarp();
+      // Q H into Yh, once the chunk before has been read out of it
+      if (i >= 1) wait_bar(&bars[kFree0 + (s ^ 1)], ((i - 1) >> 1) & 1, a.err, a.wait_ns);
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int q = 0; q < (SAVE ? 3 : 2); ++q)
+#pragma unroll
+          for (int ks = 0; ks < NP / 16; ++ks)
+            mma_bf16_ts(tbase + Lay::kYh, tbase + Lay::kX + q * (NP / 2) + 8 * ks, dq + (2 * kGroup * ks >> 4), idS, q + ks > 0);
+      }
+      __syncwarp();
+      wait_bar(&bars[kR], ph, a.err, a.wait_ns);
+      tc_fence_after();
+      if (elect_one()) {
+        // R Te^T: parts (0,0) (1,0) (0,1) (2,0) (1,1) (0,2)
+#pragma unroll
+        for (int o = 0; o < 3; ++o)
+#pragma unroll
+          for (int q = 0; q <= o; ++q)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kD + (o - q) * 32 + 8 * ks, dte + ((q * kSquare + 2048 * ks) >> 4), idS,
+                          o + q + ks > 0);
+        mma_commit(&bars[kDoneU]);
+      }
+      __syncwarp();
+      wait_bar(&bars[kU1], ph, a.err, a.wait_ns);
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_bf16_ts(tbase + Lay::kD, tbase + Lay::kUd + q * 32 + 8 * ks, dkt + (256 * ks >> 4), idD, q + ks > 0);
+        mma_commit(&bars[kDoneD]);
+      }
+      __syncwarp();
+      wait_bar(&bars[kU2], ph, a.err, a.wait_ns);
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int o = 0; o < 3; ++o)
+#pragma unroll
+          for (int q = 0; q <= o; ++q) {
+            if (!SAVE && o > 1) continue;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16_ts(tbase + Lay::kYa, tbase + Lay::kUy + (o - q) * 32 + 8 * ks, da + ((q * kSquare + 2048 * ks) >> 4), idS,
+                          o + q + ks > 0);
+          }
+        mma_commit(&bars[kDoneY]);
+      }
+      __syncwarp();
+    }
+    if (chunks > 0) {
+      if (elect_one()) mma_commit(&bars[kEnd]);
+      __syncwarp();
+      wait_bar(&bars[kEnd], 0, a.err, 2000000000ull);
+    }
+  } else {
+    // the state's warps
+    const int quarter = warp & 3, up = warp >> 2;
+    const int row = PM == 128 ? 32 * quarter + lane : 16 * quarter + (lane & 15);
+    const int part = PM == 128 ? up : 2 * up + (lane >> 4);
+    const int wpart = PM == 128 ? up : 2 * up;  // where the warp's accesses of a row begin, in parts
+    const uint32_t tq = tbase + ((uint32_t)(32 * quarter) << 16);
+    const uint32_t tZ = tq + Lay::kZ + wpart * W, tYh = tq + Lay::kYh + wpart * W, tYa = tq + Lay::kYa + wpart * W;
+    const uint32_t tR = tq + Lay::kD + wpart * (W / 2), tUd = tq + Lay::kUd + wpart * (W / 2), tUy = tq + Lay::kUy + wpart * (W / 2);
+    const uint32_t tX = tq + Lay::kX + wpart * (WN / 2), tD = tq + Lay::kD + wpart * WN;
+    const int p = p0 + row, c0 = part * W, n0 = part * WN;
+    const bool pin = p < a.P;
+    const int N = (int)a.N;
+    float st[WN];
+#pragma unroll
+    for (int n = 0; n < WN; ++n) st[n] = (a.h0 && pin && n0 + n < N) ? a.h0[(bh * a.N + n0 + n) * a.P + p] : 0.f;
+    const auto ready = [&](Bar which) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[which]);
+    };
+    if (chunks > 0) {
+      store_parts<PM, WN, 3>(tX, NP / 2, st);
+      ready(kH);
+    }
+    for (int i = 0; i < chunks; ++i) {
+      const int s = i & 1;
+      const uint32_t ph = i & 1;
+      const uint8_t *stage = smem + s * Lay::kStage;
+      const float *scal = reinterpret_cast<const float *>(stage + Lay::kRecOff + Lay::kRec - kScalars);
+      const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(stage + Lay::kVOff) + c0 * PM + row;
+      if (SAVE && pin) {
+#pragma unroll
+        for (int n = 0; n < WN; ++n)
+          if (n0 + n < N) a.carry[((bh * a.nC + i) * a.N + n0 + n) * a.Pp + p] = st[n];
+      }
+      wait_bar(&bars[kFull0 + s], (i >> 1) & 1, a.err, a.wait_ns);
+      wait_bar(&bars[kDoneS], ph, a.err, a.wait_ns);
+      tc_fence_after();
+      float x[W], w[W];
+      load_cols<PM, W>(tZ, x);
+      load_scalars<W>(w, scal + c0);
+#pragma unroll
+      for (int c = 0; c < W; ++c) x[c] = fmaf(-w[c], x[c], __bfloat162float(v[c * PM]));
+      store_parts<PM, W, 3>(tR, 32, x);
+      ready(kR);
+      wait_bar(&bars[kDoneU], ph, a.err, a.wait_ns);
+      tc_fence_after();
+      load_cols<PM, W>(tZ, x);
+      if (SAVE && pin) {
+#pragma unroll
+        for (int c = 0; c < W; ++c)
+          if (i * (int64_t)kChunk + c0 + c < len) a.e[((b * a.L + i * (int64_t)kChunk + c0 + c) * a.H + h) * a.Pp + p] = x[c];
+      }
+      load_scalars<W>(w, scal + 2 * kChunk + c0);
+#pragma unroll
+      for (int c = 0; c < W; ++c) x[c] *= w[c];
+      load_scalars<W>(w, scal + kChunk + c0);
+#pragma unroll
+      for (int c = 0; c < W; ++c) w[c] *= x[c];
+      store_parts<PM, W, 3>(tUd, 32, w);
+      ready(kU1);
+      store_parts<PM, W, SAVE ? 3 : 2>(tUy, 32, x);
+      ready(kU2);
+      wait_bar(&bars[kDoneD], ph, a.err, a.wait_ns);
+      tc_fence_after();
+      const float last = scal[3 * kChunk];
+      {
+        float d[WN];
+        if constexpr (WN == 64) {
+          load_cols<PM, 32>(tD, *reinterpret_cast<float(*)[32]>(d));
+          load_cols<PM, 32>(tD + 32, *reinterpret_cast<float(*)[32]>(d + 32));
+        } else {
+          load_cols<PM, WN>(tD, d);
+        }
+#pragma unroll
+        for (int n = 0; n < WN; ++n) st[n] = fmaf(last, st[n], d[n]);
+      }
+      // u's parts may lie where the state's go: the product with A has to be done too
+      wait_bar(&bars[kDoneY], ph, a.err, a.wait_ns);
+      tc_fence_after();
+      if (i + 1 < chunks) {
+        store_parts<PM, WN, 3>(tX, NP / 2, st);
+        ready(kH);
+      }
+      if (!SAVE) {
+        load_cols<PM, W>(tYa, w);
+        load_cols<PM, W>(tYh, x);
+        if (i >= 1) wait_bar(&bars[kOutFree], (i - 1) & 1, a.err, a.wait_ns);
+        __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(smem + Lay::kYOff) + c0 * PM + row;
+#pragma unroll
+        for (int c = 0; c < W; c += 4) {
+          const float4 g = *reinterpret_cast<const float4 *>(scal + c0 + c);
+          out[c * PM] = __float2bfloat16_rn(fmaf(a.scale * g.x, x[c], w[c]));
+          out[(c + 1) * PM] = __float2bfloat16_rn(fmaf(a.scale * g.y, x[c + 1], w[c + 1]));
+          out[(c + 2) * PM] = __float2bfloat16_rn(fmaf(a.scale * g.z, x[c + 2], w[c + 2]));
+          out[(c + 3) * PM] = __float2bfloat16_rn(fmaf(a.scale * g.w, x[c + 3], w[c + 3]));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bars[kFree0 + s]);
+        if (!SAVE) mbar_arrive(&bars[kOut]);
+      }
+    }
+    if (!SAVE && pin && a.h_final) {
+#pragma unroll
+      for (int n = 0; n < WN; ++n)
+        if (n0 + n < N) a.h_final[(bh * a.N + n0 + n) * a.P + p] = st[n];
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssuer) tmem_dealloc(tbase, Lay::kCols);
+}
+
+template <int NP, int PM, bool SAVE>
+cudaError_t launch_k(const DeltaArgs &a, cudaStream_t st) {
+  using Lay = Layout<NP, PM, SAVE>;
+  auto kern = delta_chunk_kernel<NP, PM, SAVE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
+  if (e != cudaSuccess) return e;
+  const bool wide = a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && reinterpret_cast<uintptr_t>(a.k) % 16 == 0;
+  const dim3 grid((unsigned)((a.P + PM - 1) / PM), (unsigned)a.H, (unsigned)a.Bt);
+  const bool wide_v = a.P % 8 == 0 && reinterpret_cast<uintptr_t>(a.v) % 16 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
+  kern<<<grid, kThreads, Lay::kBytes, st>>>(a, wide, wide_v);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_delta_chunk(const DeltaArgs &a, cudaStream_t st) {
+  cudaError_t e = trace_before(st, "delta_chunk");
+  if (e != cudaSuccess) return e;
+  if (a.N <= 64) e = a.P <= 64 ? launch_k<64, 64, false>(a, st) : launch_k<64, 128, false>(a, st);
+  else e = a.P <= 64 ? launch_k<128, 64, false>(a, st) : launch_k<128, 128, false>(a, st);
+  return e != cudaSuccess ? e : trace_after(st);
+}
+
+}  // namespace pdssm

@@ -131,12 +131,22 @@ struct DeltaArgs {
   // workspace: states before each chunk and adjoints behind it [Bt][H][nC][N][Pp],
   // e_t and du_t [Bt][L][H][Pp]
   float *carry, *xcarry, *e, *du;
+  // chunked kernels: error word, a record for each chunk of each value head
+  // (csrc/delta_chunk.cuh), limit of a role's wait
+  uint32_t *err;
+  uint8_t *records;
+  int64_t rec_bytes;
+  uint64_t wait_ns;
 };
 // Step by step, any size; the outputs y and h_final.
 cudaError_t launch_delta_steps(const DeltaArgs &a, cudaStream_t st);
 // The same steps, writing carry and e instead; and the adjoint's steps (dv, dh0, xcarry, du).
 cudaError_t launch_delta_steps_save(const DeltaArgs &a, cudaStream_t st);
 cudaError_t launch_delta_steps_bwd(const DeltaArgs &a, cudaStream_t st);
+// By chunks of 64 on the tensor cores (bf16 inputs): the chunks' records, then the state
+// and the outputs.
+cudaError_t launch_delta_prep(const DeltaArgs &a, bool bwd, cudaStream_t st);
+cudaError_t launch_delta_chunk(const DeltaArgs &a, cudaStream_t st);
 // dq, dk, dg and dbeta of every chunk from its carries, e and du.
 int64_t delta_grad_chunk();
 cudaError_t launch_delta_grad(const DeltaArgs &a, cudaStream_t st);
