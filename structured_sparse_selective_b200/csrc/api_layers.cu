@@ -77,9 +77,8 @@ pdssm_status run_norm(const pdssm_norm_problem *pb, QkNormArgs &a, int64_t rows,
 
 struct DeltaPlan {
   int64_t rows, slices, Pp, C, nC;
-  bool chunked;  // forward on the tensor cores
-  int64_t nF;    // its chunks a sequence
-  size_t o_carry, o_xcarry, o_e, o_du, fwd_bytes, bwd_bytes;
+  bool chunked;  // by chunks on the tensor cores
+  size_t o_carry, o_xcarry, o_e, o_du, o_y32, o_rec, fwd_bytes, bwd_bytes;
 };
 
 constexpr size_t kErrBytes = 256;
@@ -100,26 +99,32 @@ pdssm_status plan_delta(const pdssm_delta_problem *pb, DeltaPlan *pl) {
     return PDSSM_ERR_UNSUPPORTED;
   DeltaPlan p;
   p.Pp = (pb->P + 3) / 4 * 4;
-  p.C = delta_grad_chunk();
-  p.nC = (pb->seqlen + p.C - 1) / p.C;
   int64_t bytes;
   p.slices = pb->batch * pb->heads;
-  // the largest array: carries of N x Pp floats a chunk, or rows of Pp floats a step
-  if (!mul_ok(pb->batch, pb->seqlen, &p.rows) || !mul_ok(p.slices, (p.nC + 1) * 65536, &bytes) ||
-      !mul_ok(p.rows * 8, pb->heads * PDSSM_MAX_N, &bytes))
+  // the largest arrays: states of up to 64 KiB a chunk of 32 steps (with the record of 64 steps no
+  // more than 8 KiB a step), rows of Pp floats a step
+  if (!mul_ok(pb->batch, pb->seqlen, &p.rows) || !mul_ok(p.slices, (pb->seqlen + kChunk) * 8192, &bytes))
     return PDSSM_ERR_UNSUPPORTED;
-  size_t o = 0;
-  const size_t carries = (size_t)(p.slices * p.nC * pb->N * p.Pp) * 4, steps = (size_t)(p.rows * pb->heads * p.Pp) * 4;
-  p.o_carry = o; o = align256(o + carries);
-  p.o_xcarry = o; o = align256(o + carries);
+  p.chunked = chunks_apply(pb);
+  p.C = p.chunked ? kChunk : delta_grad_chunk();
+  p.nC = (pb->seqlen + p.C - 1) / p.C;
+  // backward: error word, states (chunked: one more a sequence), adjoints, e, du; chunked: y and the records
+  const size_t state = (size_t)(pb->N * p.Pp) * 4, steps = (size_t)(p.rows * pb->heads * p.Pp) * 4;
+  size_t o = p.chunked ? kErrBytes : 0;
+  p.o_carry = o; o = align256(o + (size_t)(p.slices * (p.nC + (p.chunked ? 1 : 0))) * state);
+  p.o_xcarry = o; o = align256(o + (size_t)(p.slices * p.nC) * state);
   p.o_e = o; o = align256(o + steps);
   p.o_du = o; o = align256(o + steps);
+  p.o_y32 = o; o = align256(o + (p.chunked ? steps : 0));
+  p.o_rec = o; o = align256(o + (p.chunked ? (size_t)(p.slices * p.nC * delta_record_bytes(true)) : 0));
   p.bwd_bytes = o;
-  p.chunked = chunks_apply(pb);
-  p.nF = (pb->seqlen + kChunk - 1) / kChunk;
-  p.fwd_bytes = p.chunked ? kErrBytes + (size_t)(p.slices * p.nF * delta_record_bytes(false)) : 0;
+  p.fwd_bytes = p.chunked ? kErrBytes + (size_t)(p.slices * p.nC * delta_record_bytes(false)) : 0;
   *pl = p;
   return PDSSM_OK;
+}
+
+uint64_t wait_limit(const pdssm_delta_problem *pb) {
+  return (pb->flags & PDSSM_FLAG_SHORT_WAITS) ? 1000ull : 2000000000ull;
 }
 
 DeltaArgs delta_args(const pdssm_delta_problem *pb, const DeltaPlan &p) {
@@ -229,11 +234,10 @@ pdssm_status pdssm_delta_fwd(const pdssm_delta_problem *pb, const void *q, const
   a.err = static_cast<uint32_t *>(workspace);
   a.records = static_cast<uint8_t *>(workspace) + kErrBytes;
   a.rec_bytes = delta_record_bytes(false);
-  a.C = kChunk; a.nC = p.nF;
-  a.wait_ns = (pb->flags & PDSSM_FLAG_SHORT_WAITS) ? 1000ull : 2000000000ull;
+  a.wait_ns = wait_limit(pb);
   if (cudaMemsetAsync(a.err, 0, 4, cs) != cudaSuccess) return PDSSM_ERR_CUDA;
   if ((st = cuda_status(launch_delta_prep(a, false, cs))) != PDSSM_OK) return st;
-  return cuda_status(launch_delta_chunk(a, cs));
+  return cuda_status(launch_delta_chunk(a, false, cs));
 }
 
 pdssm_status pdssm_delta_bwd_workspace_size(const pdssm_delta_problem *pb, size_t *bytes) {
@@ -274,6 +278,18 @@ pdssm_status pdssm_delta_bwd(const pdssm_delta_problem *pb, const void *q, const
   a.xcarry = reinterpret_cast<float *>(base + p.o_xcarry);
   a.e = reinterpret_cast<float *>(base + p.o_e);
   a.du = reinterpret_cast<float *>(base + p.o_du);
+  if (p.chunked) {
+    a.err = static_cast<uint32_t *>(workspace);
+    a.y32 = reinterpret_cast<float *>(base + p.o_y32);
+    a.records = reinterpret_cast<uint8_t *>(base + p.o_rec);
+    a.rec_bytes = delta_record_bytes(true);
+    a.wait_ns = wait_limit(pb);
+    if (cudaMemsetAsync(a.err, 0, 4, cs) != cudaSuccess) return PDSSM_ERR_CUDA;
+    if ((st = cuda_status(launch_delta_prep(a, true, cs))) != PDSSM_OK) return st;
+    if ((st = cuda_status(launch_delta_chunk(a, true, cs))) != PDSSM_OK) return st;
+    if ((st = cuda_status(launch_delta_chunk_bwd(a, cs))) != PDSSM_OK) return st;
+    return cuda_status(launch_delta_chunk_grad(a, cs));
+  }
   if (p.rows > 0 && (st = cuda_status(launch_delta_steps_save(a, cs))) != PDSSM_OK) return st;
   if ((st = cuda_status(launch_delta_steps_bwd(a, cs))) != PDSSM_OK) return st;
   if (p.rows > 0) st = cuda_status(launch_delta_grad(a, cs));

@@ -40,7 +40,6 @@ namespace {
 
 constexpr int kStateWarps = 8, kIssuer = 8, kLoader0 = 9, kLoaders = 2, kWriter = 11;
 constexpr int kThreads = 32 * (kWriter + 1);
-constexpr int kGroup = kChunk * 16 + 16;  // bytes of eight columns of K or Q; 16 more spread the banks
 
 enum Bar { kFull0, kFull1, kFree0, kFree1, kH, kR, kU1, kU2, kDoneS, kDoneU, kDoneD, kDoneY, kOut, kOutFree, kEnd, kBars };
 
@@ -58,44 +57,12 @@ struct Layout {
   static_assert(kZ + 64 <= kCols && (NP == 128 || kUy + kUyn <= kCols) && (NP < 128 || 96 + kUyn <= kXn), "columns");
   // shared memory of a stage
   static constexpr int kRec = (3 + delta_a_parts(SAVE)) * kSquare + kScalars;
-  static constexpr int kQ = (NP / 8) * kGroup, kV = kChunk * PM * 2;  // V and Y: [step][p]
+  static constexpr int kQ = (NP / 8) * kChunkGroup, kV = kChunk * PM * 2;  // V and Y: [step][p]
   static constexpr int kVOff = 2 * kQ, kRecOff = kVOff + kV, kStage = kRecOff + kRec;
   static constexpr int kYOff = 2 * kStage, kBarOff = kYOff + (SAVE ? 0 : kV), kBytes = kBarOff + 8 * kBars + 16;
   // a thread's share of a row: W of 64 steps, WN of NP state values
   static constexpr int kParts = 256 / PM, W = kChunk / kParts, WN = NP / kParts;
 };
-
-// `n` fp32 values as packed bf16 parts 0 .. PARTS - 1 into columns col, col + stride, ...
-// of the thread's row (col already at the thread's or the warp's part).
-template <int PM, int W, int PARTS>
-__device__ __forceinline__ void store_parts(uint32_t taddr, int stride, const float (&v)[W]) {
-  uint32_t p[3][W / 2];
-#pragma unroll
-  for (int i = 0; i < W / 2; ++i) {
-    if (PARTS == 3) split3(v[2 * i], v[2 * i + 1], p[0][i], p[1][i], p[2][i]);
-    else split2(v[2 * i], v[2 * i + 1], p[0][i], p[1][i]);
-  }
-#pragma unroll
-  for (int q = 0; q < PARTS; ++q) TmemIo<PM, W / 2>::st(taddr + q * stride, p[q]);
-}
-
-template <int PM, int W>
-__device__ __forceinline__ void load_cols(uint32_t taddr, float (&v)[W]) {
-  uint32_t r[W];
-  TmemIo<PM, W>::ld(taddr, r);
-  tmem_wait_ld();
-#pragma unroll
-  for (int i = 0; i < W; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-template <int W>
-__device__ __forceinline__ void load_scalars(float (&v)[W], const float *p) {
-#pragma unroll
-  for (int c = 0; c < W; c += 4) {
-    const float4 x = *reinterpret_cast<const float4 *>(p + c);
-    v[c] = x.x; v[c + 1] = x.y; v[c + 2] = x.z; v[c + 3] = x.w;
-  }
-}
 
 template <int NP, int PM, bool SAVE>
 __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, bool wide, bool wide_v) {
@@ -156,10 +123,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
     }
   } else if (warp >= kLoader0) {
     const int tid = threadIdx.x - 32 * kLoader0;
-    constexpr int NG = NP / 8;
-    const __nv_bfloat16 *kq[2] = {static_cast<const __nv_bfloat16 *>(a.k), static_cast<const __nv_bfloat16 *>(a.q)};
-    const int N = (int)a.N, P = (int)min((int64_t)PM, a.P - p0);
-    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + (b * a.L * a.H + h) * a.P + p0;
     for (int i = 0; i < chunks; ++i) {
       const int s = i & 1;
       if (i >= 2) wait_bar(&bars[kFree0 + s], ((i >> 1) - 1) & 1, a.err, a.wait_ns);
@@ -177,20 +140,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       }
       const int live = (int)min((int64_t)kChunk, len - (int64_t)i * kChunk);
       const int64_t row0 = b * a.L + (int64_t)i * kChunk;
-      for (int k = tid; k < 2 * kChunk * NG; k += 32 * kLoaders) {
-        const int which = k / (kChunk * NG), c = (k / NG) & (kChunk - 1), g = k % NG;
-        const __nv_bfloat16 *src = kq[which] + ((row0 + c) * a.Hk + hk) * a.N + 8 * g;
-        uint8_t *dst = st + which * Lay::kQ + g * kGroup + c * 16;
-        if (wide && c < live && 8 * g < N) cp_async16(dst, src);
-        else *reinterpret_cast<uint4 *>(dst) = c < live ? gather8(src, N - 8 * g) : make_uint4(0, 0, 0, 0);
-      }
-      for (int k = tid; k < kChunk * (PM / 8); k += 32 * kLoaders) {
-        const int c = k / (PM / 8), g = k % (PM / 8);
-        const __nv_bfloat16 *src = v + ((int64_t)i * kChunk + c) * a.H * a.P + 8 * g;
-        uint8_t *dst = st + Lay::kVOff + (c * PM + 8 * g) * 2;
-        if (wide_v && c < live && 8 * g < P) cp_async16(dst, src);
-        else *reinterpret_cast<uint4 *>(dst) = c < live ? gather8(src, P - 8 * g) : make_uint4(0, 0, 0, 0);
-      }
+      using B = const __nv_bfloat16;
+      load_tile<NP / 8, kChunkGroup, 16>(st, static_cast<B *>(a.k), row0, a.Hk, hk, a.N, 0, live, wide, tid, 32 * kLoaders);
+      load_tile<NP / 8, kChunkGroup, 16>(st + Lay::kQ, static_cast<B *>(a.q), row0, a.Hk, hk, a.N, 0, live, wide, tid, 32 * kLoaders);
+      load_tile<PM / 8, 16, 2 * PM>(st + Lay::kVOff, static_cast<B *>(a.v), row0, a.H, h, a.P, p0, live, wide_v, tid, 32 * kLoaders);
       cp_async_commit();
       cp_async_wait<0>();
       fence_proxy_async_smem();
@@ -205,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
     for (int i = 0; i < chunks; ++i) {
       const int s = i & 1;
       const uint32_t ph = i & 1, sk = base + s * Lay::kStage, sq = sk + Lay::kQ, te = sk + Lay::kRecOff, sa = te + 3 * kSquare;
-      const uint64_t dk = smem_desc(sk, kGroup, 128), dq = smem_desc(sq, kGroup, 128), dkt = smem_desc(sk, 128, kGroup),
+      const uint64_t dk = smem_desc(sk, kChunkGroup, 128), dq = smem_desc(sq, kChunkGroup, 128), dkt = smem_desc(sk, 128, kChunkGroup),
                      dte = smem_desc(te, 1024, 128), da = smem_desc(sa, 1024, 128);
       wait_bar(&bars[kFull0 + s], (i >> 1) & 1, a.err, a.wait_ns);
       wait_bar(&bars[kH], ph, a.err, a.wait_ns);
@@ -215,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
         for (int q = 0; q < 3; ++q)
 #pragma unroll
           for (int ks = 0; ks < NP / 16; ++ks)
-            mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kX + q * (NP / 2) + 8 * ks, dk + (2 * kGroup * ks >> 4), idS, q + ks > 0);
+            mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kX + q * (NP / 2) + 8 * ks, dk + (2 * kChunkGroup * ks >> 4), idS, q + ks > 0);
         mma_commit(&bars[kDoneS]);
       }
       __syncwarp();
@@ -227,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
         for (int q = 0; q < (SAVE ? 3 : 2); ++q)
 #pragma unroll
           for (int ks = 0; ks < NP / 16; ++ks)
-            mma_bf16_ts(tbase + Lay::kYh, tbase + Lay::kX + q * (NP / 2) + 8 * ks, dq + (2 * kGroup * ks >> 4), idS, q + ks > 0);
+            mma_bf16_ts(tbase + Lay::kYh, tbase + Lay::kX + q * (NP / 2) + 8 * ks, dq + (2 * kChunkGroup * ks >> 4), idS, q + ks > 0);
       }
       __syncwarp();
       wait_bar(&bars[kR], ph, a.err, a.wait_ns);
@@ -300,6 +253,23 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[which]);
     };
+    // SAVE: the state before chunk i (and behind the last), and 64 x p values of the chunk's steps
+    const auto save_state = [&](int i) {
+      float *to = a.carry + ((bh * (a.nC + 1) + i) * a.N + n0) * a.Pp + p;
+      if (p >= a.Pp) return;
+#pragma unroll
+      for (int n = 0; n < WN; ++n, to += a.Pp)
+        if (n0 + n < N) *to = st[n];
+    };
+    const auto save_rows = [&](float *rows, int i, const float (&x)[W]) {
+      const int64_t t = (int64_t)i * kChunk + c0, step = a.H * a.Pp;
+      float *to = rows + ((b * a.L + t) * a.H + h) * a.Pp + p;
+      const int n = (int)min((int64_t)W, len - t);
+      if (p >= a.Pp) return;
+#pragma unroll
+      for (int c = 0; c < W; ++c, to += step)
+        if (c < n) *to = x[c];
+    };
     if (chunks > 0) {
       store_parts<PM, WN, 3>(tX, NP / 2, st);
       ready(kH);
@@ -310,11 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       const uint8_t *stage = smem + s * Lay::kStage;
       const float *scal = reinterpret_cast<const float *>(stage + Lay::kRecOff + Lay::kRec - kScalars);
       const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(stage + Lay::kVOff) + c0 * PM + row;
-      if (SAVE && pin) {
-#pragma unroll
-        for (int n = 0; n < WN; ++n)
-          if (n0 + n < N) a.carry[((bh * a.nC + i) * a.N + n0 + n) * a.Pp + p] = st[n];
-      }
+      if (SAVE) save_state(i);
       wait_bar(&bars[kFull0 + s], (i >> 1) & 1, a.err, a.wait_ns);
       wait_bar(&bars[kDoneS], ph, a.err, a.wait_ns);
       tc_fence_after();
@@ -328,11 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       wait_bar(&bars[kDoneU], ph, a.err, a.wait_ns);
       tc_fence_after();
       load_cols<PM, W>(tZ, x);
-      if (SAVE && pin) {
-#pragma unroll
-        for (int c = 0; c < W; ++c)
-          if (i * (int64_t)kChunk + c0 + c < len) a.e[((b * a.L + i * (int64_t)kChunk + c0 + c) * a.H + h) * a.Pp + p] = x[c];
-      }
+      if (SAVE) save_rows(a.e, i, x);
       load_scalars<W>(w, scal + 2 * kChunk + c0);
 #pragma unroll
       for (int c = 0; c < W; ++c) x[c] *= w[c];
@@ -378,6 +340,16 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
           out[(c + 3) * PM] = __float2bfloat16_rn(fmaf(a.scale * g.w, x[c + 3], w[c + 3]));
         }
       }
+      if (SAVE) {
+        load_cols<PM, W>(tYh, x);
+        load_scalars<W>(w, scal + c0);
+#pragma unroll
+        for (int c = 0; c < W; ++c) x[c] *= a.scale * w[c];
+        load_cols<PM, W>(tYa, w);
+#pragma unroll
+        for (int c = 0; c < W; ++c) x[c] += w[c];
+        save_rows(a.y32, i, x);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -385,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
         if (!SAVE) mbar_arrive(&bars[kOut]);
       }
     }
+    if (SAVE) save_state(chunks);
     if (!SAVE && pin && a.h_final) {
 #pragma unroll
       for (int n = 0; n < WN; ++n)
@@ -411,11 +384,16 @@ cudaError_t launch_k(const DeltaArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_delta_chunk(const DeltaArgs &a, cudaStream_t st) {
-  cudaError_t e = trace_before(st, "delta_chunk");
+template <bool SAVE>
+static cudaError_t launch_s(const DeltaArgs &a, cudaStream_t st) {
+  if (a.N <= 64) return a.P <= 64 ? launch_k<64, 64, SAVE>(a, st) : launch_k<64, 128, SAVE>(a, st);
+  return a.P <= 64 ? launch_k<128, 64, SAVE>(a, st) : launch_k<128, 128, SAVE>(a, st);
+}
+
+cudaError_t launch_delta_chunk(const DeltaArgs &a, bool save, cudaStream_t st) {
+  cudaError_t e = trace_before(st, save ? "delta_chunk_save" : "delta_chunk");
   if (e != cudaSuccess) return e;
-  if (a.N <= 64) e = a.P <= 64 ? launch_k<64, 64, false>(a, st) : launch_k<64, 128, false>(a, st);
-  else e = a.P <= 64 ? launch_k<128, 64, false>(a, st) : launch_k<128, 128, false>(a, st);
+  e = save ? launch_s<true>(a, st) : launch_s<false>(a, st);
   return e != cudaSuccess ? e : trace_after(st);
 }
 

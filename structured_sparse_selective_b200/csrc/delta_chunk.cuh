@@ -11,7 +11,9 @@ constexpr int kChunk = 64;
 // A 64 x 64 bf16 operand, element (row c, column j): (j / 8) * 1024 + c * 16 + (j % 8) * 2.
 // Read K-major it is [rows c][k = j], read MN-major [k = c][columns j].
 constexpr int kSquare = kChunk * kChunk * 2;
-constexpr int kScalars = 4 * kChunk * 4;  // exp(G), exp(G_64 - G), beta, exp(G_64), 64 floats each
+constexpr int kChunkGroup = kChunk * 16 + 16;  // bytes of eight columns of K or Q; 16 more spread the banks
+// exp(G), exp(G_64 - G), beta, exp(G_64), and G to the base 2 as two floats, 64 values each
+constexpr int kScalars = 6 * kChunk * 4;
 // Record of a chunk: Te (3 parts), backward also Tb (3 parts), A (2 parts, backward 3), scalars.
 constexpr int delta_a_parts(bool bwd) { return bwd ? 3 : 2; }
 constexpr int64_t delta_record_bytes(bool bwd) { return ((bwd ? 6 : 3) + delta_a_parts(bwd)) * (int64_t)kSquare + kScalars; }
@@ -49,6 +51,31 @@ __device__ __forceinline__ uint4 gather8(const __nv_bfloat16 *p, int n) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The rows [row0, row0 + 64) of head `head` of x [rows][heads][n] as an operand in shared
+// memory, element (step c, column j): (j / 8) * GROUP + c * ROW + (j % 8) * 2, by `threads`
+// threads. WIDE: 16-byte asynchronous copies (n a multiple of 8, x aligned to 16 bytes).
+// Zeros behind the `live` rows and the n columns.
+template <int NG, int GROUP, int ROW>
+__device__ __forceinline__ void load_tile(uint8_t *dst, const __nv_bfloat16 *x, int64_t row0, int64_t heads, int64_t head, int64_t n,
+                                          int64_t n0, int live, bool wide, int tid, int threads) {
+  const int have = (int)min((int64_t)8 * NG, n - n0);
+  const __nv_bfloat16 *src = x + (row0 * heads + head) * n + n0;
+  const int64_t row = heads * n;
+  for (int k = tid; k < kChunk * NG; k += threads) {
+    const int c = k / NG, g = k % NG;
+    uint8_t *to = dst + g * GROUP + c * ROW;
+    if (wide && c < live && 8 * g < have) sm100::cp_async16(to, src + c * row + 8 * g);
+    else *reinterpret_cast<uint4 *>(to) = c < live ? gather8(src + c * row + 8 * g, have - 8 * g) : make_uint4(0, 0, 0, 0);
+  }
+}
+
+// 2^x, off by at most about 2^-22 of it.
+__device__ __forceinline__ float decay2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 __device__ __forceinline__ uint64_t now_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
@@ -69,6 +96,38 @@ static __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, ui
 }
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, uint32_t *err, uint64_t limit_ns) {
   return sm100::mbar_try_wait(bar, parity) || wait_slow(bar, parity, err, limit_ns);
+}
+
+// `n` fp32 values as packed bf16 parts 0 .. PARTS - 1 into columns col, col + stride, ...
+// of the thread's row (col already at the thread's or the warp's part).
+template <int PM, int W, int PARTS>
+__device__ __forceinline__ void store_parts(uint32_t taddr, int stride, const float (&v)[W]) {
+  uint32_t p[3][W / 2];
+#pragma unroll
+  for (int i = 0; i < W / 2; ++i) {
+    if (PARTS == 3) split3(v[2 * i], v[2 * i + 1], p[0][i], p[1][i], p[2][i]);
+    else split2(v[2 * i], v[2 * i + 1], p[0][i], p[1][i]);
+  }
+#pragma unroll
+  for (int q = 0; q < PARTS; ++q) sm100::TmemIo<PM, W / 2>::st(taddr + q * stride, p[q]);
+}
+
+template <int PM, int W>
+__device__ __forceinline__ void load_cols(uint32_t taddr, float (&v)[W]) {
+  uint32_t r[W];
+  sm100::TmemIo<PM, W>::ld(taddr, r);
+  sm100::tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <int W>
+__device__ __forceinline__ void load_scalars(float (&v)[W], const float *p) {
+#pragma unroll
+  for (int c = 0; c < W; c += 4) {
+    const float4 x = *reinterpret_cast<const float4 *>(p + c);
+    v[c] = x.x; v[c + 1] = x.y; v[c + 2] = x.z; v[c + 3] = x.w;
+  }
 }
 
 }  // namespace pdssm

@@ -1,0 +1,316 @@
+// The gated delta rule by chunks of 64 steps, backwards: the adjoint of the state from
+// chunk to chunk, one block per (sequence, head) (bf16 inputs; records of
+// csrc/delta_prep.cu, formulas in delta.cuh).
+//
+// The mirror of csrc/delta_chunk.cu. For one chunk whose end has the adjoint X:
+//   dU^T = (X^T K^T) diag(exp(G_64 - G)) + dY^T A      du = dU through Tb: du^T = dU^T Tb
+//   dv = beta du
+//   X'^T = exp(G_64) X^T + scale (dY diag(exp G))^T Q - (dv diag(exp G))^T K
+// Rows are the value's columns p again; X, dU, dv and dY diag(exp G) are split into three
+// bf16 parts on the way to X, dY and the records' parts are exact as they are. The chain is
+// K X -> Tb -> K^T dv; dY^T A and Q^T dY run in its pauses.
+// Written: dv, du (fp32), X at each chunk's end, dh0.
+#include <algorithm>
+
+#include "delta.cuh"
+#include "delta_chunk.cuh"
+#include "sm100.cuh"
+
+namespace pdssm {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kStateWarps = 8, kIssuer = 8, kLoader0 = 9, kLoaders = 2;
+constexpr int kThreads = 32 * (kLoader0 + kLoaders);
+
+enum Bar { kFull0, kFull1, kFree0, kFree1, kX, kR, kU, kDoneS, kDoneU, kDoneD, kEnd, kBars };
+
+template <int NP, int PM>
+struct Layout {
+  // tensor memory: P holds X's parts, then those of dv; D the parts of dU, then the update;
+  // Q the parts of dY diag(exp G); Y dY itself; Z first X^T K^T, then du; A dY^T A.
+  static constexpr int kP = 0, kPn = 3 * NP / 2, kD = kPn, kDn = NP > 96 ? NP : 96;
+  static constexpr int kQ = NP == 128 ? kP + 96 : kD + kDn, kZ = (NP == 128 ? kD : kQ) + (NP == 128 ? kDn : 96);
+  static constexpr int kA = kZ + 64, kY = kA + 64, kCols = 512;
+  static_assert(kY + 32 <= kCols, "columns");
+  static constexpr int kTile = (NP / 8) * kChunkGroup, kDy = kChunk * PM * 2, kRec = 6 * kSquare + kScalars;
+  static constexpr int kDyOff = 2 * kTile, kRecOff = kDyOff + kDy, kStage = kRecOff + kRec;
+  static constexpr int kBarOff = 2 * kStage, kBytes = kBarOff + 8 * kBars + 16;
+  static constexpr int kParts = 256 / PM, W = kChunk / kParts, WN = NP / kParts;
+};
+
+template <int NP, int PM>
+__global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs a, bool wide, bool wide_v) {
+  using Lay = Layout<NP, PM>;
+  constexpr int W = Lay::W, WN = Lay::WN;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::kBarOff);
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + kBars);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.H + h, hk = h / (a.H / a.Hk);
+  const int p0 = blockIdx.x * PM;
+  const int64_t len = live_steps(a.lengths, b, a.L);
+  const int chunks = __shfl_sync(0xffffffffu, (int)((len + kChunk - 1) / kChunk), 0);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kBars; ++i) {
+      const bool state = i == kFree0 || i == kFree1 || i == kX || i == kR || i == kU;
+      mbar_init(&bars[i], state ? kStateWarps : (i == kFull0 || i == kFull1) ? 32 * kLoaders + 1 : 1);
+    }
+    mbar_fence_init();
+  }
+  if (warp == kIssuer) {
+    tmem_alloc(tslot, Lay::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = __shfl_sync(0xffffffffu, *tslot, 0);
+
+  // Turn i works on chunk chunks - 1 - i.
+  if (warp >= kLoader0) {
+    const int tid = threadIdx.x - 32 * kLoader0;
+    for (int i = 0; i < chunks; ++i) {
+      const int s = i & 1, chunk = chunks - 1 - i;
+      if (i >= 2) wait_bar(&bars[kFree0 + s], ((i >> 1) - 1) & 1, a.err, a.wait_ns);
+      uint8_t *st = smem + s * Lay::kStage;
+      if (tid == 0) {
+        uint64_t *full = &bars[kFull0 + s];
+        mbar_expect_tx(full, Lay::kRec);
+        bulk_load(st + Lay::kRecOff, a.records + (bh * a.nC + chunk) * a.rec_bytes + 3 * kSquare, Lay::kRec, full);
+      }
+      const int live = (int)min((int64_t)kChunk, len - (int64_t)chunk * kChunk);
+      const int64_t row0 = b * a.L + (int64_t)chunk * kChunk;
+      using B = const __nv_bfloat16;
+      load_tile<NP / 8, kChunkGroup, 16>(st, static_cast<B *>(a.k), row0, a.Hk, hk, a.N, 0, live, wide, tid, 32 * kLoaders);
+      load_tile<NP / 8, kChunkGroup, 16>(st + Lay::kTile, static_cast<B *>(a.q), row0, a.Hk, hk, a.N, 0, live, wide, tid, 32 * kLoaders);
+      load_tile<PM / 8, 16, 2 * PM>(st + Lay::kDyOff, static_cast<B *>(a.dy), row0, a.H, h, a.P, p0, live, wide_v, tid, 32 * kLoaders);
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      mbar_arrive(&bars[kFull0 + s]);
+    }
+  } else if (warp == kIssuer) {
+    constexpr uint32_t idS = idesc_bf16_f32(PM, kChunk, false, false), idT = idesc_bf16_f32(PM, kChunk, false, true),
+                       idD = idesc_bf16_f32(PM, NP, false, true);
+    const uint32_t base = smem_u32(smem);
+    for (int i = 0; i < chunks; ++i) {
+      const int s = i & 1;
+      const uint32_t ph = i & 1, sk = base + s * Lay::kStage, sq = sk + Lay::kTile, tb = sk + Lay::kRecOff, sa = tb + 3 * kSquare;
+      const uint64_t dk = smem_desc(sk, kChunkGroup, 128), dkt = smem_desc(sk, 128, kChunkGroup), dqt = smem_desc(sq, 128, kChunkGroup),
+                     dtb = smem_desc(tb, 128, 1024), da = smem_desc(sa, 128, 1024);
+      wait_bar(&bars[kFull0 + s], (i >> 1) & 1, a.err, a.wait_ns);
+      wait_bar(&bars[kX], ph, a.err, a.wait_ns);
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+#pragma unroll
+          for (int ks = 0; ks < NP / 16; ++ks)
+            mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kP + q * (NP / 2) + 8 * ks, dk + (2 * kChunkGroup * ks >> 4), idS, q + ks > 0);
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_bf16_ts(tbase + Lay::kA, tbase + Lay::kY + 8 * ks, da + ((q * kSquare + 256 * ks) >> 4), idT, q + ks > 0);
+        mma_commit(&bars[kDoneS]);
+      }
+      __syncwarp();
+      wait_bar(&bars[kR], ph, a.err, a.wait_ns);
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int o = 0; o < 3; ++o)
+#pragma unroll
+          for (int q = 0; q <= o; ++q)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kD + (o - q) * 32 + 8 * ks, dtb + ((q * kSquare + 256 * ks) >> 4), idT,
+                          o + q + ks > 0);
+        mma_commit(&bars[kDoneU]);
+      }
+      __syncwarp();
+      wait_bar(&bars[kU], ph, a.err, a.wait_ns);
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_bf16_ts(tbase + Lay::kD, tbase + Lay::kP + q * 32 + 8 * ks, dkt + (256 * ks >> 4), idD, q + ks > 0);
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_bf16_ts(tbase + Lay::kD, tbase + Lay::kQ + q * 32 + 8 * ks, dqt + (256 * ks >> 4), idD, 1);
+        mma_commit(&bars[kDoneD]);
+      }
+      __syncwarp();
+    }
+    if (chunks > 0) {
+      if (elect_one()) mma_commit(&bars[kEnd]);
+      __syncwarp();
+      wait_bar(&bars[kEnd], 0, a.err, 2000000000ull);
+    }
+  } else {
+    const int quarter = warp & 3, up = warp >> 2;
+    const int row = PM == 128 ? 32 * quarter + lane : 16 * quarter + (lane & 15);
+    const int part = PM == 128 ? up : 2 * up + (lane >> 4);
+    const int wpart = PM == 128 ? up : 2 * up;
+    const uint32_t tq = tbase + ((uint32_t)(32 * quarter) << 16);
+    const uint32_t tZ = tq + Lay::kZ + wpart * W, tA = tq + Lay::kA + wpart * W;
+    const uint32_t tR = tq + Lay::kD + wpart * (W / 2), tU = tq + Lay::kP + wpart * (W / 2), tQ = tq + Lay::kQ + wpart * (W / 2),
+                   tY = tq + Lay::kY + wpart * (W / 2);
+    const uint32_t tX = tq + Lay::kP + wpart * (WN / 2), tD = tq + Lay::kD + wpart * WN;
+    const int p = p0 + row, c0 = part * W, n0 = part * WN;
+    const bool pin = p < a.P;
+    const int N = (int)a.N;
+    __nv_bfloat16 *dv = static_cast<__nv_bfloat16 *>(a.dv) + (b * a.L * a.H + h) * a.P + p;
+    const int64_t step = a.H * a.P;
+    float st[WN];
+#pragma unroll
+    for (int n = 0; n < WN; ++n) st[n] = (a.dh_final && pin && n0 + n < N) ? a.dh_final[(bh * a.N + n0 + n) * a.P + p] : 0.f;
+    const auto ready = [&](Bar which) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[which]);
+    };
+    // dY of turn i as it is, an operand of dY^T A
+    const auto store_dy = [&](int i) {
+      const int s = i & 1;
+      wait_bar(&bars[kFull0 + s], (i >> 1) & 1, a.err, a.wait_ns);
+      const uint16_t *dy = reinterpret_cast<const uint16_t *>(smem + s * Lay::kStage + Lay::kDyOff) + c0 * PM + row;
+      uint32_t r[W / 2];
+#pragma unroll
+      for (int c = 0; c < W / 2; ++c) r[c] = dy[2 * c * PM] | ((uint32_t)dy[(2 * c + 1) * PM] << 16);
+      TmemIo<PM, W / 2>::st(tY, r);
+    };
+    if (chunks > 0) {
+      store_parts<PM, WN, 3>(tX, NP / 2, st);
+      store_dy(0);
+      ready(kX);
+    }
+    for (int i = 0; i < chunks; ++i) {
+      const int s = i & 1, chunk = chunks - 1 - i;
+      const uint32_t ph = i & 1;
+      const uint8_t *stage = smem + s * Lay::kStage;
+      const float *scal = reinterpret_cast<const float *>(stage + Lay::kRecOff + Lay::kRec - kScalars);
+      const __nv_bfloat16 *dy = reinterpret_cast<const __nv_bfloat16 *>(stage + Lay::kDyOff) + c0 * PM + row;
+      if (p < a.Pp) {
+        float *to = a.xcarry + ((bh * a.nC + chunk) * a.N + n0) * a.Pp + p;
+#pragma unroll
+        for (int n = 0; n < WN; ++n, to += a.Pp)
+          if (n0 + n < N) *to = st[n];
+      }
+      wait_bar(&bars[kDoneS], ph, a.err, a.wait_ns);
+      tc_fence_after();
+      float x[W], w[W];
+      load_cols<PM, W>(tZ, x);
+      load_scalars<W>(w, scal + kChunk + c0);
+#pragma unroll
+      for (int c = 0; c < W; ++c) x[c] *= w[c];
+      load_cols<PM, W>(tA, w);
+#pragma unroll
+      for (int c = 0; c < W; ++c) x[c] += w[c];
+      store_parts<PM, W, 3>(tR, 32, x);
+      ready(kR);
+      // meanwhile scale dY diag(exp G); X's parts, whose place it may take, have been read
+      load_scalars<W>(w, scal + c0);
+#pragma unroll
+      for (int c = 0; c < W; ++c) x[c] = a.scale * w[c] * __bfloat162float(dy[c * PM]);
+      store_parts<PM, W, 3>(tQ, 32, x);
+      wait_bar(&bars[kDoneU], ph, a.err, a.wait_ns);
+      tc_fence_after();
+      load_cols<PM, W>(tZ, x);
+      float g[W];
+      load_scalars<W>(w, scal + 2 * kChunk + c0);
+      load_scalars<W>(g, scal + c0);
+#pragma unroll
+      for (int c = 0; c < W; ++c) {
+        w[c] *= x[c];
+        g[c] *= -w[c];
+      }
+      store_parts<PM, W, 3>(tU, 32, g);
+      ready(kU);
+      {
+        const int64_t t = (int64_t)chunk * kChunk + c0;
+        const int n = (int)min((int64_t)W, len - t);
+        float *to = a.du + ((b * a.L + t) * a.H + h) * a.Pp + p;
+        __nv_bfloat16 *tv = dv + t * step;
+        const int64_t wide_step = a.H * a.Pp;
+        if (p < a.Pp) {
+#pragma unroll
+          for (int c = 0; c < W; ++c, to += wide_step)
+            if (c < n) *to = x[c];
+        }
+        if (pin) {
+#pragma unroll
+          for (int c = 0; c < W; ++c, tv += step)
+            if (c < n) *tv = __float2bfloat16_rn(w[c]);
+        }
+      }
+      const float last = scal[3 * kChunk];
+      wait_bar(&bars[kDoneD], ph, a.err, a.wait_ns);
+      tc_fence_after();
+      {
+        float d[WN];
+        if constexpr (WN == 64) {
+          load_cols<PM, 32>(tD, *reinterpret_cast<float(*)[32]>(d));
+          load_cols<PM, 32>(tD + 32, *reinterpret_cast<float(*)[32]>(d + 32));
+        } else {
+          load_cols<PM, WN>(tD, d);
+        }
+#pragma unroll
+        for (int n = 0; n < WN; ++n) st[n] = fmaf(last, st[n], d[n]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kFree0 + s]);
+      if (i + 1 < chunks) {
+        store_parts<PM, WN, 3>(tX, NP / 2, st);
+        store_dy(i + 1);
+        ready(kX);
+      }
+    }
+    if (pin) {
+      for (int64_t t = len + part; t < a.L; t += Lay::kParts) dv[t * step] = __float2bfloat16_rn(0.f);
+      if (a.dh0) {
+#pragma unroll
+        for (int n = 0; n < WN; ++n)
+          if (n0 + n < N) a.dh0[(bh * a.N + n0 + n) * a.P + p] = st[n];
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssuer) tmem_dealloc(tbase, Lay::kCols);
+}
+
+template <int NP, int PM>
+cudaError_t launch_k(const DeltaArgs &a, cudaStream_t st) {
+  using Lay = Layout<NP, PM>;
+  auto kern = delta_chunk_bwd_kernel<NP, PM>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
+  if (e != cudaSuccess) return e;
+  const bool wide = a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && reinterpret_cast<uintptr_t>(a.k) % 16 == 0;
+  const bool wide_v = a.P % 8 == 0 && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0;
+  const dim3 grid((unsigned)((a.P + PM - 1) / PM), (unsigned)a.H, (unsigned)a.Bt);
+  kern<<<grid, kThreads, Lay::kBytes, st>>>(a, wide, wide_v);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_delta_chunk_bwd(const DeltaArgs &a, cudaStream_t st) {
+  cudaError_t e = trace_before(st, "delta_chunk_bwd");
+  if (e != cudaSuccess) return e;
+  if (a.N <= 64) e = a.P <= 64 ? launch_k<64, 64>(a, st) : launch_k<64, 128>(a, st);
+  else e = a.P <= 64 ? launch_k<128, 64>(a, st) : launch_k<128, 128>(a, st);
+  return e != cudaSuccess ? e : trace_after(st);
+}
+
+}  // namespace pdssm

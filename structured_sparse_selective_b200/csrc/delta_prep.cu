@@ -9,7 +9,7 @@
 //   Te = (1 + N diag(beta))^-1 = 1 - X diag(beta),  Tb = (1 + diag(beta) N)^-1 = 1 - diag(beta) X,
 // one from the other without a division by a beta that may be 0. This kernel writes, per
 // value head and chunk, one record: Te, for the backward pass Tb, A_ij = scale D_ij <q_i, k_j>
-// (j <= i), and exp(G_i), exp(G_64 - G_i), beta_i.
+// (j <= i), and exp(G_i), exp(G_64 - G_i), beta_i, G_i.
 // The products of q and k rows are exact in bf16 and summed in fp32: one tensor-core
 // product [K; Q] K^T of 128 x 64 a chunk and key head (tcgen05.mma from shared memory,
 // M = 128, so that the whole accumulator is used). X is fp32 on the ordinary cores: two
@@ -55,18 +55,12 @@ __device__ __forceinline__ void load_rows(uint8_t *dst, const DeltaArgs &a, int6
   }
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // A step's running log decay in two floats (base 2) and its beta.
 struct Gate {
   float hi, lo, beta, pad;
 };
 
-__device__ __forceinline__ float decay(float hi, float lo, const Gate &j) { return exp2_fast((hi - j.hi) + (lo - j.lo)); }
+__device__ __forceinline__ float decay(float hi, float lo, const Gate &j) { return decay2((hi - j.hi) + (lo - j.lo)); }
 
 // Column j of the 32 x 32 triangle at (o, o): x = N_j - N diag(beta) x by forward substitution,
 // nt[j][i] = N_ij. Each known x_m is taken out of the rows below it (independent FMAs).
@@ -201,21 +195,23 @@ __global__ void __launch_bounds__(kThreads, NP == 64 ? 5 : 4) delta_prep_kernel(
         if (lane >= o) sum += up;
       }
       const double last = __shfl_sync(0xffffffffu, sum, 31), G[2] = {sum - g1, sum};
-      const float all = exp2_fast((float)last);
+      const float all = decay2((float)last);
       float grow[2], fade[2], bt[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const float hi = (float)G[s];
         bt[s] = 2 * lane + s < live ? be[s] : 0.f;
         gate[2 * lane + s] = {hi, (float)(G[s] - (double)hi), bt[s], 0.f};
-        grow[s] = exp2_fast(hi);
-        fade[s] = exp2_fast((float)(last - G[s]));
+        grow[s] = decay2(hi);
+        fade[s] = decay2((float)(last - G[s]));
       }
       float2 *out = reinterpret_cast<float2 *>(scal);
       out[lane] = make_float2(grow[0], grow[1]);
       out[32 + lane] = make_float2(fade[0], fade[1]);
       out[64 + lane] = make_float2(bt[0], bt[1]);
       out[96 + lane] = make_float2(all, all);
+      out[128 + lane] = make_float2((float)G[0], (float)G[1]);
+      out[160 + lane] = make_float2((float)(G[0] - (double)(float)G[0]), (float)(G[1] - (double)(float)G[1]));
       if (hh + 1 < r_heads) fetch_gates(h + 1);
     }
     if (hh == 0) wait_bar(bar, 0, a.err, 2000000000ull);

@@ -131,6 +131,7 @@ struct DeltaArgs {
   // workspace: states before each chunk and adjoints behind it [Bt][H][nC][N][Pp],
   // e_t and du_t [Bt][L][H][Pp]
   float *carry, *xcarry, *e, *du;
+  float *y32;  // chunked: y_t before its rounding, and carry has [nC + 1] states
   // chunked kernels: error word, a record for each chunk of each value head
   // (csrc/delta_chunk.cuh), limit of a role's wait
   uint32_t *err;
@@ -146,7 +147,10 @@ cudaError_t launch_delta_steps_bwd(const DeltaArgs &a, cudaStream_t st);
 // By chunks of 64 on the tensor cores (bf16 inputs): the chunks' records, then the state
 // and the outputs.
 cudaError_t launch_delta_prep(const DeltaArgs &a, bool bwd, cudaStream_t st);
-cudaError_t launch_delta_chunk(const DeltaArgs &a, cudaStream_t st);
+cudaError_t launch_delta_chunk(const DeltaArgs &a, bool save, cudaStream_t st);
+// The adjoint by chunks (dv, dh0, xcarry, du); and the other gradients from what both wrote.
+cudaError_t launch_delta_chunk_bwd(const DeltaArgs &a, cudaStream_t st);
+cudaError_t launch_delta_chunk_grad(const DeltaArgs &a, cudaStream_t st);
 // dq, dk, dg and dbeta of every chunk from its carries, e and du.
 int64_t delta_grad_chunk();
 cudaError_t launch_delta_grad(const DeltaArgs &a, cudaStream_t st);
