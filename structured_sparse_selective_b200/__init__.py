@@ -492,20 +492,26 @@ def backward(logits: Optional[torch.Tensor], s: torch.Tensor, idx: torch.Tensor,
 # ------------------------------------------- layers beside the scan: q / k preparation, gated delta rule
 
 _NORM_MODES = {"rms": 0, "l2": 1}
-
-
-def _addr(t: Optional[torch.Tensor], index: int):
-    """Device address of a contiguous tensor on CUDA device ``index`` (None -> NULL)."""
-    if t is None:
-        return None
-    if t.get_device() != index or not t.is_contiguous():
-        _ptr(t, torch.device("cuda", index))  # says what is wrong with it
-    return t.data_ptr()
+_REAL = {torch.float32: F32, torch.bfloat16: BF16}
+_workspaces: Dict[tuple, int] = {}  # workspace bytes by problem (sizes, types and flags), so a call need not ask again
 
 
 def _expect(name: str, t: Optional[torch.Tensor], shape, dtype) -> None:
     if t is not None and (t.shape != shape or t.dtype is not dtype):
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def _addr(tensors, index: int):
+    """Device addresses of contiguous tensors on CUDA device ``index`` (None -> NULL)."""
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+        elif t.get_device() == index and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            _ptr(t, torch.device("cuda", index))  # says what is wrong with it
+    return out
 
 
 def _handle(stream, index: int) -> int:
@@ -516,8 +522,6 @@ def _handle(stream, index: int) -> int:
 
 def _used_on(stream, index: int, tensors) -> None:
     """Tensors allocated here for a call on ``stream``: the allocator must not reuse them before it is done."""
-    if stream is None:
-        return
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_handle(stream, index), index)
     for t in tensors:
         if t is not None:
@@ -533,9 +537,10 @@ def _size(fn, pb, where: str) -> int:
 def _index(t: torch.Tensor) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError("expected a torch.Tensor")
-    if not t.is_cuda:
+    i = t.get_device()
+    if i < 0:
         raise ValueError("libpdssm takes device memory only; got a CPU tensor")
-    return t.get_device()
+    return i
 
 
 def _nbytes(workspace: Optional[torch.Tensor]) -> int:
@@ -544,8 +549,9 @@ def _nbytes(workspace: Optional[torch.Tensor]) -> int:
 
 def pdssm_qk_norm(pb: NormProblem, q, k, wq, wk, inv_freq, positions, q_out, k_out, stream=None) -> None:
     i = _index(q)
-    _check(_lib.pdssm_qk_norm(pb, _addr(q, i), _addr(k, i), _addr(wq, i), _addr(wk, i), _addr(inv_freq, i),
-                              _addr(positions, i), _addr(q_out, i), _addr(k_out, i), _handle(stream, i)), "pdssm_qk_norm")
+    st = _lib.pdssm_qk_norm(pb, *_addr((q, k, wq, wk, inv_freq, positions, q_out, k_out), i), _handle(stream, i))
+    if st:
+        raise PdssmError(st, "pdssm_qk_norm")
 
 
 def pdssm_qk_norm_bwd_workspace_size(pb: NormProblem) -> int:
@@ -555,10 +561,10 @@ def pdssm_qk_norm_bwd_workspace_size(pb: NormProblem) -> int:
 def pdssm_qk_norm_bwd(pb: NormProblem, q, k, wq, wk, inv_freq, positions, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
                       stream=None) -> None:
     i = _index(q)
-    _check(_lib.pdssm_qk_norm_bwd(pb, _addr(q, i), _addr(k, i), _addr(wq, i), _addr(wk, i), _addr(inv_freq, i),
-                                  _addr(positions, i), _addr(dq_out, i), _addr(dk_out, i), _addr(dq, i), _addr(dk, i),
-                                  _addr(dwq, i), _addr(dwk, i), _addr(workspace, i), _nbytes(workspace),
-                                  _handle(stream, i)), "pdssm_qk_norm_bwd")
+    st = _lib.pdssm_qk_norm_bwd(pb, *_addr((q, k, wq, wk, inv_freq, positions, dq_out, dk_out, dq, dk, dwq, dwk, workspace), i),
+                                _nbytes(workspace), _handle(stream, i))
+    if st:
+        raise PdssmError(st, "pdssm_qk_norm_bwd")
 
 
 def pdssm_delta_workspace_size(pb: DeltaProblem) -> int:
@@ -567,9 +573,10 @@ def pdssm_delta_workspace_size(pb: DeltaProblem) -> int:
 
 def pdssm_delta_fwd(pb: DeltaProblem, q, k, v, g, beta, lengths, h0, y, h_final, workspace, stream=None) -> None:
     i = _index(q)
-    _check(_lib.pdssm_delta_fwd(pb, _addr(q, i), _addr(k, i), _addr(v, i), _addr(g, i), _addr(beta, i),
-                                _addr(lengths, i), _addr(h0, i), _addr(y, i), _addr(h_final, i), _addr(workspace, i),
-                                _nbytes(workspace), _handle(stream, i)), "pdssm_delta_fwd")
+    st = _lib.pdssm_delta_fwd(pb, *_addr((q, k, v, g, beta, lengths, h0, y, h_final, workspace), i), _nbytes(workspace),
+                              _handle(stream, i))
+    if st:
+        raise PdssmError(st, "pdssm_delta_fwd")
 
 
 def pdssm_delta_bwd_workspace_size(pb: DeltaProblem) -> int:
@@ -579,27 +586,33 @@ def pdssm_delta_bwd_workspace_size(pb: DeltaProblem) -> int:
 def pdssm_delta_bwd(pb: DeltaProblem, q, k, v, g, beta, lengths, h0, dy, dh_final, dq, dk, dv, dg, dbeta, dh0, workspace,
                     stream=None) -> None:
     i = _index(q)
-    _check(_lib.pdssm_delta_bwd(pb, _addr(q, i), _addr(k, i), _addr(v, i), _addr(g, i), _addr(beta, i),
-                                _addr(lengths, i), _addr(h0, i), _addr(dy, i), _addr(dh_final, i), _addr(dq, i),
-                                _addr(dk, i), _addr(dv, i), _addr(dg, i), _addr(dbeta, i), _addr(dh0, i),
-                                _addr(workspace, i), _nbytes(workspace), _handle(stream, i)), "pdssm_delta_bwd")
+    st = _lib.pdssm_delta_bwd(pb, *_addr((q, k, v, g, beta, lengths, h0, dy, dh_final, dq, dk, dv, dg, dbeta, dh0, workspace), i),
+                              _nbytes(workspace), _handle(stream, i))
+    if st:
+        raise PdssmError(st, "pdssm_delta_bwd")
 
 
 def _norm_problem(q, k, wq, wk, inv_freq, positions, eps, mode, interleaved) -> NormProblem:
+    dt = q.dtype
     if mode not in _NORM_MODES:
         raise ValueError(f"mode must be 'rms' or 'l2', got {mode!r}")
-    if q.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"q and k must be float32 or bfloat16, got {q.dtype}")
+    if dt not in _REAL:
+        raise ValueError(f"q and k must be float32 or bfloat16, got {dt}")
     Bt, L, Hq, N = q.shape
-    _expect("k", k, (Bt, L, k.shape[2], N), q.dtype)
-    _expect("wq", wq, (N,), torch.float32)
-    _expect("wk", wk, (N,), torch.float32)
-    _expect("positions", positions, (Bt, L), torch.int32)
+    kb, kl, Hk, kn = k.shape
+    if kb != Bt or kl != L or kn != N or k.dtype is not dt:
+        _expect("k", k, (Bt, L, Hk, N), dt)
+    if wq is not None:
+        _expect("wq", wq, (N,), torch.float32)
+    if wk is not None:
+        _expect("wk", wk, (N,), torch.float32)
+    if positions is not None:
+        _expect("positions", positions, (Bt, L), torch.int32)
     rot = 0
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
         _expect("inv_freq", inv_freq, (rot // 2,), torch.float32)
-    return NormProblem(Bt, L, Hq, k.shape[2], N, _DT[q.dtype], _NORM_MODES[mode], rot, int(interleaved), eps, 0)
+    return NormProblem(Bt, L, Hq, Hk, N, _REAL[dt], _NORM_MODES[mode], rot, int(interleaved), eps, 0)
 
 
 def qk_norm(q: torch.Tensor, k: torch.Tensor, wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None,
@@ -611,12 +624,20 @@ def qk_norm(q: torch.Tensor, k: torch.Tensor, wq: Optional[torch.Tensor] = None,
     sequence). ``mode``: "rms" or "l2". Results: "q", "k", written to ``q_out`` / ``k_out`` where given
     (which may be q and k themselves)."""
     pb = _norm_problem(q, k, wq, wk, inv_freq, positions, eps, mode, interleaved)
-    _expect("q_out", q_out, q.shape, q.dtype)
-    _expect("k_out", k_out, k.shape, q.dtype)
-    new = [torch.empty_like(q) if q_out is None else None, torch.empty_like(k) if k_out is None else None]
-    q_out, k_out = q_out if new[0] is None else new[0], k_out if new[1] is None else new[1]
+    new = []
+    if q_out is None:
+        q_out = torch.empty_like(q)
+        new.append(q_out)
+    else:
+        _expect("q_out", q_out, q.shape, q.dtype)
+    if k_out is None:
+        k_out = torch.empty_like(k)
+        new.append(k_out)
+    else:
+        _expect("k_out", k_out, k.shape, q.dtype)
     pdssm_qk_norm(pb, q, k, wq, wk, inv_freq, positions, q_out, k_out, stream)
-    _used_on(stream, q.get_device(), new)
+    if stream is not None:
+        _used_on(stream, q.get_device(), new)
     return {"q": q_out, "k": k_out}
 
 
@@ -640,24 +661,45 @@ def qk_norm_backward(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_
         ws = torch.empty(pdssm_qk_norm_bwd_workspace_size(pb), dtype=torch.uint8, device=q.device)
     pdssm_qk_norm_bwd(pb, q, k, wq, wk, inv_freq, positions, dq_out, dk_out, out["dq"], out["dk"], out.get("dwq"),
                       out.get("dwk"), ws, stream)
-    _used_on(stream, q.get_device(), [ws, *out.values()])
+    if stream is not None:
+        _used_on(stream, q.get_device(), [ws, *out.values()])
     return out
 
 
-def _delta_problem(q, k, v, g, beta, h0, scale, lengths, flags) -> DeltaProblem:
-    if q.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"q, k and v must be float32 or bfloat16, got {q.dtype}")
-    if g.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"g and beta must be float32 or bfloat16, got {g.dtype}")
-    Bt, L, Hk, N = q.shape
-    H, P = v.shape[2:]
-    _expect("k", k, q.shape, q.dtype)
-    _expect("v", v, (Bt, L, H, P), q.dtype)
-    _expect("g", g, (Bt, L, H), g.dtype)
-    _expect("beta", beta, g.shape, g.dtype)
-    _expect("h0", h0, (Bt, H, N, P), torch.float32)
-    _expect("lengths", lengths, (Bt,), torch.int32)
-    return DeltaProblem(Bt, L, H, Hk, N, P, _DT[q.dtype], _DT[g.dtype], N ** -0.5 if scale is None else scale, flags)
+def _delta_problem(q, k, v, g, beta, h0, scale, lengths, flags):
+    """The problem, and its key in the table of workspace sizes."""
+    dt, gt = q.dtype, g.dtype
+    if dt not in _REAL:
+        raise ValueError(f"q, k and v must be float32 or bfloat16, got {dt}")
+    if gt not in _REAL:
+        raise ValueError(f"g and beta must be float32 or bfloat16, got {gt}")
+    shape = q.shape
+    Bt, L, Hk, N = shape
+    vb, vl, H, P = v.shape
+    if k.shape != shape or k.dtype is not dt:
+        _expect("k", k, shape, dt)
+    if vb != Bt or vl != L or v.dtype is not dt:
+        _expect("v", v, (Bt, L, H, P), dt)
+    gates = (Bt, L, H)
+    if g.shape != gates:
+        _expect("g", g, gates, gt)
+    if beta.shape != gates or beta.dtype is not gt:
+        _expect("beta", beta, gates, gt)
+    if h0 is not None:
+        _expect("h0", h0, (Bt, H, N, P), torch.float32)
+    if lengths is not None:
+        _expect("lengths", lengths, (Bt,), torch.int32)
+    key = (Bt, L, H, Hk, N, P, _REAL[dt], _REAL[gt], flags)
+    return DeltaProblem(Bt, L, H, Hk, N, P, key[6], key[7], N ** -0.5 if scale is None else scale, flags), key
+
+
+def _workspace_bytes(fn, pb: DeltaProblem, key: tuple) -> int:
+    n = _workspaces.get((fn.__name__,) + key)
+    if n is None:
+        if len(_workspaces) >= 4096:
+            _workspaces.clear()
+        n = _workspaces[(fn.__name__,) + key] = fn(pb)
+    return n
 
 
 def delta_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
@@ -671,22 +713,22 @@ def delta_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     g (log decay), beta [Bt, L, H]; h0 [Bt, H, N, P] float32; lengths int32 [Bt]: steps of each sequence, the
     rest is padding. scale: N ** -0.5 by default. Results: "y" like v and, unless ``want_h_final`` is false,
     "h_final", written to ``h_final`` where given, which may be ``h0`` itself."""
-    pb = _delta_problem(q, k, v, g, beta, h0, scale, lengths, flags)
-    i = _index(q)
+    pb, key = _delta_problem(q, k, v, g, beta, h0, scale, lengths, flags)
     y = torch.empty_like(v)
     new = [y]
     if h_final is not None:
-        _expect("h_final", h_final, (pb.batch, pb.heads, pb.N, pb.P), torch.float32)
+        _expect("h_final", h_final, (key[0], key[2], key[4], key[5]), torch.float32)
     elif want_h_final:
-        h_final = torch.empty(pb.batch, pb.heads, pb.N, pb.P, dtype=torch.float32, device=q.device)
+        h_final = torch.empty_like(h0) if h0 is not None else v.new_empty((key[0], key[2], key[4], key[5]), dtype=torch.float32)
         new.append(h_final)
     if workspace is None:
-        n = pdssm_delta_workspace_size(pb)
+        n = _workspace_bytes(pdssm_delta_workspace_size, pb, key)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
             new.append(workspace)
     pdssm_delta_fwd(pb, q, k, v, g, beta, lengths, h0, y, h_final, workspace, stream)
-    _used_on(stream, i, new)
+    if stream is not None:
+        _used_on(stream, q.get_device(), new)
     return {"y": y} if h_final is None else {"y": y, "h_final": h_final}
 
 
@@ -698,19 +740,23 @@ def delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     """Gradients of ``delta_forward`` for dy (like v) and dh_final (float32 [Bt, H, N, P] or None: zeros):
     "dq", "dk" (summed over the value heads that share a key head), "dv", "dg", "dbeta", each in the type of what
     it belongs to, and "dh0" (by default where an h0 is given)."""
-    pb = _delta_problem(q, k, v, g, beta, h0, scale, lengths, flags)
+    pb, key = _delta_problem(q, k, v, g, beta, h0, scale, lengths, flags)
+    state = (key[0], key[2], key[4], key[5])
     _expect("dy", dy, v.shape, v.dtype)
-    _expect("dh_final", dh_final, (pb.batch, pb.heads, pb.N, pb.P), torch.float32)
-    i = _index(q)
-    out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v), "dg": torch.empty_like(g),
-           "dbeta": torch.empty_like(beta)}
-    if h0 is not None if want_dh0 is None else want_dh0:
-        out["dh0"] = torch.empty(pb.batch, pb.heads, pb.N, pb.P, dtype=torch.float32, device=q.device)
-    new = list(out.values())
+    if dh_final is not None:
+        _expect("dh_final", dh_final, state, torch.float32)
+    dq, dk, dv, dg, db = (torch.empty_like(x) for x in (q, k, v, g, beta))
+    dh0 = None
+    if want_dh0 or (want_dh0 is None and h0 is not None):
+        dh0 = v.new_empty(state, dtype=torch.float32)
+    new = [dq, dk, dv, dg, db, dh0]
     if workspace is None:
-        workspace = torch.empty(pdssm_delta_bwd_workspace_size(pb), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(_workspace_bytes(pdssm_delta_bwd_workspace_size, pb, key), dtype=torch.uint8, device=q.device)
         new.append(workspace)
-    pdssm_delta_bwd(pb, q, k, v, g, beta, lengths, h0, dy, dh_final, out["dq"], out["dk"], out["dv"], out["dg"],
-                    out["dbeta"], out.get("dh0"), workspace, stream)
-    _used_on(stream, i, new)
+    pdssm_delta_bwd(pb, q, k, v, g, beta, lengths, h0, dy, dh_final, dq, dk, dv, dg, db, dh0, workspace, stream)
+    if stream is not None:
+        _used_on(stream, q.get_device(), new)
+    out = {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dbeta": db}
+    if dh0 is not None:
+        out["dh0"] = dh0
     return out

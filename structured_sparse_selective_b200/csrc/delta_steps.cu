@@ -1,17 +1,16 @@
 // The gated delta rule step by step (formulas in delta.cuh), forwards and backwards:
-// single tokens and short runs, fp32 inputs, and every size.
+// short runs, fp32 inputs and every size, and one kernel for a single token.
 //
-// The columns of H are independent of one another. A warp owns 16 columns: lane
-// (rg, cl) = (lane / 4, lane % 4) holds columns 4 cl .. 4 cl + 3 and rows
-// 32 j + 4 rg .. + 3 in registers for the whole sequence, so the state moves once in
-// and once out. k^T H is a sum over the lane's rows and three shuffles over the eight
-// row groups; no barrier joins the warps but the one a tile of 8 steps has, whose
-// k, q, v, decay and beta a loader warp brings to shared memory in fp32 while the
-// others work on the tile before.
-// A step's products are in row pairs (fma.rn.f32x2), which halves the instructions.
-// What bounds it: for one step the state's bytes (read and written once); for long
-// sequences the chain dot -> shuffles -> update of each step, and with enough
-// sequences the issue rate of its ~140 instructions a warp.
+// The columns of H are independent of one another, so a lane has one column, all its rows
+// in registers for the whole sequence: k^T H and q^T H are sums inside a lane, and a step
+// needs neither shuffles nor barriers (with rows spread over eight lanes and three shuffles
+// a step, a step of 32 rows took 400 cycles). A step is one pass over the row pairs,
+//   H = a H + u k,  y += q H,  next e: d += k' H   (k' the next step's key),
+// four packed instructions a pair (fma.rn.f32x2 works on two rows). k and q come from
+// shared memory as broadcasts; four loader warps bring them there, with v, the decay and
+// beta, in fp32, a tile of 8 steps ahead, so one barrier joins the warps every 8 steps.
+// What bounds it: the chain of steps, one sequence's time being length x (issue of 64 to
+// 256 packed instructions + the latency of the last sums); the state moves once in and out.
 #include <algorithm>
 
 #include "delta.cuh"
@@ -20,9 +19,10 @@ namespace pdssm {
 
 namespace {
 
-constexpr int kTS = 8;        // steps a tile
-constexpr int kWarpCols = 16;
-constexpr int kMaxWarps = PDSSM_MAX_P / kWarpCols;
+constexpr int kTS = 8;  // steps a tile
+constexpr int kMaxWarps = PDSSM_MAX_P / 32;
+// One loader warp took 3,000 cycles for a tile, longer than the steps of 32 rows in it.
+constexpr int kLoaders = 4, kLS = kTS / kLoaders;
 
 // One tile in shared memory: rows of k and q (padded with zeros to 32 J), of the
 // block's columns of v (or dy), and (a, beta).
@@ -42,25 +42,25 @@ struct Tile {
   static size_t bytes(int cols) { return (size_t)2 * kTS * (2 * kRow + cols + 2) * 4; }
 };
 
-// The loader warp. A tile's values wait in registers while the tile before is computed:
+// A loader warp, with kLS steps of each tile. A tile's values wait in registers while the tile before is computed:
 // fetch() starts the loads of one tile, put() writes them to shared memory a tile later,
 // so HBM's latency is behind a whole tile's work. The loads are unconditional, from a
 // valid place where there is nothing to load: with a branch around each they ran one
-// after the other (LM layer: 1.9 ms).
+// after the other.
 template <int J, typename T, typename G>
 struct Loader {
-  static constexpr int M = kMaxWarps / 2;
+  static constexpr int M = kMaxWarps;
   const DeltaArgs &a;
   const T *k, *q, *c;
   const G *g, *beta;
-  int lane, p0, cols, n;
+  int lane, first, p0, cols, n;  // first: the warp's first step of a tile
   int64_t rowk, rowc;
-  T kv[kTS][J], qv[kTS][J], cv[kTS][M];
+  T kv[kLS][J], qv[kLS][J], cv[kLS][M];
   G gv, bv;
 
   // `src`: v forwards, dy backwards.
-  __device__ Loader(const DeltaArgs &a_, int64_t b, int64_t h, int p0_, int cols_, const void *src)
-      : a(a_), lane(threadIdx.x & 31), p0(p0_), cols(cols_), n(0), rowk(a_.Hk * a_.N), rowc(a_.H * a_.P) {
+  __device__ Loader(const DeltaArgs &a_, int64_t b, int64_t h, int who, int p0_, int cols_, const void *src)
+      : a(a_), lane(threadIdx.x & 31), first(who * kLS), p0(p0_), cols(cols_), n(0), rowk(a_.Hk * a_.N), rowc(a_.H * a_.P) {
     const int64_t hk = h / (a.H / a.Hk);
     k = static_cast<const T *>(a.k) + b * a.L * rowk + hk * a.N;
     q = static_cast<const T *>(a.q) + b * a.L * rowk + hk * a.N;
@@ -74,8 +74,8 @@ struct Loader {
     n = (int)(steps < kTS ? steps : kTS);
     if (n <= 0) return;
 #pragma unroll
-    for (int s = 0; s < kTS; ++s) {
-      const int64_t t = t0 + min(s, n - 1);
+    for (int s = 0; s < kLS; ++s) {
+      const int64_t t = t0 + min(first + s, n - 1);
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const int i = min(lane + 32 * j, (int)a.N - 1);
@@ -85,144 +85,80 @@ struct Loader {
 #pragma unroll
       for (int j = 0; j < M; ++j) cv[s][j] = c[t * rowc + min(p0 + min(lane + 32 * j, cols - 1), (int)a.P - 1)];
     }
-    const int64_t t = (t0 + min(lane, n - 1)) * a.H;
-    gv = g[t];
-    bv = beta[t];
+    if (first == 0) {
+      const int64_t t = (t0 + min(lane, n - 1)) * a.H;
+      gv = g[t];
+      bv = beta[t];
+    }
   }
 
   __device__ __forceinline__ void put(const Tile<J> &tile) {
     if (n <= 0) return;
 #pragma unroll
-    for (int s = 0; s < kTS; ++s) {
+    for (int s = 0; s < kLS; ++s) {
+      const int at = first + s;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const int i = lane + 32 * j;
-        tile.k[s * 32 * J + i] = i < a.N ? to_f32(kv[s][j]) : 0.f;
-        tile.q[s * 32 * J + i] = i < a.N ? to_f32(qv[s][j]) * a.scale : 0.f;
+        tile.k[at * 32 * J + i] = i < a.N ? to_f32(kv[s][j]) : 0.f;
+        tile.q[at * 32 * J + i] = i < a.N ? to_f32(qv[s][j]) * a.scale : 0.f;
       }
 #pragma unroll
       for (int j = 0; j < M; ++j) {
         const int i = lane + 32 * j;
-        if (i < cols) tile.c[s * cols + i] = p0 + i < a.P ? to_f32(cv[s][j]) : 0.f;
+        if (i < cols) tile.c[at * cols + i] = p0 + i < a.P ? to_f32(cv[s][j]) : 0.f;
       }
     }
-    if (lane < kTS) tile.ab[lane] = make_float2(expf(clamp_gate(to_f32(gv))), to_f32(bv));
+    if (first == 0 && lane < kTS) tile.ab[lane] = make_float2(expf(clamp_gate(to_f32(gv))), to_f32(bv));
   }
 };
 
-// The lane's part of a state [N][P] at `p` (null: zeros), in row pairs.
-template <int J>
-__device__ __forceinline__ void load_state(pair2 (&h)[2 * J][4], const float *p, int64_t N, int64_t P, int64_t ld, int rg, int col) {
-  const bool wide = ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+// A column of a state [N][ld] at `p` (null: zeros) in row pairs.
+template <int R>
+__device__ __forceinline__ void load_column(pair2 (&x)[R], const float *p, int N, int64_t ld, bool in) {
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    float v[4][4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t n = 32 * j + 4 * rg + r;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[r][c] = 0.f;
-      if (p && n < N) {
-        if (wide && col + 3 < P) {
-          const float4 x = *reinterpret_cast<const float4 *>(p + n * ld + col);
-          v[r][0] = x.x; v[r][1] = x.y; v[r][2] = x.z; v[r][3] = x.w;
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (col + c < P) v[r][c] = p[n * ld + col + c];
-        }
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      h[2 * j][c] = pack2(v[0][c], v[1][c]);
-      h[2 * j + 1][c] = pack2(v[2][c], v[3][c]);
-    }
-  }
+  for (int r = 0; r < R; ++r)
+    x[r] = pack2(p && in && 2 * r < N ? p[2 * r * ld] : 0.f, p && in && 2 * r + 1 < N ? p[(2 * r + 1) * ld] : 0.f);
 }
 
-template <int J>
-__device__ __forceinline__ void store_state(const pair2 (&h)[2 * J][4], float *p, int64_t N, int64_t P, int64_t ld, int rg, int col) {
-  const bool wide = ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+template <int R>
+__device__ __forceinline__ void store_column(const pair2 (&x)[R], float *p, int N, int64_t ld) {
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    float v[4][4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      unpack2(h[2 * j][c], v[0][c], v[1][c]);
-      unpack2(h[2 * j + 1][c], v[2][c], v[3][c]);
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t n = 32 * j + 4 * rg + r;
-      if (n >= N) continue;
-      if (wide && col + 3 < P) {
-        *reinterpret_cast<float4 *>(p + n * ld + col) = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (col + c < P) p[n * ld + col + c] = v[r][c];
-      }
-    }
-  }
-}
-
-// The lane's four rows a j of a vector in shared memory, as pairs.
-template <int J>
-__device__ __forceinline__ void load_rows(pair2 (&x)[2 * J], const float *p, int rg) {
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const float4 v = *reinterpret_cast<const float4 *>(p + 32 * j + 4 * rg);
-    x[2 * j] = pack2(v.x, v.y);
-    x[2 * j + 1] = pack2(v.z, v.w);
-  }
-}
-
-// s[c] = sum over the lane's rows of x h[c].
-template <int J>
-__device__ __forceinline__ void dot_rows(float (&s)[4], const pair2 (&x)[2 * J], const pair2 (&h)[2 * J][4]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    pair2 p = mul2(x[0], h[0][c]);
-#pragma unroll
-    for (int i = 1; i < 2 * J; ++i) p = fma2(x[i], h[i][c], p);
+  for (int r = 0; r < R; ++r) {
     float u, w;
-    unpack2(p, u, w);
-    s[c] = u + w;
+    unpack2(x[r], u, w);
+    if (2 * r < N) p[2 * r * ld] = u;
+    if (2 * r + 1 < N) p[(2 * r + 1) * ld] = w;
   }
 }
 
-// Sum over the eight row groups, in every lane.
-__device__ __forceinline__ void sum_groups(float (&s)[4]) {
+__device__ __forceinline__ float total(const pair2 (&s)[4]) {
+  float v[8];
 #pragma unroll
-  for (int o = 4; o < 32; o <<= 1)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) s[c] += __shfl_xor_sync(0xffffffffu, s[c], o);
+  for (int i = 0; i < 4; ++i) unpack2(s[i], v[2 * i], v[2 * i + 1]);
+  return ((v[0] + v[2]) + (v[4] + v[6])) + ((v[1] + v[3]) + (v[5] + v[7]));
 }
 
-// Sum over the eight row groups of column c = 2 (lane >> 4) + (lane >> 3 & 1) of the
-// lane's four: four shuffles instead of twelve where one lane needs one column.
-__device__ __forceinline__ float sum_groups_one(const float (&s)[4], int lane) {
-  const bool up = lane & 16, mid = lane & 8;
-  const float a = (up ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, up ? s[0] : s[2], 16);
-  const float b = (up ? s[3] : s[1]) + __shfl_xor_sync(0xffffffffu, up ? s[1] : s[3], 16);
-  float r = (mid ? b : a) + __shfl_xor_sync(0xffffffffu, mid ? a : b, 8);
-  return r + __shfl_xor_sync(0xffffffffu, r, 4);
+// Four rows of a vector in shared memory.
+__device__ __forceinline__ void two_pairs(const float *p, pair2 &x, pair2 &y) {
+  const float4 v = *reinterpret_cast<const float4 *>(p);
+  x = pack2(v.x, v.y);
+  y = pack2(v.z, v.w);
 }
 
-// grid: (column groups, heads, batch); warps 0 .. warps - 1 compute, the last loads.
+// grid: (column groups, heads, batch); warps 0 .. warps - 1 compute, the others load.
 // SAVE: writes e_t and, every a.C steps, the state before them (for the backward pass).
 template <int J, typename T, typename G, bool SAVE>
-__global__ void __launch_bounds__(32 * (kMaxWarps + 1)) delta_steps_kernel(DeltaArgs a) {
+__global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_kernel(DeltaArgs a) {
+  constexpr int R = 16 * J, kRow = 32 * J;
+  constexpr bool kKeep = J <= 2;  // a step's key stays in registers from the pass before
   extern __shared__ __align__(16) float smem[];
-  const int warps = blockDim.x / 32 - 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rg = lane >> 2, cols = warps * kWarpCols, p0 = blockIdx.x * cols;
+  const int warps = blockDim.x / 32 - kLoaders, warp = threadIdx.x >> 5;
+  const int cols = warps * 32, p0 = blockIdx.x * cols;
   const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.H + h;
   const int64_t len = live_steps(a.lengths, b, a.L);
-  const int col = p0 + warp * kWarpCols + 4 * (lane & 3);
-  const bool loader = warp == warps;
-  if (loader) {
-    Loader<J, T, G> in(a, b, h, p0, cols, a.v);
+  if (warp >= warps) {
+    Loader<J, T, G> in(a, b, h, warp - warps, p0, cols, a.v);
     in.fetch(0, len);
     in.put(Tile<J>(smem, cols, 0));
     in.fetch(kTS, len - kTS);
@@ -234,69 +170,106 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1)) delta_steps_kernel(Delta
     }
     return;
   }
-  pair2 st[2 * J][4];
-  load_state<J>(st, a.h0 ? a.h0 + bh * a.N * a.P : nullptr, a.N, a.P, a.P, rg, col);
+  const int col = p0 + threadIdx.x, N = (int)a.N;
+  const bool in = col < a.P, room = col < a.Pp;
+  pair2 st[R];
+  load_column<R>(st, a.h0 ? a.h0 + bh * a.N * a.P + col : nullptr, N, a.P, in);
   __syncthreads();
-  const int yc = 2 * (lane >> 4) + ((lane >> 3) & 1);
-  T *y = static_cast<T *>(a.y);
-  for (int64_t t0 = 0, i = 0; t0 < len; t0 += kTS, ++i) {
-    const Tile<J> tile(smem, cols, i & 1);
-    const int n = (int)min((int64_t)kTS, len - t0);
-    for (int s = 0; s < n; ++s) {
-      if (SAVE && ((t0 + s) & (a.C - 1)) == 0)
-        store_state<J>(st, a.carry + (bh * a.nC + (t0 + s) / a.C) * a.N * a.Pp, a.N, a.Pp, a.Pp, rg, col);
-      pair2 k[2 * J], q[2 * J];
-      load_rows<J>(k, tile.k + s * 32 * J, rg);
-      load_rows<J>(q, tile.q + s * 32 * J, rg);
-      const float4 v4 = *reinterpret_cast<const float4 *>(tile.c + s * cols + warp * kWarpCols + 4 * (lane & 3));
-      const float2 ab = tile.ab[s];
-      float d[4], e[4];
-      dot_rows<J>(d, k, st);
-      sum_groups(d);
-      e[0] = fmaf(-ab.x, d[0], v4.x); e[1] = fmaf(-ab.x, d[1], v4.y);
-      e[2] = fmaf(-ab.x, d[2], v4.z); e[3] = fmaf(-ab.x, d[3], v4.w);
-      const int64_t row = (b * a.L + t0 + s) * a.H + h;
-      if (SAVE && lane < 4 && col < a.Pp)
-        *reinterpret_cast<float4 *>(a.e + row * a.Pp + col) = make_float4(e[0], e[1], e[2], e[3]);
-      const pair2 aa = pack2(ab.x, ab.x);
+  T *y = static_cast<T *>(a.y) + (b * a.L * a.H + h) * a.P + col;
+  float *e_out = SAVE ? a.e + (b * a.L * a.H + h) * a.Pp + col : nullptr;
+  const int64_t step = a.H * (SAVE ? a.Pp : a.P);
+  pair2 d[4] = {}, k[kKeep ? R : 2];
+  const auto first_key = [&](const float *ks) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float u = ab.y * e[c];
-        const pair2 uu = pack2(u, u);
-#pragma unroll
-        for (int r = 0; r < 2 * J; ++r) st[r][c] = fma2(k[r], uu, mul2(aa, st[r][c]));
+    for (int r = 0; r < R; r += 2) {
+      pair2 k0, k1;
+      two_pairs(ks + 2 * r, k0, k1);
+      d[r & 3] = fma2(k0, st[r], d[r & 3]);
+      d[(r + 1) & 3] = fma2(k1, st[r + 1], d[(r + 1) & 3]);
+      if (kKeep) {
+        k[r % (kKeep ? R : 2)] = k0;
+        k[(r + 1) % (kKeep ? R : 2)] = k1;
       }
+    }
+  };
+  if (len > 0) first_key(Tile<J>(smem, cols, 0).k);
+  for (int64_t t0 = 0, i = 0; t0 < len; t0 += kTS, ++i) {
+    const int n = (int)min((int64_t)kTS, len - t0);
+    const Tile<J> tile(smem, cols, i & 1), after(smem, cols, (i + 1) & 1);
+    for (int s = 0; s < n; ++s) {
+      if (SAVE && room && ((t0 + s) & (a.C - 1)) == 0)
+        store_column<R>(st, a.carry + (bh * a.nC + (t0 + s) / a.C) * a.N * a.Pp + col, N, a.Pp);
+      const float2 ab = tile.ab[s];
+      const float e = fmaf(-ab.x, total(d), tile.c[s * cols + threadIdx.x]);
+      const float u = ab.y * e;
+      const pair2 aa = pack2(ab.x, ab.x), uu = pack2(u, u);
+      if (SAVE && room) {
+        *e_out = e;
+        e_out += step;
+      }
+      // the next step's key, where the tile has it; the next tile's first is read behind the barrier
+      const float *qs = tile.q + s * kRow, *ks = tile.k + s * kRow;
+      pair2 z[4] = {};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) d[r] = 0;
+      const auto pass = [&](bool next) {
+#pragma unroll
+        for (int r = 0; r < R; r += 2) {
+          pair2 q0, q1, k0, k1, n0, n1;
+          if (kKeep) {
+            k0 = k[r % (kKeep ? R : 2)];
+            k1 = k[(r + 1) % (kKeep ? R : 2)];
+          } else {
+            two_pairs(ks + 2 * r, k0, k1);
+          }
+          st[r] = fma2(k0, uu, mul2(aa, st[r]));
+          st[r + 1] = fma2(k1, uu, mul2(aa, st[r + 1]));
+          if (!SAVE) {
+            two_pairs(qs + 2 * r, q0, q1);
+            z[r & 3] = fma2(q0, st[r], z[r & 3]);
+            z[(r + 1) & 3] = fma2(q1, st[r + 1], z[(r + 1) & 3]);
+          }
+          if (next) {
+            two_pairs(ks + kRow + 2 * r, n0, n1);
+            d[r & 3] = fma2(n0, st[r], d[r & 3]);
+            d[(r + 1) & 3] = fma2(n1, st[r + 1], d[(r + 1) & 3]);
+            if (kKeep) {
+              k[r % (kKeep ? R : 2)] = n0;
+              k[(r + 1) % (kKeep ? R : 2)] = n1;
+            }
+          }
+        }
+      };
+      if (s + 1 < n) pass(true);
+      else pass(false);
       if (!SAVE) {
-        float z[4];
-        dot_rows<J>(z, q, st);
-        const float out = sum_groups_one(z, lane);
-        if (!(lane & 4) && col + yc < a.P) st_out(y + row * a.P + col + yc, out);
+        if (in) st_out(y, total(z));
+        y += step;
       }
     }
     __syncthreads();
+    if (t0 + kTS < len) first_key(after.k);
   }
-  if (!SAVE) {
-    for (int64_t t = len + rg; t < a.L; t += 8)
-      for (int c = 0; c < 4; ++c)
-        if (col + c < a.P) st_out(y + ((b * a.L + t) * a.H + h) * a.P + col + c, 0.f);
-    if (a.h_final) store_state<J>(st, a.h_final + bh * a.N * a.P, a.N, a.P, a.P, rg, col);
+  if (!SAVE && in) {
+    for (int64_t t = len; t < a.L; ++t, y += step) st_out(y, 0.f);
+    if (a.h_final) store_column<R>(st, a.h_final + bh * a.N * a.P + col, N, a.P);
   }
 }
 
-// The adjoint X runs from the last step to the first; writes dv_t, du_t, X' at the end
-// of each chunk of a.C steps, and dh0.
+// The adjoint X runs from the last step to the first; writes dv_t, du_t, X at the end
+// of each chunk of a.C steps, and dh0. A step is one pass over the row pairs:
+//   X = a (X - w k) of the step behind, X += dy q, du += k X.
 template <int J, typename T, typename G>
-__global__ void __launch_bounds__(32 * (kMaxWarps + 1)) delta_steps_bwd_kernel(DeltaArgs a) {
+__global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_bwd_kernel(DeltaArgs a) {
+  constexpr int R = 16 * J, kRow = 32 * J;
   extern __shared__ __align__(16) float smem[];
-  const int warps = blockDim.x / 32 - 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rg = lane >> 2, cols = warps * kWarpCols, p0 = blockIdx.x * cols;
+  const int warps = blockDim.x / 32 - kLoaders, warp = threadIdx.x >> 5;
+  const int cols = warps * 32, p0 = blockIdx.x * cols;
   const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.H + h;
   const int64_t len = live_steps(a.lengths, b, a.L);
-  const int col = p0 + warp * kWarpCols + 4 * (lane & 3);
-  const bool loader = warp == warps;
   const int64_t tiles = (len + kTS - 1) / kTS;
-  if (loader) {
-    Loader<J, T, G> in(a, b, h, p0, cols, a.dy);
+  if (warp >= warps) {
+    Loader<J, T, G> in(a, b, h, warp - warps, p0, cols, a.dy);
     const auto fetch = [&](int64_t i) {  // the i-th tile from the end; nothing behind the first
       const int64_t t0 = (tiles - 1 - i) * kTS;
       in.fetch(t0, i < tiles ? len - t0 : 0);
@@ -312,75 +285,170 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1)) delta_steps_bwd_kernel(D
     }
     return;
   }
-  pair2 st[2 * J][4];
-  load_state<J>(st, a.dh_final ? a.dh_final + bh * a.N * a.P : nullptr, a.N, a.P, a.P, rg, col);
+  const int col = p0 + threadIdx.x, N = (int)a.N;
+  const bool in = col < a.P, room = col < a.Pp;
+  pair2 x[R];
+  load_column<R>(x, a.dh_final ? a.dh_final + bh * a.N * a.P + col : nullptr, N, a.P, in);
   __syncthreads();
-  T *dv = static_cast<T *>(a.dv);
+  T *dv = static_cast<T *>(a.dv) + (b * a.L * a.H + h) * a.P + col;
+  float *du_out = a.du + (b * a.L * a.H + h) * a.Pp + col;
   for (int64_t i = 0; i < tiles; ++i) {
     const int64_t t0 = (tiles - 1 - i) * kTS;
     const Tile<J> tile(smem, cols, i & 1);
     const int n = (int)min((int64_t)kTS, len - t0);
     for (int s = n - 1; s >= 0; --s) {
       const int64_t t = t0 + s;
-      if (t == len - 1 || ((t + 1) & (a.C - 1)) == 0)
-        store_state<J>(st, a.xcarry + (bh * a.nC + t / a.C) * a.N * a.Pp, a.N, a.Pp, a.Pp, rg, col);
-      pair2 k[2 * J], q[2 * J];
-      load_rows<J>(k, tile.k + s * 32 * J, rg);
-      load_rows<J>(q, tile.q + s * 32 * J, rg);
-      const float4 d4 = *reinterpret_cast<const float4 *>(tile.c + s * cols + warp * kWarpCols + 4 * (lane & 3));
+      if (room && (t == len - 1 || ((t + 1) & (a.C - 1)) == 0))
+        store_column<R>(x, a.xcarry + (bh * a.nC + t / a.C) * a.N * a.Pp + col, N, a.Pp);
       const float2 ab = tile.ab[s];
-      const float dy[4] = {d4.x, d4.y, d4.z, d4.w};
+      const float dy = tile.c[s * cols + threadIdx.x];
+      const pair2 dd = pack2(dy, dy), aa = pack2(ab.x, ab.x);
+      const float *ks = tile.k + s * kRow, *qs = tile.q + s * kRow;
+      pair2 sum[4] = {};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const pair2 dd = pack2(dy[c], dy[c]);
-#pragma unroll
-        for (int r = 0; r < 2 * J; ++r) st[r][c] = fma2(q[r], dd, st[r][c]);
+      for (int r = 0; r < R; r += 2) {
+        pair2 q0, q1, k0, k1;
+        two_pairs(qs + 2 * r, q0, q1);
+        two_pairs(ks + 2 * r, k0, k1);
+        x[r] = fma2(q0, dd, x[r]);
+        x[r + 1] = fma2(q1, dd, x[r + 1]);
+        sum[r & 3] = fma2(k0, x[r], sum[r & 3]);
+        sum[(r + 1) & 3] = fma2(k1, x[r + 1], sum[(r + 1) & 3]);
       }
-      float du[4];
-      dot_rows<J>(du, k, st);
-      sum_groups(du);
-      const int64_t row = (b * a.L + t) * a.H + h;
-      const pair2 aa = pack2(ab.x, ab.x);
+      const float du = total(sum), w = ab.y * du;
+      const pair2 ww = pack2(-w, -w);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float w = -ab.y * du[c];
-        const pair2 ww = pack2(w, w);
-#pragma unroll
-        for (int r = 0; r < 2 * J; ++r) st[r][c] = mul2(aa, fma2(k[r], ww, st[r][c]));
+      for (int r = 0; r < R; r += 2) {
+        pair2 k0, k1;
+        two_pairs(ks + 2 * r, k0, k1);
+        x[r] = mul2(aa, fma2(k0, ww, x[r]));
+        x[r + 1] = mul2(aa, fma2(k1, ww, x[r + 1]));
       }
-      if (lane < 4 && col < a.Pp) {
-        *reinterpret_cast<float4 *>(a.du + row * a.Pp + col) = make_float4(du[0], du[1], du[2], du[3]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (col + c < a.P) st_out(dv + row * a.P + col + c, ab.y * du[c]);
-      }
+      if (room) du_out[t * a.H * a.Pp] = du;
+      if (in) st_out(dv + t * a.H * a.P, w);
     }
     __syncthreads();
   }
-  for (int64_t t = len + rg; t < a.L; t += 8)
-    for (int c = 0; c < 4; ++c)
-      if (col + c < a.P) st_out(dv + ((b * a.L + t) * a.H + h) * a.P + col + c, 0.f);
-  if (a.dh0) store_state<J>(st, a.dh0 + bh * a.N * a.P, a.N, a.P, a.P, rg, col);
+  if (!in) return;
+  for (int64_t t = len; t < a.L; ++t) st_out(dv + t * a.H * a.P, 0.f);
+  if (a.dh0) store_column<R>(x, a.dh0 + bh * a.N * a.P + col, N, a.P);
 }
 
-enum Which { kForward, kForwardSave, kBackward };
+// ------------------------------------------------------------------ one token
+
+// One step of every sequence: the state is read and written once and that is the cost, so
+// the rows are spread over the lanes for wide loads: lane (rg, cl) = (lane / 4, lane % 4)
+// has columns 4 cl .. + 3 of the warp's 16 and rows 32 j + 4 rg .. + 3. The warps are on
+// their own; k^T H and q^T H are finished by three shuffles.
+template <int J, typename T, typename G>
+__global__ void __launch_bounds__(128) delta_token_kernel(DeltaArgs a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane >> 2;
+  const int col = (blockIdx.x * (blockDim.x >> 5) + warp) * 16 + 4 * (lane & 3);
+  const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.H + h, hk = h / (a.H / a.Hk);
+  const int N = (int)a.N, P = (int)a.P;
+  const bool on = !a.lengths || a.lengths[b] > 0;
+  const float *h0 = a.h0 ? a.h0 + bh * N * P : nullptr;
+  float *hf = a.h_final ? a.h_final + bh * N * P : nullptr;
+  const bool wide = P % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.h0) | reinterpret_cast<uintptr_t>(a.h_final)) & 15) == 0;
+  float st[4 * J][4];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int n = 32 * j + 4 * rg + r;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (h0 && n < N) {
+        const float *p = h0 + n * P + col;
+        if (wide) {
+          if (col < P) x = *reinterpret_cast<const float4 *>(p);
+        } else {
+          if (col < P) x.x = p[0];
+          if (col + 1 < P) x.y = p[1];
+          if (col + 2 < P) x.z = p[2];
+          if (col + 3 < P) x.w = p[3];
+        }
+      }
+      st[4 * j + r][0] = x.x; st[4 * j + r][1] = x.y; st[4 * j + r][2] = x.z; st[4 * j + r][3] = x.w;
+    }
+  }
+  float k[4 * J], q[4 * J], v[4] = {}, y[4] = {};
+  float decay = 1.f, beta = 0.f;
+  if (on) {
+    const T *kp = static_cast<const T *>(a.k) + (b * a.Hk + hk) * N, *qp = static_cast<const T *>(a.q) + (b * a.Hk + hk) * N;
+#pragma unroll
+    for (int i = 0; i < 4 * J; ++i) {
+      const int n = 32 * (i / 4) + 4 * rg + (i & 3);
+      k[i] = n < N ? ldf(kp + n) : 0.f;
+      q[i] = n < N ? ldf(qp + n) * a.scale : 0.f;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (col + c < P) v[c] = ldf(static_cast<const T *>(a.v) + bh * P + col + c);
+    decay = expf(clamp_gate(ldf(static_cast<const G *>(a.g) + bh)));
+    beta = ldf(static_cast<const G *>(a.beta) + bh);
+    float d[4] = {};
+#pragma unroll
+    for (int i = 0; i < 4 * J; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) d[c] = fmaf(k[i], st[i][c], d[c]);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) d[c] += __shfl_xor_sync(0xffffffffu, d[c], o);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float u = beta * fmaf(-decay, d[c], v[c]);
+#pragma unroll
+      for (int i = 0; i < 4 * J; ++i) {
+        st[i][c] = fmaf(k[i], u, decay * st[i][c]);
+        y[c] = fmaf(q[i], st[i][c], y[c]);
+      }
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) y[c] += __shfl_xor_sync(0xffffffffu, y[c], o);
+  }
+  if (rg == 0) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (col + c < P) st_out(static_cast<T *>(a.y) + bh * P + col + c, y[c]);
+  }
+  if (!hf) return;
+#pragma unroll
+  for (int i = 0; i < 4 * J; ++i) {
+    const int n = 32 * (i / 4) + 4 * rg + (i & 3);
+    if (n >= N) continue;
+    float *p = hf + n * P + col;
+    if (wide) {
+      if (col < P) *reinterpret_cast<float4 *>(p) = make_float4(st[i][0], st[i][1], st[i][2], st[i][3]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (col + c < P) p[c] = st[i][c];
+    }
+  }
+}
+
+enum Which { kForward, kForwardSave, kBackward, kToken };
 
 template <int J, typename T, typename G>
 cudaError_t launch_jtg(const DeltaArgs &a, Which which, cudaStream_t st) {
-  // all columns of a head in one block share its loaded tiles; with few sequences the
-  // columns are spread over more blocks, down to one warp, until there is one an SM
-  int warps = (int)((a.P + kWarpCols - 1) / kWarpCols);
-  const int64_t all = warps;
-  while (warps > 1 && a.Bt * a.H * ((all + warps - 1) / warps) < 148) warps = (warps + 1) / 2;
+  if (which == kToken) {
+    const int groups = (int)((a.P + 15) / 16), warps = std::min(groups, 4);
+    delta_token_kernel<J, T, G><<<dim3((unsigned)((groups + warps - 1) / warps), (unsigned)a.H, (unsigned)a.Bt), 32 * warps, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  // all columns of a head in one block share its loaded tiles; with few sequences each
+  // warp is a block of its own
+  int warps = (int)((a.P + 31) / 32);
+  const int all = warps;
+  if (a.Bt * a.H * all <= 148) warps = 1;
   const dim3 grid((unsigned)((all + warps - 1) / warps), (unsigned)a.H, (unsigned)a.Bt);
-  const size_t smem = Tile<J>::bytes(warps * kWarpCols);
+  const size_t smem = Tile<J>::bytes(warps * 32);
   auto kern = which == kForward ? delta_steps_kernel<J, T, G, false>
                                 : which == kForwardSave ? delta_steps_kernel<J, T, G, true> : delta_steps_bwd_kernel<J, T, G>;
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  kern<<<grid, 32 * (warps + 1), smem, st>>>(a);
+  kern<<<grid, 32 * (warps + kLoaders), smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -401,7 +469,9 @@ cudaError_t launch(const DeltaArgs &a, Which which, const char *name, cudaStream
 
 }  // namespace
 
-cudaError_t launch_delta_steps(const DeltaArgs &a, cudaStream_t st) { return launch(a, kForward, "delta_steps", st); }
+cudaError_t launch_delta_steps(const DeltaArgs &a, cudaStream_t st) {
+  return a.L == 1 ? launch(a, kToken, "delta_token", st) : launch(a, kForward, "delta_steps", st);
+}
 cudaError_t launch_delta_steps_save(const DeltaArgs &a, cudaStream_t st) { return launch(a, kForwardSave, "delta_steps_save", st); }
 cudaError_t launch_delta_steps_bwd(const DeltaArgs &a, cudaStream_t st) { return launch(a, kBackward, "delta_steps_bwd", st); }
 
