@@ -1,16 +1,18 @@
 // The gated delta rule step by step (formulas in delta.cuh), forwards and backwards:
 // short runs, fp32 inputs and every size, and one kernel for a single token.
 //
-// The columns of H are independent of one another, so a lane has one column, all its rows
-// in registers for the whole sequence: k^T H and q^T H are sums inside a lane, and a step
-// needs neither shuffles nor barriers (with rows spread over eight lanes and three shuffles
-// a step, a step of 32 rows took 400 cycles). A step is one pass over the row pairs,
+// The columns of H are independent of one another. A column's rows are spread over LPC
+// lanes of a warp, in registers for the whole sequence, so k^T H and q^T H are a few sums
+// in a lane and log2(LPC) shuffles, and no barrier joins the warps but one every 8 steps.
+// A step is one pass over a lane's row pairs,
 //   H = a H + u k,  y += q H,  next e: d += k' H   (k' the next step's key),
-// four packed instructions a pair (fma.rn.f32x2 works on two rows). k and q come from
-// shared memory as broadcasts; four loader warps bring them there, with v, the decay and
-// beta, in fp32, a tile of 8 steps ahead, so one barrier joins the warps every 8 steps.
-// What bounds it: the chain of steps, one sequence's time being length x (issue of 64 to
-// 256 packed instructions + the latency of the last sums); the state moves once in and out.
+// four packed instructions a pair (fma.rn.f32x2 works on two rows); the shuffles of y wait
+// with those of the next step's d. k and q come from shared memory; loader warps bring
+// them there, with v, the decay and beta, in fp32, a tile of 8 steps ahead.
+// What bounds it: the chain of steps, each the latency of the sums, the shuffles and one
+// update. With a whole column of 32 rows a lane (no shuffles) a step took 460 cycles, with
+// eight lanes and four columns a lane 400: eight or sixteen rows a lane keep both the
+// issue and the shuffles short. The state moves once in and out.
 #include <algorithm>
 
 #include "delta.cuh"
@@ -20,9 +22,9 @@ namespace pdssm {
 namespace {
 
 constexpr int kTS = 8;  // steps a tile
-constexpr int kMaxWarps = PDSSM_MAX_P / 32;
-// One loader warp took 3,000 cycles for a tile, longer than the steps of 32 rows in it.
-constexpr int kLoaders = 4, kLS = kTS / kLoaders;
+constexpr int kMaxWarps = 8;     // computing warps of a block
+constexpr int kMaxCols = 64;     // their columns
+constexpr int kLoaders = 4, kLS = kTS / kLoaders;  // one loader alone took longer for a tile than its steps
 
 // One tile in shared memory: rows of k and q (padded with zeros to 32 J), of the
 // block's columns of v (or dy), and (a, beta).
@@ -49,7 +51,7 @@ struct Tile {
 // after the other.
 template <int J, typename T, typename G>
 struct Loader {
-  static constexpr int M = kMaxWarps;
+  static constexpr int M = kMaxCols / 32;
   const DeltaArgs &a;
   const T *k, *q, *c;
   const G *g, *beta;
@@ -113,48 +115,70 @@ struct Loader {
   }
 };
 
-// A column of a state [N][ld] at `p` (null: zeros) in row pairs.
-template <int R>
-__device__ __forceinline__ void load_column(pair2 (&x)[R], const float *p, int N, int64_t ld, bool in) {
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-    x[r] = pack2(p && in && 2 * r < N ? p[2 * r * ld] : 0.f, p && in && 2 * r + 1 < N ? p[(2 * r + 1) * ld] : 0.f);
-}
+// How a column's rows lie in LPC lanes: piece j of lane l has rows 4 (LPC j + l) .. + 3.
+template <int J>
+struct Rows {
+  static constexpr int LPC = J == 4 ? 8 : 4, kPieces = 32 * J / (4 * LPC), R = 2 * kPieces;  // R row pairs a lane
+  static constexpr int kCols = 32 / LPC;                                                     // columns a warp
+};
 
-template <int R>
-__device__ __forceinline__ void store_column(const pair2 (&x)[R], float *p, int N, int64_t ld) {
+// The lane's rows of a state column at `p` (null: zeros), row length ld.
+template <int J>
+__device__ __forceinline__ void load_column(pair2 (&x)[Rows<J>::R], const float *p, int l, int N, int64_t ld, bool in) {
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    float u, w;
-    unpack2(x[r], u, w);
-    if (2 * r < N) p[2 * r * ld] = u;
-    if (2 * r + 1 < N) p[(2 * r + 1) * ld] = w;
+  for (int j = 0; j < Rows<J>::kPieces; ++j) {
+    float v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int n = 4 * (Rows<J>::LPC * j + l) + r;
+      v[r] = p && in && n < N ? p[n * ld] : 0.f;
+    }
+    x[2 * j] = pack2(v[0], v[1]);
+    x[2 * j + 1] = pack2(v[2], v[3]);
   }
 }
 
-__device__ __forceinline__ float total(const pair2 (&s)[4]) {
-  float v[8];
+template <int J>
+__device__ __forceinline__ void store_column(const pair2 (&x)[Rows<J>::R], float *p, int l, int N, int64_t ld) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) unpack2(s[i], v[2 * i], v[2 * i + 1]);
-  return ((v[0] + v[2]) + (v[4] + v[6])) + ((v[1] + v[3]) + (v[5] + v[7]));
+  for (int j = 0; j < Rows<J>::kPieces; ++j) {
+    float v[4];
+    unpack2(x[2 * j], v[0], v[1]);
+    unpack2(x[2 * j + 1], v[2], v[3]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int n = 4 * (Rows<J>::LPC * j + l) + r;
+      if (n < N) p[n * ld] = v[r];
+    }
+  }
 }
 
-// Four rows of a vector in shared memory.
-__device__ __forceinline__ void two_pairs(const float *p, pair2 &x, pair2 &y) {
-  const float4 v = *reinterpret_cast<const float4 *>(p);
-  x = pack2(v.x, v.y);
-  y = pack2(v.z, v.w);
+// The lane's rows of a vector in shared memory.
+template <int J>
+__device__ __forceinline__ void load_rows(pair2 (&x)[Rows<J>::R], const float *p, int l) {
+#pragma unroll
+  for (int j = 0; j < Rows<J>::kPieces; ++j) {
+    const float4 v = *reinterpret_cast<const float4 *>(p + 4 * (Rows<J>::LPC * j + l));
+    x[2 * j] = pack2(v.x, v.y);
+    x[2 * j + 1] = pack2(v.z, v.w);
+  }
+}
+
+__device__ __forceinline__ float total(const pair2 (&s)[2]) {
+  float a, b, c, d;
+  unpack2(s[0], a, b);
+  unpack2(s[1], c, d);
+  return (a + c) + (b + d);
 }
 
 // grid: (column groups, heads, batch); warps 0 .. warps - 1 compute, the others load.
 // SAVE: writes e_t and, every a.C steps, the state before them (for the backward pass).
 template <int J, typename T, typename G, bool SAVE>
 __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_kernel(DeltaArgs a) {
-  constexpr int R = 16 * J, kRow = 32 * J;
-  constexpr bool kKeep = J <= 2;  // a step's key stays in registers from the pass before
+  constexpr int R = Rows<J>::R, LPC = Rows<J>::LPC, kRow = 32 * J;
   extern __shared__ __align__(16) float smem[];
   const int warps = blockDim.x / 32 - kLoaders, warp = threadIdx.x >> 5;
-  const int cols = warps * 32, p0 = blockIdx.x * cols;
+  const int cols = warps * Rows<J>::kCols, p0 = blockIdx.x * cols;
   const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.H + h;
   const int64_t len = live_steps(a.lengths, b, a.L);
   if (warp >= warps) {
@@ -170,101 +194,92 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_kerne
     }
     return;
   }
-  const int col = p0 + threadIdx.x, N = (int)a.N;
+  const int c = threadIdx.x / LPC, l = threadIdx.x % LPC, col = p0 + c, N = (int)a.N;
   const bool in = col < a.P, room = col < a.Pp;
-  pair2 st[R];
-  load_column<R>(st, a.h0 ? a.h0 + bh * a.N * a.P + col : nullptr, N, a.P, in);
+  pair2 st[R], k[R], d[2] = {}, z[2] = {};
+  load_column<J>(st, a.h0 ? a.h0 + bh * a.N * a.P + col : nullptr, l, N, a.P, in);
   __syncthreads();
   T *y = static_cast<T *>(a.y) + (b * a.L * a.H + h) * a.P + col;
   float *e_out = SAVE ? a.e + (b * a.L * a.H + h) * a.Pp + col : nullptr;
   const int64_t step = a.H * (SAVE ? a.Pp : a.P);
-  pair2 d[4] = {}, k[kKeep ? R : 2];
-  const auto first_key = [&](const float *ks) {
+  if (len > 0) {
+    load_rows<J>(k, Tile<J>(smem, cols, 0).k, l);
 #pragma unroll
-    for (int r = 0; r < R; r += 2) {
-      pair2 k0, k1;
-      two_pairs(ks + 2 * r, k0, k1);
-      d[r & 3] = fma2(k0, st[r], d[r & 3]);
-      d[(r + 1) & 3] = fma2(k1, st[r + 1], d[(r + 1) & 3]);
-      if (kKeep) {
-        k[r % (kKeep ? R : 2)] = k0;
-        k[(r + 1) % (kKeep ? R : 2)] = k1;
-      }
-    }
-  };
-  if (len > 0) first_key(Tile<J>(smem, cols, 0).k);
-  for (int64_t t0 = 0, i = 0; t0 < len; t0 += kTS, ++i) {
-    const int n = (int)min((int64_t)kTS, len - t0);
-    const Tile<J> tile(smem, cols, i & 1), after(smem, cols, (i + 1) & 1);
-    for (int s = 0; s < n; ++s) {
-      if (SAVE && room && ((t0 + s) & (a.C - 1)) == 0)
-        store_column<R>(st, a.carry + (bh * a.nC + (t0 + s) / a.C) * a.N * a.Pp + col, N, a.Pp);
+    for (int r = 0; r < R; ++r) d[r & 1] = fma2(k[r], st[r], r < 2 ? 0 : d[r & 1]);
+  }
+  const bool writes = l == 0 && (SAVE ? room : in);
+  int buf = 0;
+  for (int64_t t0 = 0; t0 < len; t0 += kTS, buf ^= 1) {
+    const Tile<J> tile(smem, cols, buf), after(smem, cols, buf ^ 1);
+    if (SAVE && room && (t0 & (a.C - 1)) == 0)  // a.C is a multiple of kTS
+      store_column<J>(st, a.carry + (bh * a.nC + t0 / a.C) * a.N * a.Pp + col, l, N, a.Pp);
+    const float *kl = tile.k + 4 * l, *ql = tile.q + 4 * l, *cl = tile.c + c;
+    // everything a step reads comes ahead of the shuffles that it waits for
+    const auto one = [&](int s, bool last, bool has_y) {
       const float2 ab = tile.ab[s];
-      const float e = fmaf(-ab.x, total(d), tile.c[s * cols + threadIdx.x]);
-      const float u = ab.y * e;
-      const pair2 aa = pack2(ab.x, ab.x), uu = pack2(u, u);
-      if (SAVE && room) {
-        *e_out = e;
-        e_out += step;
+      const float v = cl[s * cols];
+      pair2 q[R], next[R];
+      if (!SAVE) load_rows<J>(q, ql + s * kRow, 0);
+      if (last) {  // the next step's key is in the next tile, if there is one
+        __syncthreads();
+        load_rows<J>(next, after.k, l);
+      } else {
+        load_rows<J>(next, kl + (s + 1) * kRow, 0);
       }
-      // the next step's key, where the tile has it; the next tile's first is read behind the barrier
-      const float *qs = tile.q + s * kRow, *ks = tile.k + s * kRow;
-      pair2 z[4] = {};
+      float kh = total(d), out = SAVE ? 0.f : total(z);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) d[r] = 0;
-      const auto pass = [&](bool next) {
+      for (int o = 1; o < LPC; o <<= 1) {
+        kh += __shfl_xor_sync(0xffffffffu, kh, o);
+        if (!SAVE) out += __shfl_xor_sync(0xffffffffu, out, o);
+      }
+      const float e = fmaf(-ab.x, kh, v), u = ab.y * e;
+      const pair2 aa = pack2(ab.x, ab.x), uu = pack2(u, u);
 #pragma unroll
-        for (int r = 0; r < R; r += 2) {
-          pair2 q0, q1, k0, k1, n0, n1;
-          if (kKeep) {
-            k0 = k[r % (kKeep ? R : 2)];
-            k1 = k[(r + 1) % (kKeep ? R : 2)];
-          } else {
-            two_pairs(ks + 2 * r, k0, k1);
-          }
-          st[r] = fma2(k0, uu, mul2(aa, st[r]));
-          st[r + 1] = fma2(k1, uu, mul2(aa, st[r + 1]));
-          if (!SAVE) {
-            two_pairs(qs + 2 * r, q0, q1);
-            z[r & 3] = fma2(q0, st[r], z[r & 3]);
-            z[(r + 1) & 3] = fma2(q1, st[r + 1], z[(r + 1) & 3]);
-          }
-          if (next) {
-            two_pairs(ks + kRow + 2 * r, n0, n1);
-            d[r & 3] = fma2(n0, st[r], d[r & 3]);
-            d[(r + 1) & 3] = fma2(n1, st[r + 1], d[(r + 1) & 3]);
-            if (kKeep) {
-              k[r % (kKeep ? R : 2)] = n0;
-              k[(r + 1) % (kKeep ? R : 2)] = n1;
-            }
-          }
-        }
-      };
-      if (s + 1 < n) pass(true);
-      else pass(false);
-      if (!SAVE) {
-        if (in) st_out(y, total(z));
+      for (int r = 0; r < R; ++r) {
+        st[r] = fma2(k[r], uu, mul2(aa, st[r]));
+        d[r & 1] = fma2(next[r], st[r], r < 2 ? 0 : d[r & 1]);
+        if (!SAVE) z[r & 1] = fma2(q[r], st[r], r < 2 ? 0 : z[r & 1]);
+        k[r] = next[r];
+      }
+      if (SAVE) {
+        if (writes) *e_out = e;
+        e_out += step;
+      } else if (has_y) {  // the step before's y
+        if (writes) st_out(y, out);
         y += step;
       }
+    };
+    if (len - t0 >= kTS) {
+      one(0, false, t0 > 0);
+#pragma unroll
+      for (int s = 1; s < kTS; ++s) one(s, s == kTS - 1, true);
+    } else {
+      const int n = (int)(len - t0);
+      for (int s = 0; s < n; ++s) one(s, s + 1 == n, t0 + s > 0);
     }
-    __syncthreads();
-    if (t0 + kTS < len) first_key(after.k);
   }
-  if (!SAVE && in) {
-    for (int64_t t = len; t < a.L; ++t, y += step) st_out(y, 0.f);
-    if (a.h_final) store_column<R>(st, a.h_final + bh * a.N * a.P + col, N, a.P);
+  if (SAVE) return;
+  if (len > 0) {
+    float out = total(z);
+#pragma unroll
+    for (int o = 1; o < LPC; o <<= 1) out += __shfl_xor_sync(0xffffffffu, out, o);
+    if (l == 0 && in) st_out(y, out);
+    y += step;
   }
+  if (!in) return;
+  for (int64_t t = len + l; t < a.L; t += LPC) st_out(y + (t - len) * step, 0.f);
+  if (a.h_final) store_column<J>(st, a.h_final + bh * a.N * a.P + col, l, N, a.P);
 }
 
 // The adjoint X runs from the last step to the first; writes dv_t, du_t, X at the end
-// of each chunk of a.C steps, and dh0. A step is one pass over the row pairs:
-//   X = a (X - w k) of the step behind, X += dy q, du += k X.
+// of each chunk of a.C steps, and dh0. A step is
+//   X += dy q,  du = k X (sums and shuffles),  X = a (X - w k).
 template <int J, typename T, typename G>
 __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_bwd_kernel(DeltaArgs a) {
-  constexpr int R = 16 * J, kRow = 32 * J;
+  constexpr int R = Rows<J>::R, LPC = Rows<J>::LPC, kRow = 32 * J;
   extern __shared__ __align__(16) float smem[];
   const int warps = blockDim.x / 32 - kLoaders, warp = threadIdx.x >> 5;
-  const int cols = warps * 32, p0 = blockIdx.x * cols;
+  const int cols = warps * Rows<J>::kCols, p0 = blockIdx.x * cols;
   const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.H + h;
   const int64_t len = live_steps(a.lengths, b, a.L);
   const int64_t tiles = (len + kTS - 1) / kTS;
@@ -285,53 +300,78 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_bwd_k
     }
     return;
   }
-  const int col = p0 + threadIdx.x, N = (int)a.N;
+  const int c = threadIdx.x / LPC, l = threadIdx.x % LPC, col = p0 + c, N = (int)a.N;
   const bool in = col < a.P, room = col < a.Pp;
   pair2 x[R];
-  load_column<R>(x, a.dh_final ? a.dh_final + bh * a.N * a.P + col : nullptr, N, a.P, in);
+  load_column<J>(x, a.dh_final ? a.dh_final + bh * a.N * a.P + col : nullptr, l, N, a.P, in);
   __syncthreads();
   T *dv = static_cast<T *>(a.dv) + (b * a.L * a.H + h) * a.P + col;
   float *du_out = a.du + (b * a.L * a.H + h) * a.Pp + col;
-  for (int64_t i = 0; i < tiles; ++i) {
+  pair2 k[R], q[R];
+  if (tiles > 0) {
+    const Tile<J> tile(smem, cols, 0);
+    const int s = (int)(len - (tiles - 1) * kTS) - 1;
+    load_rows<J>(k, tile.k + s * kRow, l);
+    load_rows<J>(q, tile.q + s * kRow, l);
+  }
+  const bool writes_du = l == 0 && room, writes_dv = l == 0 && in;
+  const int64_t step_du = a.H * a.Pp, step_dv = a.H * a.P;
+  T *dv_at = dv + (len - 1) * step_dv;
+  du_out += (len - 1) * step_du;
+  int buf = 0;
+  for (int64_t i = 0; i < tiles; ++i, buf ^= 1) {
     const int64_t t0 = (tiles - 1 - i) * kTS;
-    const Tile<J> tile(smem, cols, i & 1);
-    const int n = (int)min((int64_t)kTS, len - t0);
-    for (int s = n - 1; s >= 0; --s) {
-      const int64_t t = t0 + s;
-      if (room && (t == len - 1 || ((t + 1) & (a.C - 1)) == 0))
-        store_column<R>(x, a.xcarry + (bh * a.nC + t / a.C) * a.N * a.Pp + col, N, a.Pp);
+    const Tile<J> tile(smem, cols, buf), before(smem, cols, buf ^ 1);
+    if (room && (i == 0 || ((t0 + kTS) & (a.C - 1)) == 0))  // a.C is a multiple of kTS
+      store_column<J>(x, a.xcarry + (bh * a.nC + t0 / a.C) * a.N * a.Pp + col, l, N, a.Pp);
+    const float *kl = tile.k + 4 * l, *ql = tile.q + 4 * l, *cl = tile.c + c;
+    const auto one = [&](int s) {
       const float2 ab = tile.ab[s];
-      const float dy = tile.c[s * cols + threadIdx.x];
-      const pair2 dd = pack2(dy, dy), aa = pack2(ab.x, ab.x);
-      const float *ks = tile.k + s * kRow, *qs = tile.q + s * kRow;
-      pair2 sum[4] = {};
-#pragma unroll
-      for (int r = 0; r < R; r += 2) {
-        pair2 q0, q1, k0, k1;
-        two_pairs(qs + 2 * r, q0, q1);
-        two_pairs(ks + 2 * r, k0, k1);
-        x[r] = fma2(q0, dd, x[r]);
-        x[r + 1] = fma2(q1, dd, x[r + 1]);
-        sum[r & 3] = fma2(k0, x[r], sum[r & 3]);
-        sum[(r + 1) & 3] = fma2(k1, x[r + 1], sum[(r + 1) & 3]);
+      const float dy = cl[s * cols];
+      // the key and query of the step before, ahead of the shuffles
+      pair2 kn[R], qn[R];
+      if (s == 0) {  // it is in the tile before, if there is one
+        __syncthreads();
+        load_rows<J>(kn, before.k + (kTS - 1) * kRow, l);
+        load_rows<J>(qn, before.q + (kTS - 1) * kRow, l);
+      } else {
+        load_rows<J>(kn, kl + (s - 1) * kRow, 0);
+        load_rows<J>(qn, ql + (s - 1) * kRow, 0);
       }
-      const float du = total(sum), w = ab.y * du;
+      const pair2 dd = pack2(dy, dy), aa = pack2(ab.x, ab.x);
+      pair2 sum[2];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        x[r] = fma2(q[r], dd, x[r]);
+        sum[r & 1] = fma2(k[r], x[r], r < 2 ? 0 : sum[r & 1]);
+      }
+      float du = total(sum);
+#pragma unroll
+      for (int o = 1; o < LPC; o <<= 1) du += __shfl_xor_sync(0xffffffffu, du, o);
+      const float w = ab.y * du;
       const pair2 ww = pack2(-w, -w);
 #pragma unroll
-      for (int r = 0; r < R; r += 2) {
-        pair2 k0, k1;
-        two_pairs(ks + 2 * r, k0, k1);
-        x[r] = mul2(aa, fma2(k0, ww, x[r]));
-        x[r + 1] = mul2(aa, fma2(k1, ww, x[r + 1]));
+      for (int r = 0; r < R; ++r) {
+        x[r] = mul2(aa, fma2(k[r], ww, x[r]));
+        k[r] = kn[r];
+        q[r] = qn[r];
       }
-      if (room) du_out[t * a.H * a.Pp] = du;
-      if (in) st_out(dv + t * a.H * a.P, w);
+      if (writes_du) *du_out = du;
+      if (writes_dv) st_out(dv_at, w);
+      du_out -= step_du;
+      dv_at -= step_dv;
+    };
+    const int64_t n = len - t0;
+    if (n >= kTS) {
+#pragma unroll
+      for (int s = kTS - 1; s >= 0; --s) one(s);
+    } else {
+      for (int s = (int)n - 1; s >= 0; --s) one(s);
     }
-    __syncthreads();
   }
   if (!in) return;
-  for (int64_t t = len; t < a.L; ++t) st_out(dv + t * a.H * a.P, 0.f);
-  if (a.dh0) store_column<R>(x, a.dh0 + bh * a.N * a.P + col, N, a.P);
+  for (int64_t t = len + l; t < a.L; t += LPC) st_out(dv + t * a.H * a.P, 0.f);
+  if (a.dh0) store_column<J>(x, a.dh0 + bh * a.N * a.P + col, l, N, a.P);
 }
 
 // ------------------------------------------------------------------ one token
@@ -439,13 +479,14 @@ cudaError_t launch_jtg(const DeltaArgs &a, Which which, cudaStream_t st) {
     delta_token_kernel<J, T, G><<<dim3((unsigned)((groups + warps - 1) / warps), (unsigned)a.H, (unsigned)a.Bt), 32 * warps, 0, st>>>(a);
     return cudaGetLastError();
   }
-  // all columns of a head in one block share its loaded tiles; with few sequences each
-  // warp is a block of its own
-  int warps = (int)((a.P + 31) / 32);
-  const int all = warps;
-  if (a.Bt * a.H * all <= 148) warps = 1;
+  // up to 8 warps share a block's loaded tiles; with few sequences the columns are spread
+  // over more blocks, down to 2 warps, until there is one an SM
+  constexpr int kCols = Rows<J>::kCols;
+  const int all = (int)((a.P + kCols - 1) / kCols);
+  int warps = std::min(all, kMaxWarps);
+  while (warps > 2 && a.Bt * a.H * ((all + warps - 1) / warps) < 148) warps = (warps + 1) / 2;
   const dim3 grid((unsigned)((all + warps - 1) / warps), (unsigned)a.H, (unsigned)a.Bt);
-  const size_t smem = Tile<J>::bytes(warps * 32);
+  const size_t smem = Tile<J>::bytes(warps * kCols);
   auto kern = which == kForward ? delta_steps_kernel<J, T, G, false>
                                 : which == kForwardSave ? delta_steps_kernel<J, T, G, true> : delta_steps_bwd_kernel<J, T, G>;
   kern<<<grid, 32 * (warps + kLoaders), smem, st>>>(a);
