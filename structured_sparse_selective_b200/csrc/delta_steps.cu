@@ -24,7 +24,7 @@ namespace {
 constexpr int kTS = 8;  // steps a tile
 constexpr int kMaxWarps = 8;     // computing warps of a block
 constexpr int kMaxCols = 64;     // their columns
-constexpr int kLoaders = 4, kLS = kTS / kLoaders;  // one loader alone took longer for a tile than its steps
+constexpr int kLoaders = 4;      // loader w has the tiles w, w + 4, ...
 
 // One tile in shared memory: rows of k and q (padded with zeros to 32 J), of the
 // block's columns of v (or dy), and (a, beta).
@@ -44,9 +44,9 @@ struct Tile {
   static size_t bytes(int cols) { return (size_t)2 * kTS * (2 * kRow + cols + 2) * 4; }
 };
 
-// A loader warp, with kLS steps of each tile. A tile's values wait in registers while the tile before is computed:
-// fetch() starts the loads of one tile, put() writes them to shared memory a tile later,
-// so HBM's latency is behind a whole tile's work. The loads are unconditional, from a
+// A loader warp, with every fourth tile. A tile's values wait in registers: fetch() starts
+// its loads four tiles ahead, put() writes them to shared memory, so HBM's latency (about
+// 1,400 cycles, as long as 9 steps of 32 rows) is behind four tiles' work. The loads are unconditional, from a
 // valid place where there is nothing to load: with a branch around each they ran one
 // after the other.
 template <int J, typename T, typename G>
@@ -55,14 +55,14 @@ struct Loader {
   const DeltaArgs &a;
   const T *k, *q, *c;
   const G *g, *beta;
-  int lane, first, p0, cols, n;  // first: the warp's first step of a tile
+  int lane, p0, cols, n;
   int64_t rowk, rowc;
-  T kv[kLS][J], qv[kLS][J], cv[kLS][M];
+  T kv[kTS][J], qv[kTS][J], cv[kTS][M];
   G gv, bv;
 
   // `src`: v forwards, dy backwards.
-  __device__ Loader(const DeltaArgs &a_, int64_t b, int64_t h, int who, int p0_, int cols_, const void *src)
-      : a(a_), lane(threadIdx.x & 31), first(who * kLS), p0(p0_), cols(cols_), n(0), rowk(a_.Hk * a_.N), rowc(a_.H * a_.P) {
+  __device__ Loader(const DeltaArgs &a_, int64_t b, int64_t h, int p0_, int cols_, const void *src)
+      : a(a_), lane(threadIdx.x & 31), p0(p0_), cols(cols_), n(0), rowk(a_.Hk * a_.N), rowc(a_.H * a_.P) {
     const int64_t hk = h / (a.H / a.Hk);
     k = static_cast<const T *>(a.k) + b * a.L * rowk + hk * a.N;
     q = static_cast<const T *>(a.q) + b * a.L * rowk + hk * a.N;
@@ -76,8 +76,8 @@ struct Loader {
     n = (int)(steps < kTS ? steps : kTS);
     if (n <= 0) return;
 #pragma unroll
-    for (int s = 0; s < kLS; ++s) {
-      const int64_t t = t0 + min(first + s, n - 1);
+    for (int s = 0; s < kTS; ++s) {
+      const int64_t t = t0 + min(s, n - 1);
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const int i = min(lane + 32 * j, (int)a.N - 1);
@@ -87,33 +87,48 @@ struct Loader {
 #pragma unroll
       for (int j = 0; j < M; ++j) cv[s][j] = c[t * rowc + min(p0 + min(lane + 32 * j, cols - 1), (int)a.P - 1)];
     }
-    if (first == 0) {
-      const int64_t t = (t0 + min(lane, n - 1)) * a.H;
-      gv = g[t];
-      bv = beta[t];
-    }
+    const int64_t t = (t0 + min(lane, n - 1)) * a.H;
+    gv = g[t];
+    bv = beta[t];
   }
 
   __device__ __forceinline__ void put(const Tile<J> &tile) {
     if (n <= 0) return;
 #pragma unroll
-    for (int s = 0; s < kLS; ++s) {
-      const int at = first + s;
+    for (int s = 0; s < kTS; ++s) {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const int i = lane + 32 * j;
-        tile.k[at * 32 * J + i] = i < a.N ? to_f32(kv[s][j]) : 0.f;
-        tile.q[at * 32 * J + i] = i < a.N ? to_f32(qv[s][j]) * a.scale : 0.f;
+        tile.k[s * 32 * J + i] = i < a.N ? to_f32(kv[s][j]) : 0.f;
+        tile.q[s * 32 * J + i] = i < a.N ? to_f32(qv[s][j]) * a.scale : 0.f;
       }
 #pragma unroll
       for (int j = 0; j < M; ++j) {
         const int i = lane + 32 * j;
-        if (i < cols) tile.c[at * cols + i] = p0 + i < a.P ? to_f32(cv[s][j]) : 0.f;
+        if (i < cols) tile.c[s * cols + i] = p0 + i < a.P ? to_f32(cv[s][j]) : 0.f;
       }
     }
-    if (first == 0 && lane < kTS) tile.ab[lane] = make_float2(expf(clamp_gate(to_f32(gv))), to_f32(bv));
+    if (lane < kTS) tile.ab[lane] = make_float2(expf(clamp_gate(to_f32(gv))), to_f32(bv));
   }
 };
+
+// Loader `who` through the tiles: tile i + 1 goes into its buffer while tile i is computed.
+template <int J, typename In, typename Fetch>
+__device__ __forceinline__ void run_loader(In &in, int who, int64_t tiles, float *smem, int cols, const Fetch &fetch) {
+  fetch(who);
+  if (who == 0) {
+    in.put(Tile<J>(smem, cols, 0));
+    fetch(kLoaders);
+  }
+  __syncthreads();
+  for (int64_t i = 0; i < tiles; ++i) {
+    if (((i + 1) & (kLoaders - 1)) == who) {
+      in.put(Tile<J>(smem, cols, (i + 1) & 1));
+      fetch(i + 1 + kLoaders);
+    }
+    __syncthreads();
+  }
+}
 
 // How a column's rows lie in LPC lanes: piece j of lane l has rows 4 (LPC j + l) .. + 3.
 template <int J>
@@ -182,16 +197,8 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_kerne
   const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.H + h;
   const int64_t len = live_steps(a.lengths, b, a.L);
   if (warp >= warps) {
-    Loader<J, T, G> in(a, b, h, warp - warps, p0, cols, a.v);
-    in.fetch(0, len);
-    in.put(Tile<J>(smem, cols, 0));
-    in.fetch(kTS, len - kTS);
-    __syncthreads();
-    for (int64_t t0 = 0, i = 0; t0 < len; t0 += kTS, ++i) {
-      in.put(Tile<J>(smem, cols, (i + 1) & 1));
-      in.fetch(t0 + 2 * kTS, len - t0 - 2 * kTS);
-      __syncthreads();
-    }
+    Loader<J, T, G> in(a, b, h, p0, cols, a.v);
+    run_loader<J>(in, warp - warps, (len + kTS - 1) / kTS, smem, cols, [&](int64_t i) { in.fetch(i * kTS, len - i * kTS); });
     return;
   }
   const int c = threadIdx.x / LPC, l = threadIdx.x % LPC, col = p0 + c, N = (int)a.N;
@@ -284,20 +291,11 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_bwd_k
   const int64_t len = live_steps(a.lengths, b, a.L);
   const int64_t tiles = (len + kTS - 1) / kTS;
   if (warp >= warps) {
-    Loader<J, T, G> in(a, b, h, warp - warps, p0, cols, a.dy);
-    const auto fetch = [&](int64_t i) {  // the i-th tile from the end; nothing behind the first
+    Loader<J, T, G> in(a, b, h, p0, cols, a.dy);
+    run_loader<J>(in, warp - warps, tiles, smem, cols, [&](int64_t i) {  // tiles from the last to the first
       const int64_t t0 = (tiles - 1 - i) * kTS;
       in.fetch(t0, i < tiles ? len - t0 : 0);
-    };
-    fetch(0);
-    in.put(Tile<J>(smem, cols, 0));
-    fetch(1);
-    __syncthreads();
-    for (int64_t i = 0; i < tiles; ++i) {
-      in.put(Tile<J>(smem, cols, (i + 1) & 1));
-      fetch(i + 2);
-      __syncthreads();
-    }
+    });
     return;
   }
   const int c = threadIdx.x / LPC, l = threadIdx.x % LPC, col = p0 + c, N = (int)a.N;
