@@ -8,12 +8,13 @@
 // and backwards, with d = dy turned by the negative angles:
 //   dw += d x r;  dx = r (d w - x r * share * sum_i d_i w_i x_i r)
 //
-// What bounds it: HBM. Each value is read once and written once (backward: x and
-// dy read, dx written); the arithmetic is a few operations a value. A head is held
-// by a group of 2^g lanes in 16-byte (or 8-byte) pieces, so the sum is a shuffle
-// reduction inside the group and a pair's partner is in the same lane or a fixed
-// number of lanes away; heads whose size, rotated width or alignment do not allow
-// that take the one-value-a-lane path with the partner read through shared memory.
+// What bounds it: HBM and the issue rate, both near. Each value is read once and written
+// once (backward: x and dy read, dx written). A head is held by a group of 2^g lanes, two
+// pieces of four values a lane: a piece of the first rotated half and its partner in the
+// second, so a pair turns inside a lane (with one 16-byte piece a lane and the partner by
+// shuffles the LM layer took 80 us, issue-bound). Heads whose size, rotated width or
+// alignment do not allow pieces take the one-value-a-lane path with the partner read
+// through shared memory.
 // The angles are the same for all heads of a token: a block computes them once for
 // its tile of tokens. Their product and reduction to [-pi, pi] are in double
 // precision, since at position 10^6 a float's angle is off by 0.03.
@@ -27,50 +28,40 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTile = 8;   // tokens a tile
-constexpr int kUnroll = 4;    // heads in flight per lane group
+constexpr int kBlocks = 148 * 2;  // of q and of k each: together four of 256 threads an SM
 
-template <typename T, int VEC>
-struct Piece;  // VEC values moved as one access
-template <>
-struct Piece<float, 4> { using V = float4; };
-template <>
-struct Piece<float, 2> { using V = float2; };
-template <>
-struct Piece<float, 1> { using V = float; };
-template <>
-struct Piece<__nv_bfloat16, 8> { using V = uint4; };
-template <>
-struct Piece<__nv_bfloat16, 4> { using V = uint2; };
-template <>
-struct Piece<__nv_bfloat16, 1> { using V = __nv_bfloat16; };
+enum Turn { kNone, kHalves, kNeighbours };
 
-template <typename T, int VEC>
-__device__ __forceinline__ void load_piece(const T *p, float *v) {
-  union { typename Piece<T, VEC>::V raw; T e[VEC]; } u;
-  u.raw = *reinterpret_cast<const typename Piece<T, VEC>::V *>(p);
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) v[i] = to_f32(u.e[i]);
+// Four values moved as one access.
+__device__ __forceinline__ void load4(const float *p, float *v) {
+  const float4 x = *reinterpret_cast<const float4 *>(p);
+  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
 }
-
-__device__ __forceinline__ void put(float &o, float v) { o = v; }
-__device__ __forceinline__ void put(__nv_bfloat16 &o, float v) { o = __float2bfloat16_rn(v); }
-
-template <typename T, int VEC>
-__device__ __forceinline__ void store_piece(T *p, const float *v) {
-  union U { typename Piece<T, VEC>::V raw; T e[VEC]; __device__ U() {} } u;
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) put(u.e[i], v[i]);
-  *reinterpret_cast<typename Piece<T, VEC>::V *>(p) = u.raw;
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float *v) {
+  const uint2 x = *reinterpret_cast<const uint2 *>(p);
+  v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xffff0000u);
+  v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(float *p, const float *v) {
+  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float *v) {
+  union { uint2 raw; __nv_bfloat162 h[2]; } u;
+  u.h[0] = __floats2bfloat162_rn(v[0], v[1]);
+  u.h[1] = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2 *>(p) = u.raw;
 }
 
 // cos and sin of position * f, the product reduced by whole turns in double.
-__device__ __forceinline__ float2 angle(int position, float f) {
+// `coarse`: by the hardware's sine and cosine, off by up to 2^-21 (results rounded to bf16).
+__device__ __forceinline__ float2 angle(int position, float f, bool coarse) {
   const double a = (double)position * (double)f;
   const double turns = rint(a * 0.15915494309189535);
   double r = fma(turns, -6.283185307179586, a);
   r = fma(turns, -2.4492935982947064e-16, r);
   float s, c;
-  sincosf((float)r, &s, &c);
+  if (coarse) __sincosf((float)r, &s, &c);
+  else sincosf((float)r, &s, &c);
   return make_float2(c, s);
 }
 
@@ -88,47 +79,21 @@ struct Args {
 };
 
 // The angles of tokens [t0, t0 + nt) into tab[token][rot / 2].
-__device__ __forceinline__ void fill_angles(const Args &a, int64_t t0, int nt, float2 *tab) {
+__device__ __forceinline__ void fill_angles(const Args &a, int64_t t0, int nt, float2 *tab, bool coarse) {
   const int h = a.rot / 2;
   for (int i = threadIdx.x; i < nt * h; i += kThreads) {
     const int t = i / h, j = i - t * h;
     const int64_t row = t0 + t;
     const int pos = a.positions ? a.positions[row] : (int)(row % a.seqlen);
-    tab[i] = angle(pos, a.inv_freq[j]);
+    tab[i] = angle(pos, a.inv_freq[j], coarse);
   }
 }
 
-// Turns the lane's piece. Values [i0, i0 + VEC) of the head; `sign` -1 turns back.
-// VEC > 1: partners are in the lane (interleaved) or rot / 2 / VEC lanes away.
-template <int VEC, int LANES>
-__device__ __forceinline__ void turn_piece(float *v, int i0, const Args &a, const float2 *tab, float sign) {
-  const int h = a.rot / 2;
-  if (a.interleaved) {
-    if (i0 < a.rot) {
-#pragma unroll
-      for (int e = 0; e + 1 < VEC; e += 2) {
-        if (i0 + e < a.rot) {
-          const float2 cs = tab[(i0 + e) >> 1];
-          const float s = sign * cs.y, p = v[e], q = v[e + 1];
-          v[e] = p * cs.x - q * s;
-          v[e + 1] = q * cs.x + p * s;
-        }
-      }
-    }
-  } else {
-    const bool low = i0 < h, in = i0 < a.rot;
-    const int lane = threadIdx.x & 31, away = h / VEC;
-    const int src = !in ? lane : low ? lane + away : lane - away;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const float o = __shfl_sync(0xffffffffu, v[e], src);
-      if (in) {
-        const float2 cs = tab[low ? i0 + e : i0 + e - h];
-        const float s = sign * cs.y;
-        v[e] = low ? v[e] * cs.x - o * s : v[e] * cs.x + o * s;
-      }
-    }
-  }
+// 1 / sqrt(s): the hardware's, one Newton step nearer (without it, a head of one value, whose
+// gradient is a difference of nearly equal terms, is off by more than fp32's rounding).
+__device__ __forceinline__ float inverse_sqrt(float s) {
+  const float r = rsqrtf(s), e = fmaf(-s * r, r, 1.f);
+  return s > 0.f && s < INFINITY ? fmaf(0.5f * r, e, r) : r;
 }
 
 template <int LANES>
@@ -138,99 +103,135 @@ __device__ __forceinline__ float group_sum(float s) {
   return s;
 }
 
-// LANES lanes hold one head in pieces of VEC values. blockIdx.y: 0 = q, 1 = k.
-// kUnroll heads of a lane group are in flight at once: one load a lane and 2,048
-// threads an SM are about the 35 KB that HBM's latency needs, and the table's
-// barriers leave gaps, so several are taken.
-template <typename T, int VEC, int LANES, bool BWD>
-__global__ void __launch_bounds__(kThreads) qk_piece_kernel(Args a) {
-  extern __shared__ float2 tab[];
-  const int which = blockIdx.y, H = a.heads[which];
-  const T *x = static_cast<const T *>(a.x[which]);
-  const T *dy = static_cast<const T *>(a.dy[which]);
-  T *out = static_cast<T *>(a.out[which]);
-  const float *w = a.w[which];
-  constexpr int kGroups = kThreads / LANES;
-  const int group = threadIdx.x / LANES, gl = threadIdx.x % LANES, i0 = gl * VEC;
-  const bool in = i0 < a.N;
-  const int half = a.rot / 2;
-  float wv[VEC], dw[VEC];
+// Turns the lane's two pieces, values [ia, ia + 4) and [ib, ib + 4) of the head, by the
+// token's angles; `sign` -1 turns back.
+template <int TURN>
+__device__ __forceinline__ void turn_pieces(float (&v)[8], int ia, int ib, int rot, const float2 *tab, float sign) {
+  const auto pair = [&](float &x, float &y, float c, float s) {
+    const float p = x, q = y;
+    s *= sign;
+    x = p * c - q * s;
+    y = q * c + p * s;
+  };
+  if (TURN == kHalves) {
+    if (ia < rot) {  // then the second piece is the first's partner
+      const float4 t0 = *reinterpret_cast<const float4 *>(tab + ia), t1 = *reinterpret_cast<const float4 *>(tab + ia + 2);
+      pair(v[0], v[4], t0.x, t0.y);
+      pair(v[1], v[5], t0.z, t0.w);
+      pair(v[2], v[6], t1.x, t1.y);
+      pair(v[3], v[7], t1.z, t1.w);
+    }
+  } else if (TURN == kNeighbours) {
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    wv[e] = (w && in) ? w[i0 + e] : 1.f;
+    for (int s = 0; s < 2; ++s) {
+      const int i = s ? ib : ia;
+      if (i < rot) pair(v[4 * s], v[4 * s + 1], tab[i >> 1].x, tab[i >> 1].y);
+      if (i + 2 < rot) pair(v[4 * s + 2], v[4 * s + 3], tab[(i >> 1) + 1].x, tab[(i >> 1) + 1].y);
+    }
+  }
+}
+
+// LANES lanes hold one head, two pieces of four values a lane; blockIdx.y: 0 = q, 1 = k.
+// U heads of a lane group are in flight at once, so that their loads cover HBM's latency.
+template <typename T, int LANES, int TURN, bool BWD>
+__global__ void __launch_bounds__(kThreads, 4) qk_piece_kernel(Args a) {
+  extern __shared__ __align__(16) float2 tab[];
+  constexpr int U = BWD ? 2 : 4, kGroups = kThreads / LANES;
+  constexpr bool kCoarse = sizeof(T) == 2;
+  const int which = blockIdx.y, H = a.heads[which], N = a.N, half = a.rot / 2;
+  const int group = threadIdx.x / LANES, gl = threadIdx.x % LANES;
+  // the lane's pieces: partners first, then what does not turn
+  const int pairs = TURN == kHalves ? half / 4 : 0;
+  const int ia = gl < pairs ? 4 * gl : 4 * (2 * gl), ib = gl < pairs ? ia + half : ia + 4;
+  const bool ina = ia < N, inb = ib < N;
+  const unsigned per_head = H > 1 ? 0xffffffffu / (unsigned)H + 1 : 0;  // item / H as a product (items < 2^16)
+  float wv[8], dw[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int i = e < 4 ? ia + e : ib + e - 4;
+    wv[e] = a.w[which] && i < N ? a.w[which][i] : 1.f;
     dw[e] = 0.f;
   }
   for (int64_t t0 = (int64_t)blockIdx.x * a.tile; t0 < a.rows; t0 += (int64_t)gridDim.x * a.tile) {
     const int nt = (int)(a.rows - t0 < a.tile ? a.rows - t0 : a.tile);
-    if (half) {
+    if (TURN != kNone) {
       __syncthreads();
-      fill_angles(a, t0, nt, tab);
+      fill_angles(a, t0, nt, tab, kCoarse);
       __syncthreads();
     }
     const int items = nt * H;
+    const T *x = static_cast<const T *>(a.x[which]) + t0 * H * N;
+    const T *dy = static_cast<const T *>(a.dy[which]) + (BWD ? t0 * H * N : 0);
+    T *out = static_cast<T *>(a.out[which]) + t0 * H * N;
     // every lane of a warp takes part in each shuffle: the loop bound is the block's
-    for (int it0 = 0; it0 < items; it0 += kGroups * kUnroll) {
-      float v[kUnroll][VEC], d[kUnroll][VEC];
+    for (int it0 = 0; it0 < items; it0 += kGroups * U) {
+      float v[U][8], d[U][8];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int it = it0 + u * kGroups + group;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[u][e] = d[u][e] = 0.f;
-        if (it < items && in) {
-          const int64_t at = (t0 * H + it) * a.N + i0;
-          load_piece<T, VEC>(x + at, v[u]);
-          if (BWD) load_piece<T, VEC>(dy + at, d[u]);
+        for (int e = 0; e < 8; ++e) v[u][e] = d[u][e] = 0.f;
+        if (it < items) {
+          if (ina) load4(x + it * N + ia, v[u]);
+          if (inb) load4(x + it * N + ib, v[u] + 4);
+          if (BWD && ina) load4(dy + it * N + ia, d[u]);
+          if (BWD && inb) load4(dy + it * N + ib, d[u] + 4);
         }
       }
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
+      for (int u = 0; u < U; ++u) {
         if (it0 + u * kGroups >= items) break;
         const int it = it0 + u * kGroups + group;
-        const float2 *row = tab + (it < items ? it / H : 0) * half;
+        const int token = TURN != kNone && it < items ? (H > 1 ? (int)__umulhi((unsigned)it, per_head) : it) : 0;
+        const float2 *row = tab + token * half;
         float s = 0.f;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s = fmaf(v[u][e], v[u][e], s);
-        s = group_sum<LANES>(s);
-        const float r = 1.f / sqrtf(fmaf(s, a.share, a.eps));
+        for (int e = 0; e < 8; ++e) s = fmaf(v[u][e], v[u][e], s);
+        const float r = inverse_sqrt(fmaf(group_sum<LANES>(s), a.share, a.eps));
         if (!BWD) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) v[u][e] = v[u][e] * r * wv[e];
-          if (half) turn_piece<VEC, LANES>(v[u], i0, a, row, 1.f);
-          if (it < items && in) store_piece<T, VEC>(out + (t0 * H + it) * a.N + i0, v[u]);
-        } else {
-          if (half) turn_piece<VEC, LANES>(d[u], i0, a, row, -1.f);
-          float dot = 0.f;
-          if (it < items) {  // a group behind the last head holds zeros, and r may be infinite there
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              const float xh = v[u][e] * r;
-              if (in) dw[e] = fmaf(d[u][e], xh, dw[e]);
-              d[u][e] *= wv[e];
-              v[u][e] = xh;
-              dot = fmaf(d[u][e], xh, dot);
-            }
+          for (int e = 0; e < 8; ++e) v[u][e] = v[u][e] * r * wv[e];
+          turn_pieces<TURN>(v[u], ia, ib, a.rot, row, 1.f);
+          if (it < items) {
+            if (ina) store4(out + it * N + ia, v[u]);
+            if (inb) store4(out + it * N + ib, v[u] + 4);
           }
-          if (!in) dot = 0.f;
+        } else {
+          turn_pieces<TURN>(d[u], ia, ib, a.rot, row, -1.f);
+          float dot = 0.f;
+          const bool la = it < items && ina, lb = it < items && inb;  // r may be infinite where there is nothing
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float xh = (e < 4 ? la : lb) ? v[u][e] * r : 0.f;
+            dw[e] = fmaf(d[u][e], xh, dw[e]);
+            d[u][e] *= wv[e];
+            v[u][e] = xh;
+            dot = fmaf(d[u][e], xh, dot);
+          }
           dot = group_sum<LANES>(dot) * a.share;
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) d[u][e] = r * (d[u][e] - v[u][e] * dot);
-          if (it < items && in) store_piece<T, VEC>(out + (t0 * H + it) * a.N + i0, d[u]);
+          for (int e = 0; e < 8; ++e) d[u][e] = r * (d[u][e] - v[u][e] * dot);
+          if (la) store4(out + it * N + ia, d[u]);
+          if (lb) store4(out + it * N + ib, d[u] + 4);
         }
       }
     }
   }
   if (BWD && a.part[which]) {
     // the block's share of dw: lane groups added in a fixed order
-    __shared__ float acc[kThreads / LANES][LANES * VEC + 1];
+    __shared__ float acc[kGroups][8 * LANES + 1];
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[group][i0 + e] = dw[e];
+    for (int e = 0; e < 8; ++e) {
+      const int i = e < 4 ? ia + e : ib + e - 4;
+      if (i < N) acc[group][i] = dw[e];
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.N; i += kThreads) {
+    for (int i = threadIdx.x; i < N; i += kThreads) {
       float s = 0.f;
 #pragma unroll 8
-      for (int g = 0; g < kThreads / LANES; ++g) s += acc[g][i];
-      a.part[which][(int64_t)blockIdx.x * a.N + i] = s;
+      for (int g = 0; g < kGroups; ++g) s += acc[g][i];
+      a.part[which][(int64_t)blockIdx.x * N + i] = s;
     }
   }
 }
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) qk_value_kernel(Args a) {
     const int nt = (int)(a.rows - t0 < a.tile ? a.rows - t0 : a.tile);
     if (half) {
       __syncthreads();
-      fill_angles(a, t0, nt, tab);
+      fill_angles(a, t0, nt, tab, sizeof(T) == 2);
       __syncthreads();
     }
     for (int it = warp; it < nt * H; it += kWarps) {
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kThreads) qk_value_kernel(Args a) {
         d[e] = (BWD && i < a.N) ? ldf(dy + at + i) : 0.f;
         s = fmaf(v[e], v[e], s);
       }
-      const float r = 1.f / sqrtf(fmaf(group_sum<32>(s), a.share, a.eps));
+      const float r = inverse_sqrt(fmaf(group_sum<32>(s), a.share, a.eps));
       if (!BWD) {
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = v[e] * r * wv[e];
@@ -332,67 +333,55 @@ __global__ void __launch_bounds__(kThreads) qk_value_kernel(Args a) {
   }
 }
 
-// dw[i] = the blocks' shares in a fixed order, in double: 32 slices of the blocks
-// side by side, then the slices. One block for q, one for k.
+// dw[i] = the blocks' shares in a fixed order, in double: 32 slices of the blocks side by
+// side, then the slices. A block has 32 values of q's (blockIdx.y 0) or k's weight.
 __global__ void __launch_bounds__(1024) qk_weight_kernel(const float *pq, const float *pk, int nblk, int N, float *dwq,
                                                          float *dwk) {
-  const float *p = blockIdx.x ? pk : pq;
-  float *dw = blockIdx.x ? dwk : dwq;
+  const float *p = blockIdx.y ? pk : pq;
+  float *dw = blockIdx.y ? dwk : dwq;
   if (!p || !dw) return;
   __shared__ double acc[32][33];
-  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  for (int i0 = 0; i0 < N; i0 += 32) {
-    const int i = i0 + lane;
-    double s = 0;
-    if (i < N)
-      for (int b = slice; b < nblk; b += 32) s += p[(int64_t)b * N + i];
-    acc[slice][lane] = s;
-    __syncthreads();
-    if (slice == 0 && i < N) {
-      double t = 0;
-      for (int k = 0; k < 32; ++k) t += acc[k][lane];
-      dw[i] = (float)t;
-    }
-    __syncthreads();
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
+  double s = 0;
+  if (i < N)
+#pragma unroll 10
+    for (int b = slice; b < nblk; b += 32) s += p[(int64_t)b * N + i];
+  acc[slice][lane] = s;
+  __syncthreads();
+  if (slice == 0 && i < N) {
+    double t = 0;
+#pragma unroll 8
+    for (int k = 0; k < 32; ++k) t += acc[k][lane];
+    dw[i] = (float)t;
   }
 }
 
-template <typename T, int VEC, bool BWD>
-bool launch_lanes(const Args &a, dim3 grid, size_t smem, cudaStream_t st) {
-  const int pieces = a.N / VEC;
-  if (pieces <= 4) qk_piece_kernel<T, VEC, 4, BWD><<<grid, kThreads, smem, st>>>(a);
-  else if (pieces <= 8) qk_piece_kernel<T, VEC, 8, BWD><<<grid, kThreads, smem, st>>>(a);
-  else if (pieces <= 16) qk_piece_kernel<T, VEC, 16, BWD><<<grid, kThreads, smem, st>>>(a);
-  else if (pieces <= 32) qk_piece_kernel<T, VEC, 32, BWD><<<grid, kThreads, smem, st>>>(a);
-  else return false;
-  return true;
+template <typename T, int TURN, bool BWD>
+void launch_lanes(const Args &a, dim3 grid, size_t smem, cudaStream_t st) {
+  const int lanes = (a.N / 4 + 1) / 2;
+  if (lanes <= 4) qk_piece_kernel<T, 4, TURN, BWD><<<grid, kThreads, smem, st>>>(a);
+  else if (lanes <= 8) qk_piece_kernel<T, 8, TURN, BWD><<<grid, kThreads, smem, st>>>(a);
+  else qk_piece_kernel<T, 16, TURN, BWD><<<grid, kThreads, smem, st>>>(a);
 }
 
-// Whether heads can be moved in pieces of `vec` values of `size` bytes.
-bool pieces_fit(const Args &a, int vec, int size, bool bwd) {
-  if (a.N % vec || a.N / vec > 32) return false;
-  if (a.rot && !a.interleaved && (a.rot / 2) % vec) return false;
-  for (int i = 0; i < 2; ++i) {
-    const uintptr_t all = reinterpret_cast<uintptr_t>(a.x[i]) | reinterpret_cast<uintptr_t>(a.out[i]) |
-                          (bwd ? reinterpret_cast<uintptr_t>(a.dy[i]) : 0);
-    if (all % (vec * size)) return false;
-  }
-  return true;
+template <typename T, bool BWD>
+void launch_turn(const Args &a, dim3 grid, size_t smem, cudaStream_t st) {
+  // heads in pieces of four values, which a pair may not cross, from addresses that allow them
+  uintptr_t all = 0;
+  for (int i = 0; i < 2; ++i)
+    all |= reinterpret_cast<uintptr_t>(a.x[i]) | reinterpret_cast<uintptr_t>(a.out[i]) | (BWD ? reinterpret_cast<uintptr_t>(a.dy[i]) : 0);
+  if (a.N % 4 || all % (4 * sizeof(T)) || (a.rot && !a.interleaved && a.rot % 8)) qk_value_kernel<T, BWD><<<grid, kThreads, smem, st>>>(a);
+  else if (!a.rot) launch_lanes<T, kNone, BWD>(a, grid, smem, st);
+  else if (a.interleaved) launch_lanes<T, kNeighbours, BWD>(a, grid, smem, st);
+  else launch_lanes<T, kHalves, BWD>(a, grid, smem, st);
 }
 
 template <bool BWD>
 cudaError_t launch(const Args &a, int io_t, int blocks, cudaStream_t st) {
   const dim3 grid(blocks, 2);
   const size_t smem = sizeof(float2) * a.tile * (a.rot / 2);
-  if (io_t == PDSSM_BF16) {
-    using T = __nv_bfloat16;
-    if (pieces_fit(a, 8, 2, BWD)) launch_lanes<T, 8, BWD>(a, grid, smem, st);
-    else if (pieces_fit(a, 4, 2, BWD)) launch_lanes<T, 4, BWD>(a, grid, smem, st);
-    else qk_value_kernel<T, BWD><<<grid, kThreads, smem, st>>>(a);
-  } else {
-    if (pieces_fit(a, 4, 4, BWD)) launch_lanes<float, 4, BWD>(a, grid, smem, st);
-    else qk_value_kernel<float, BWD><<<grid, kThreads, smem, st>>>(a);
-  }
+  if (io_t == PDSSM_BF16) launch_turn<__nv_bfloat16, BWD>(a, grid, smem, st);
+  else launch_turn<float, BWD>(a, grid, smem, st);
   return cudaGetLastError();
 }
 
@@ -400,17 +389,19 @@ cudaError_t launch(const Args &a, int io_t, int blocks, cudaStream_t st) {
 
 // Tokens a tile: up to 8 share one table of angles and one pair of barriers, fewer
 // when that would leave SMs without a block.
-static int qk_tile(int64_t rows) { return (int)std::min<int64_t>(kMaxTile, std::max<int64_t>(1, rows / (148 * 4))); }
+static int qk_tile(int64_t rows) { return (int)std::min<int64_t>(kMaxTile, std::max<int64_t>(1, rows / kBlocks)); }
 
 int qk_norm_blocks(int64_t rows) {
   const int64_t tiles = (rows + qk_tile(rows) - 1) / qk_tile(rows);
-  return (int)std::min<int64_t>(tiles, 148 * 4);
+  return (int)std::min<int64_t>(tiles, kBlocks);
 }
 
 cudaError_t launch_qk_norm(const QkNormArgs &q, bool bwd, cudaStream_t st) {
   Args a{};
   a.rows = q.rows; a.seqlen = q.seqlen;
-  a.N = (int)q.N; a.rot = q.rot; a.interleaved = q.interleaved; a.tile = qk_tile(q.rows);
+  a.N = (int)q.N; a.rot = q.rot; a.interleaved = q.interleaved;
+  // items of a tile are counted in 16 bits
+  a.tile = std::max(q.heads[0], q.heads[1]) > 4096 ? 1 : qk_tile(q.rows);
   a.share = q.l2 ? 1.f : 1.f / (float)q.N;
   a.eps = q.eps;
   a.inv_freq = q.inv_freq; a.positions = q.positions;
@@ -426,7 +417,7 @@ cudaError_t launch_qk_norm(const QkNormArgs &q, bool bwd, cudaStream_t st) {
   if ((e = trace_after(st)) != cudaSuccess) return e;
   if (bwd && (q.dw[0] || q.dw[1])) {
     if ((e = trace_before(st, "qk_weight_grad")) != cudaSuccess) return e;
-    qk_weight_kernel<<<2, 1024, 0, st>>>(a.part[0], a.part[1], blocks, a.N, q.dw[0], q.dw[1]);
+    qk_weight_kernel<<<dim3((a.N + 31) / 32, 2), 1024, 0, st>>>(a.part[0], a.part[1], blocks, a.N, q.dw[0], q.dw[1]);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = trace_after(st);
   }

@@ -24,11 +24,11 @@ def npy(t):
     return None if t is None else t.detach().double().cpu().numpy()
 
 
-def close(name, got, want, n, unit=2.0 ** -24, axes=None):
-    """|got - want| <= half a step of got's type + 8 sqrt(n) unit S, S over `axes` (a slice's) at least 1."""
+def close(name, got, want, n, unit=2.0 ** -24, axes=None, operands=1.0):
+    """|got - want| <= half a step of got's type + 8 sqrt(n) unit S, S over `axes` (a slice's) at least `operands`."""
     g = npy(got)
     assert g.shape == want.shape, name
-    S = np.maximum(1.0, np.abs(want).max(axis=axes, keepdims=True)) if want.size else 1.0
+    S = np.maximum(operands, np.abs(want).max(axis=axes, keepdims=True)) if want.size else 1.0
     lim = HALF[got.dtype] * np.abs(want) + 8 * np.sqrt(n) * unit * S
     bad = ~(np.abs(g - want) <= lim)
     assert not bad.any(), f"{name}: {bad.sum()} of {bad.size} off, worst {np.abs(g - want)[bad].max():.3g} at limit {np.broadcast_to(lim, g.shape)[bad].min():.3g}"
@@ -86,7 +86,14 @@ def test_qk_norm_backward(c, dt, weights, far):
     assert set(out) == ({"dq", "dk", "dwq", "dwk"} if weights else {"dq", "dk"})
     for n, x, d in (("q", q, dq), ("k", k, dk)):
         dx, dw = norm_oracle(x, kw, "w" + n, d)
-        close("d" + n, out["d" + n], dx, c[4], axes=(-1,))
+        # dx = d w / s - x (sum of d w x) share / s^3: two terms of up to sqrt(2) |d| |w| / s (a turned pair is at most sqrt(2)
+        # larger than its larger value), s = sqrt(share |x|^2 + eps), whose difference can be far smaller than their roundings
+        # (a head of one value: it is 0 but for eps), so S is the terms' size
+        xs = npy(x)
+        s = np.sqrt((xs ** 2).sum(-1, keepdims=True) / (c[4] if c[7] == "rms" else 1) + kw["eps"])
+        w = 1.0 if kw["w" + n] is None else np.abs(npy(kw["w" + n])).max()
+        terms = np.sqrt(2) * np.abs(npy(d)).max(-1, keepdims=True) * w / s
+        close("d" + n, out["d" + n], dx, c[4], axes=(-1,), operands=np.maximum(1.0, terms) if x.numel() else 1.0)
         if weights:  # a sum over all tokens and heads
             close("dw" + n, out["dw" + n], dw, max(1, x.numel()))
 
