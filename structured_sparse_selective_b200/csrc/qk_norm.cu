@@ -10,7 +10,7 @@
 //
 // What bounds it: HBM and the issue rate, both near. Each value is read once and written
 // once (backward: x and dy read, dx written). A head is held by a group of 2^g lanes, two
-// pieces of four values a lane: a piece of the first rotated half and its partner in the
+// pieces of four or eight values a lane: a piece of the first rotated half and its partner in the
 // second, so a pair turns inside a lane (with one 16-byte piece a lane and the partner by
 // shuffles the LM layer took 80 us, issue-bound). Heads whose size, rotated width or
 // alignment do not allow pieces take the one-value-a-lane path with the partner read
@@ -32,24 +32,43 @@ constexpr int kBlocks = 148 * 2;  // of q and of k each: together four of 256 th
 
 enum Turn { kNone, kHalves, kNeighbours };
 
-// Four values moved as one access.
-__device__ __forceinline__ void load4(const float *p, float *v) {
+// V values moved as one access: 4 floats, 4 or 8 bf16.
+template <int V>
+__device__ __forceinline__ void load(const float *p, float *v) {
+  static_assert(V == 4, "16 bytes");
   const float4 x = *reinterpret_cast<const float4 *>(p);
   v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float *v) {
-  const uint2 x = *reinterpret_cast<const uint2 *>(p);
-  v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xffff0000u);
-  v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xffff0000u);
+template <int V>
+__device__ __forceinline__ void load(const __nv_bfloat16 *p, float *v) {
+  uint32_t w[V / 2];
+  if constexpr (V == 8) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(p);
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+  } else {
+    const uint2 x = *reinterpret_cast<const uint2 *>(p);
+    w[0] = x.x; w[1] = x.y;
+  }
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
 }
-__device__ __forceinline__ void store4(float *p, const float *v) {
+template <int V>
+__device__ __forceinline__ void store(float *p, const float *v) {
   *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float *v) {
-  union { uint2 raw; __nv_bfloat162 h[2]; } u;
-  u.h[0] = __floats2bfloat162_rn(v[0], v[1]);
-  u.h[1] = __floats2bfloat162_rn(v[2], v[3]);
-  *reinterpret_cast<uint2 *>(p) = u.raw;
+template <int V>
+__device__ __forceinline__ void store(__nv_bfloat16 *p, const float *v) {
+  uint32_t w[V / 2];
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  if constexpr (V == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
 }
 
 // cos and sin of position * f, the product reduced by whole turns in double.
@@ -103,10 +122,10 @@ __device__ __forceinline__ float group_sum(float s) {
   return s;
 }
 
-// Turns the lane's two pieces, values [ia, ia + 4) and [ib, ib + 4) of the head, by the
+// Turns the lane's two pieces, values [ia, ia + V) and [ib, ib + V) of the head, by the
 // token's angles; `sign` -1 turns back.
-template <int TURN>
-__device__ __forceinline__ void turn_pieces(float (&v)[8], int ia, int ib, int rot, const float2 *tab, float sign) {
+template <int V, int TURN>
+__device__ __forceinline__ void turn_pieces(float (&v)[2 * V], int ia, int ib, int rot, const float2 *tab, float sign) {
   const auto pair = [&](float &x, float &y, float c, float s) {
     const float p = x, q = y;
     s *= sign;
@@ -115,116 +134,126 @@ __device__ __forceinline__ void turn_pieces(float (&v)[8], int ia, int ib, int r
   };
   if (TURN == kHalves) {
     if (ia < rot) {  // then the second piece is the first's partner
-      const float4 t0 = *reinterpret_cast<const float4 *>(tab + ia), t1 = *reinterpret_cast<const float4 *>(tab + ia + 2);
-      pair(v[0], v[4], t0.x, t0.y);
-      pair(v[1], v[5], t0.z, t0.w);
-      pair(v[2], v[6], t1.x, t1.y);
-      pair(v[3], v[7], t1.z, t1.w);
+#pragma unroll
+      for (int e = 0; e < V; e += 2) {
+        const float4 t = *reinterpret_cast<const float4 *>(tab + ia + e);
+        pair(v[e], v[V + e], t.x, t.y);
+        pair(v[e + 1], v[V + e + 1], t.z, t.w);
+      }
     }
   } else if (TURN == kNeighbours) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int i = s ? ib : ia;
-      if (i < rot) pair(v[4 * s], v[4 * s + 1], tab[i >> 1].x, tab[i >> 1].y);
-      if (i + 2 < rot) pair(v[4 * s + 2], v[4 * s + 3], tab[(i >> 1) + 1].x, tab[(i >> 1) + 1].y);
+    for (int e = 0; e < 2 * V; e += 2) {
+      const int i = e < V ? ia + e : ib + e - V;
+      if (i < rot) pair(v[e], v[e + 1], tab[i >> 1].x, tab[i >> 1].y);
     }
   }
 }
 
-// LANES lanes hold one head, two pieces of four values a lane; blockIdx.y: 0 = q, 1 = k.
-// U heads of a lane group are in flight at once, so that their loads cover HBM's latency.
-template <typename T, int LANES, int TURN, bool BWD>
+// LANES lanes hold one head, two pieces of V values a lane (FULL: all lanes do);
+// blockIdx.y: 0 = q, 1 = k. U heads of a lane group are in flight at once, so that their
+// loads cover HBM's latency.
+template <typename T, int V, int LANES, int TURN, bool BWD, bool FULL>
 __global__ void __launch_bounds__(kThreads, 4) qk_piece_kernel(Args a) {
   extern __shared__ __align__(16) float2 tab[];
-  constexpr int U = BWD ? 2 : 4, kGroups = kThreads / LANES;
-  constexpr bool kCoarse = sizeof(T) == 2;
+  constexpr int U = V == 8 ? 2 : BWD ? 2 : 4, kGroups = kThreads / LANES;
   const int which = blockIdx.y, H = a.heads[which], N = a.N, half = a.rot / 2;
   const int group = threadIdx.x / LANES, gl = threadIdx.x % LANES;
   // the lane's pieces: partners first, then what does not turn
-  const int pairs = TURN == kHalves ? half / 4 : 0;
-  const int ia = gl < pairs ? 4 * gl : 4 * (2 * gl), ib = gl < pairs ? ia + half : ia + 4;
-  const bool ina = ia < N, inb = ib < N;
+  const int pairs = TURN == kHalves ? half / V : 0;
+  const int ia = gl < pairs ? V * gl : V * (2 * gl), ib = gl < pairs ? ia + half : ia + V;
+  const bool ina = FULL || ia < N, inb = FULL || ib < N;
   const unsigned per_head = H > 1 ? 0xffffffffu / (unsigned)H + 1 : 0;  // item / H as a product (items < 2^16)
-  float wv[8], dw[8];
+  float wv[2 * V], dw[BWD ? 2 * V : 1];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int i = e < 4 ? ia + e : ib + e - 4;
+  for (int e = 0; e < 2 * V; ++e) {
+    const int i = e < V ? ia + e : ib + e - V;
     wv[e] = a.w[which] && i < N ? a.w[which][i] : 1.f;
-    dw[e] = 0.f;
+    if (BWD) dw[e] = 0.f;
   }
   for (int64_t t0 = (int64_t)blockIdx.x * a.tile; t0 < a.rows; t0 += (int64_t)gridDim.x * a.tile) {
     const int nt = (int)(a.rows - t0 < a.tile ? a.rows - t0 : a.tile);
     if (TURN != kNone) {
       __syncthreads();
-      fill_angles(a, t0, nt, tab, kCoarse);
+      fill_angles(a, t0, nt, tab, sizeof(T) == 2);
       __syncthreads();
     }
     const int items = nt * H;
     const T *x = static_cast<const T *>(a.x[which]) + t0 * H * N;
     const T *dy = static_cast<const T *>(a.dy[which]) + (BWD ? t0 * H * N : 0);
     T *out = static_cast<T *>(a.out[which]) + t0 * H * N;
-    // every lane of a warp takes part in each shuffle: the loop bound is the block's
-    for (int it0 = 0; it0 < items; it0 += kGroups * U) {
-      float v[U][8], d[U][8];
+    // `whole`: every group of the block has a head in each of the U places
+    const auto batch = [&](int it0, bool whole) {
+      float v[U][2 * V], d[BWD ? U : 1][2 * V];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int it = it0 + u * kGroups + group;
+        if (!(FULL && whole)) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[u][e] = d[u][e] = 0.f;
-        if (it < items) {
-          if (ina) load4(x + it * N + ia, v[u]);
-          if (inb) load4(x + it * N + ib, v[u] + 4);
-          if (BWD && ina) load4(dy + it * N + ia, d[u]);
-          if (BWD && inb) load4(dy + it * N + ib, d[u] + 4);
+          for (int e = 0; e < 2 * V; ++e) {
+            v[u][e] = 0.f;
+            if (BWD) d[BWD ? u : 0][e] = 0.f;
+          }
+        }
+        if (whole || it < items) {
+          if (ina) load<V>(x + it * N + ia, v[u]);
+          if (inb) load<V>(x + it * N + ib, v[u] + V);
+          if (BWD && ina) load<V>(dy + it * N + ia, d[BWD ? u : 0]);
+          if (BWD && inb) load<V>(dy + it * N + ib, d[BWD ? u : 0] + V);
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (it0 + u * kGroups >= items) break;
+        if (!whole && it0 + u * kGroups >= items) break;  // the same for all: shuffles follow
         const int it = it0 + u * kGroups + group;
-        const int token = TURN != kNone && it < items ? (H > 1 ? (int)__umulhi((unsigned)it, per_head) : it) : 0;
+        const bool la = (whole || it < items) && ina, lb = (whole || it < items) && inb;
+        const int token = TURN != kNone && (whole || it < items) ? (H > 1 ? (int)__umulhi((unsigned)it, per_head) : it) : 0;
         const float2 *row = tab + token * half;
-        float s = 0.f;
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(v[u][e], v[u][e], s);
-        const float r = inverse_sqrt(fmaf(group_sum<LANES>(s), a.share, a.eps));
+        for (int e = 0; e < 2 * V; e += 2) {
+          s0 = fmaf(v[u][e], v[u][e], s0);
+          s1 = fmaf(v[u][e + 1], v[u][e + 1], s1);
+        }
+        const float r = inverse_sqrt(fmaf(group_sum<LANES>(s0 + s1), a.share, a.eps));
         if (!BWD) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[u][e] = v[u][e] * r * wv[e];
-          turn_pieces<TURN>(v[u], ia, ib, a.rot, row, 1.f);
-          if (it < items) {
-            if (ina) store4(out + it * N + ia, v[u]);
-            if (inb) store4(out + it * N + ib, v[u] + 4);
-          }
+          for (int e = 0; e < 2 * V; ++e) v[u][e] = v[u][e] * r * wv[e];
+          turn_pieces<V, TURN>(v[u], ia, ib, a.rot, row, 1.f);
+          if (la) store<V>(out + it * N + ia, v[u]);
+          if (lb) store<V>(out + it * N + ib, v[u] + V);
         } else {
-          turn_pieces<TURN>(d[u], ia, ib, a.rot, row, -1.f);
+          float(&g)[2 * V] = d[BWD ? u : 0];
+          turn_pieces<V, TURN>(g, ia, ib, a.rot, row, -1.f);
           float dot = 0.f;
-          const bool la = it < items && ina, lb = it < items && inb;  // r may be infinite where there is nothing
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float xh = (e < 4 ? la : lb) ? v[u][e] * r : 0.f;
-            dw[e] = fmaf(d[u][e], xh, dw[e]);
-            d[u][e] *= wv[e];
+          for (int e = 0; e < 2 * V; ++e) {  // r may be infinite where there is nothing
+            const float xh = (e < V ? la : lb) ? v[u][e] * r : 0.f;
+            dw[BWD ? e : 0] = fmaf(g[e], xh, dw[BWD ? e : 0]);
+            g[e] *= wv[e];
             v[u][e] = xh;
-            dot = fmaf(d[u][e], xh, dot);
+            dot = fmaf(g[e], xh, dot);
           }
           dot = group_sum<LANES>(dot) * a.share;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[u][e] = r * (d[u][e] - v[u][e] * dot);
-          if (la) store4(out + it * N + ia, d[u]);
-          if (lb) store4(out + it * N + ib, d[u] + 4);
+          for (int e = 0; e < 2 * V; ++e) g[e] = r * (g[e] - v[u][e] * dot);
+          if (la) store<V>(out + it * N + ia, g);
+          if (lb) store<V>(out + it * N + ib, g + V);
         }
       }
-    }
+    };
+    int it0 = 0;
+    for (; it0 + kGroups * U <= items; it0 += kGroups * U) batch(it0, true);
+    if (it0 < items) batch(it0, false);
   }
   if (BWD && a.part[which]) {
     // the block's share of dw: lane groups added in a fixed order
-    __shared__ float acc[kGroups][8 * LANES + 1];
+    __shared__ float acc[BWD ? kGroups : 1][2 * V * LANES + 1];
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = e < 4 ? ia + e : ib + e - 4;
-      if (i < N) acc[group][i] = dw[e];
+    for (int e = 0; e < 2 * V; ++e) {
+      const int i = e < V ? ia + e : ib + e - V;
+      if (i < N) acc[group][i] = dw[BWD ? e : 0];
     }
     __syncthreads();
     for (int i = threadIdx.x; i < N; i += kThreads) {
@@ -356,32 +385,54 @@ __global__ void __launch_bounds__(1024) qk_weight_kernel(const float *pq, const 
   }
 }
 
-template <typename T, int TURN, bool BWD>
-void launch_lanes(const Args &a, dim3 grid, size_t smem, cudaStream_t st) {
-  const int lanes = (a.N / 4 + 1) / 2;
-  if (lanes <= 4) qk_piece_kernel<T, 4, TURN, BWD><<<grid, kThreads, smem, st>>>(a);
-  else if (lanes <= 8) qk_piece_kernel<T, 8, TURN, BWD><<<grid, kThreads, smem, st>>>(a);
-  else qk_piece_kernel<T, 16, TURN, BWD><<<grid, kThreads, smem, st>>>(a);
+template <typename T, int V, int LANES, int TURN, bool BWD>
+void launch_full(const Args &a, dim3 grid, size_t smem, cudaStream_t st) {
+  if (a.N == 2 * V * LANES) qk_piece_kernel<T, V, LANES, TURN, BWD, true><<<grid, kThreads, smem, st>>>(a);
+  else qk_piece_kernel<T, V, LANES, TURN, BWD, false><<<grid, kThreads, smem, st>>>(a);
 }
 
-template <typename T, bool BWD>
+template <typename T, int V, int TURN, bool BWD>
+void launch_lanes(const Args &a, dim3 grid, size_t smem, cudaStream_t st) {
+  const int lanes = (a.N / V + 1) / 2;
+  if (lanes <= 4) launch_full<T, V, 4, TURN, BWD>(a, grid, smem, st);
+  else if (V == 8 || lanes <= 8) launch_full<T, V, 8, TURN, BWD>(a, grid, smem, st);
+  else if constexpr (V == 4) launch_full<T, V, 16, TURN, BWD>(a, grid, smem, st);
+}
+
+template <typename T, int V, bool BWD>
 void launch_turn(const Args &a, dim3 grid, size_t smem, cudaStream_t st) {
-  // heads in pieces of four values, which a pair may not cross, from addresses that allow them
+  if (!a.rot) launch_lanes<T, V, kNone, BWD>(a, grid, smem, st);
+  else if (a.interleaved) launch_lanes<T, V, kNeighbours, BWD>(a, grid, smem, st);
+  else launch_lanes<T, V, kHalves, BWD>(a, grid, smem, st);
+}
+
+// Whether heads can be moved in pieces of `v` values, which a pair may not cross, of `size` bytes each.
+bool pieces_fit(const Args &a, int v, int size, bool bwd) {
   uintptr_t all = 0;
   for (int i = 0; i < 2; ++i)
-    all |= reinterpret_cast<uintptr_t>(a.x[i]) | reinterpret_cast<uintptr_t>(a.out[i]) | (BWD ? reinterpret_cast<uintptr_t>(a.dy[i]) : 0);
-  if (a.N % 4 || all % (4 * sizeof(T)) || (a.rot && !a.interleaved && a.rot % 8)) qk_value_kernel<T, BWD><<<grid, kThreads, smem, st>>>(a);
-  else if (!a.rot) launch_lanes<T, kNone, BWD>(a, grid, smem, st);
-  else if (a.interleaved) launch_lanes<T, kNeighbours, BWD>(a, grid, smem, st);
-  else launch_lanes<T, kHalves, BWD>(a, grid, smem, st);
+    all |= reinterpret_cast<uintptr_t>(a.x[i]) | reinterpret_cast<uintptr_t>(a.out[i]) | (bwd ? reinterpret_cast<uintptr_t>(a.dy[i]) : 0);
+  return a.N % v == 0 && all % (v * size) == 0 && (!a.rot || a.interleaved || a.rot % (2 * v) == 0);
 }
 
 template <bool BWD>
 cudaError_t launch(const Args &a, int io_t, int blocks, cudaStream_t st) {
   const dim3 grid(blocks, 2);
   const size_t smem = sizeof(float2) * a.tile * (a.rot / 2);
-  if (io_t == PDSSM_BF16) launch_turn<__nv_bfloat16, BWD>(a, grid, smem, st);
-  else launch_turn<float, BWD>(a, grid, smem, st);
+  using B = __nv_bfloat16;
+  if (io_t == PDSSM_BF16) {
+    // sixteen values a lane where registers allow it (forwards): fewer lanes to sum over and half the accesses
+    if (!BWD && pieces_fit(a, 8, 2, BWD)) {
+      if constexpr (!BWD) launch_turn<B, 8, BWD>(a, grid, smem, st);
+    } else if (pieces_fit(a, 4, 2, BWD)) {
+      launch_turn<B, 4, BWD>(a, grid, smem, st);
+    } else {
+      qk_value_kernel<B, BWD><<<grid, kThreads, smem, st>>>(a);
+    }
+  } else if (pieces_fit(a, 4, 4, BWD)) {
+    launch_turn<float, 4, BWD>(a, grid, smem, st);
+  } else {
+    qk_value_kernel<float, BWD><<<grid, kThreads, smem, st>>>(a);
+  }
   return cudaGetLastError();
 }
 
