@@ -64,7 +64,7 @@ pdssm_status check_norm(const pdssm_norm_problem *pb, int64_t *rows) {
 }
 
 size_t norm_bwd_bytes(const pdssm_norm_problem *pb, int64_t rows) {
-  return rows ? align256((size_t)2 * qk_norm_blocks(rows) * pb->N * 4) : 0;
+  return rows ? align256((size_t)2 * qk_norm_bwd_blocks(rows) * pb->N * 4) : 0;
 }
 
 pdssm_status run_norm(const pdssm_norm_problem *pb, QkNormArgs &a, int64_t rows, bool bwd, cudaStream_t cs) {

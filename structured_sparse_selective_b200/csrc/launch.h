@@ -95,7 +95,7 @@ int64_t scan_bwd_column_blocks(int64_t slices, int64_t P, bool cplx);
 cudaError_t launch_scan_bwd(const ScanBwdArgs &a, cudaStream_t st);
 
 // The norm and rotation of query and key heads (csrc/qk_norm.cu). Index 0 is q, 1 is k;
-// `out` is y forwards and dx backwards. part: qk_norm_blocks(rows) * 2 * N floats where a
+// `out` is y forwards and dx backwards. part: qk_norm_bwd_blocks(rows) * 2 * N floats where a
 // weight's gradient is wanted.
 struct QkNormArgs {
   int64_t rows, seqlen, heads[2], N;
@@ -108,7 +108,7 @@ struct QkNormArgs {
   const int32_t *positions;
   float *dw[2], *part;
 };
-int qk_norm_blocks(int64_t rows);
+int qk_norm_bwd_blocks(int64_t rows);
 cudaError_t launch_qk_norm(const QkNormArgs &a, bool bwd, cudaStream_t st);
 
 // The gated delta rule (csrc/delta.cuh); validated and laid out by the C-ABI layer.

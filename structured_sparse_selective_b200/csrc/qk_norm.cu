@@ -28,7 +28,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTile = 8;   // tokens a tile
-constexpr int kBlocks = 148 * 2;  // of q and of k each: together four of 256 threads an SM
+// Blocks of 256 threads of q and of k each: together four an SM, three backwards, which
+// needs the registers.
+constexpr int blocks_of(bool bwd) { return bwd ? 148 * 3 / 2 : 148 * 2; }
 
 enum Turn { kNone, kHalves, kNeighbours };
 
@@ -154,7 +156,7 @@ __device__ __forceinline__ void turn_pieces(float (&v)[2 * V], int ia, int ib, i
 // blockIdx.y: 0 = q, 1 = k. U heads of a lane group are in flight at once, so that their
 // loads cover HBM's latency.
 template <typename T, int V, int LANES, int TURN, bool BWD, bool FULL>
-__global__ void __launch_bounds__(kThreads, 4) qk_piece_kernel(Args a) {
+__global__ void __launch_bounds__(kThreads, BWD ? 3 : 4) qk_piece_kernel(Args a) {
   extern __shared__ __align__(16) float2 tab[];
   constexpr int U = V == 8 ? 2 : BWD ? 2 : 4, kGroups = kThreads / LANES;
   const int which = blockIdx.y, H = a.heads[which], N = a.N, half = a.rot / 2;
@@ -440,23 +442,27 @@ cudaError_t launch(const Args &a, int io_t, int blocks, cudaStream_t st) {
 
 // Tokens a tile: up to 8 share one table of angles and one pair of barriers, fewer
 // when that would leave SMs without a block.
-static int qk_tile(int64_t rows) { return (int)std::min<int64_t>(kMaxTile, std::max<int64_t>(1, rows / kBlocks)); }
-
-int qk_norm_blocks(int64_t rows) {
-  const int64_t tiles = (rows + qk_tile(rows) - 1) / qk_tile(rows);
-  return (int)std::min<int64_t>(tiles, kBlocks);
+static int qk_tile(int64_t rows, bool bwd) {
+  return (int)std::min<int64_t>(kMaxTile, std::max<int64_t>(1, rows / blocks_of(bwd)));
 }
+
+static int qk_blocks(int64_t rows, bool bwd) {
+  const int64_t tiles = (rows + qk_tile(rows, bwd) - 1) / qk_tile(rows, bwd);
+  return (int)std::min<int64_t>(tiles, blocks_of(bwd));
+}
+
+int qk_norm_bwd_blocks(int64_t rows) { return qk_blocks(rows, true); }
 
 cudaError_t launch_qk_norm(const QkNormArgs &q, bool bwd, cudaStream_t st) {
   Args a{};
   a.rows = q.rows; a.seqlen = q.seqlen;
   a.N = (int)q.N; a.rot = q.rot; a.interleaved = q.interleaved;
   // items of a tile are counted in 16 bits
-  a.tile = std::max(q.heads[0], q.heads[1]) > 4096 ? 1 : qk_tile(q.rows);
+  a.tile = std::max(q.heads[0], q.heads[1]) > 4096 ? 1 : qk_tile(q.rows, bwd);
   a.share = q.l2 ? 1.f : 1.f / (float)q.N;
   a.eps = q.eps;
   a.inv_freq = q.inv_freq; a.positions = q.positions;
-  const int blocks = qk_norm_blocks(q.rows);
+  const int blocks = qk_blocks(q.rows, bwd);
   for (int i = 0; i < 2; ++i) {
     a.heads[i] = (int)q.heads[i]; a.x[i] = q.x[i]; a.dy[i] = q.dy[i]; a.out[i] = q.out[i]; a.w[i] = q.w[i];
     a.part[i] = (bwd && q.dw[i]) ? q.part + (int64_t)i * blocks * q.N : nullptr;
