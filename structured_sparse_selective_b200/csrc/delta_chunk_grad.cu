@@ -31,7 +31,7 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;  // 16 warps: the loads of a phase are what it waits for
 
 template <int NP, int PP>
 struct Layout {
@@ -40,11 +40,11 @@ struct Layout {
   static constexpr int kYo = 2 * kKq, kDo = kYo + kRow, kUo = kDo + 2 * kRow, kHo = kUo + 2 * kRow, kFo = kHo + 2 * kH;
   static constexpr int kScal = kFo + 4 * kSquare;                 // the record's scalars
   static constexpr int kRed = kScal + kScalars;                   // dG, dbeta (64 floats each), <X, H'> by warp
-  static constexpr int kBar = kRed + 4 * (2 * kChunk + 8), kBytes = kBar + 24;
+  static constexpr int kBar = kRed + 4 * (2 * kChunk + 16), kBytes = kBar + 24;
   // tensor memory: the two squares; dY H^T, then F1 K; dU H^T, then the other products of dk;
   // U X^T, for N <= 64 in the place of the squares
   static constexpr int kP1 = 0, kP2 = 64, kI1 = 128, kI2 = 128 + NP, kUx = NP == 64 ? 0 : 128 + 2 * NP, kCols = NP == 64 ? 256 : 512;
-  static constexpr int WN = NP / 4;
+  static constexpr int WN = NP / 8;  // a thread's columns of an accumulator of NP
 };
 
 __device__ __forceinline__ float sum4(float4 a, float4 b, float c) {
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
   const uint32_t tbase = __shfl_sync(0xffffffffu, *tslot, 0), sbase = smem_u32(smem);
 
   // the thread's row of an accumulator and its part of the columns
-  const int quarter = warp & 3, row = 16 * quarter + (lane & 15), part = 2 * (warp >> 2) + (lane >> 4);
+  const int quarter = warp & 3, row = 16 * quarter + (lane & 15), up = warp >> 2, part = 2 * up + (lane >> 4);
   const uint32_t tq = tbase + ((uint32_t)(32 * quarter) << 16);
   float dq[WN] = {}, dk[WN] = {};
 
@@ -169,26 +169,27 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
       put_parts(smem + Lay::kDo + off, smem + Lay::kDo + Lay::kRow + off, du[0], du[1]);
       put_parts(smem + Lay::kUo + off, smem + Lay::kUo + Lay::kRow + off, times(e[0], beta), times(e[1], beta));
     }
-    const auto load_state = [&](const float *from, const float *with) {  // returns the thread's share of <from, with>
-      float dot = 0.f;
-#pragma unroll 4
-      for (int k = tid; k < NP * PG; k += kThreads) {
-        const int n = k / PG, g = k % PG;
-        float4 x[2] = {};
+    // a state of the workspace into registers, and from there as operands
+    constexpr int kPer = NP * PG / kThreads;
+    const auto fetch_state = [&](const float *from, float4 (&x)[kPer][2]) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (n < N && 8 * g + 4 * s < Pp) {
-            const int i = n * Pp + 8 * g + 4 * s;
-            x[s] = *reinterpret_cast<const float4 *>(from + i);
-            if (with) dot = sum4(x[s], *reinterpret_cast<const float4 *>(with + i), dot);
-          }
-        }
-        uint8_t *to = smem + Lay::kHo + g * Lay::kHGroup + n * 16;
-        put_parts(to, to + Lay::kH, x[0], x[1]);
+      for (int k = 0; k < kPer; ++k) {
+        const int n = (tid + k * kThreads) / PG, g = tid % PG;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          x[k][s] = n < N && 8 * g + 4 * s < Pp ? *reinterpret_cast<const float4 *>(from + n * Pp + 8 * g + 4 * s) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      return dot;
     };
-    load_state(carry, nullptr);
+    const auto put_state = [&](const float4 (&x)[kPer][2]) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        uint8_t *to = smem + Lay::kHo + (tid % PG) * Lay::kHGroup + ((tid + k * kThreads) / PG) * 16;
+        put_parts(to, to + Lay::kH, x[k][0], x[k][1]);
+      }
+    };
+    float4 sx[kPer][2];
+    fetch_state(carry, sx);
+    put_state(sx);
     cp_async_wait<0>();
     fence_proxy_async_smem();
     __syncthreads();
@@ -216,34 +217,39 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
       }
       __syncwarp();
     }
+    // X, and its product with the state behind the chunk, while the tensor core works
+    float xh = 0.f;
+    {
+      float4 sh[kPer][2];
+      fetch_state(xcarry, sx);
+      fetch_state(carry + a.N * a.Pp, sh);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) xh = sum4(sx[k][0], sh[k][0], sum4(sx[k][1], sh[k][1], xh));
+    }
     wait_bar(&bars[0], ph, a.err, 2000000000ull);
     tc_fence_after();
-    const float xh = load_state(xcarry, carry + a.N * a.Pp);  // the state behind the chunk
+    put_state(sx);
     {
       const float hi = scal[4 * kChunk + row], lo = scal[5 * kChunk + row], beta = scal[2 * kChunk + row];
-      float p1[16], p2[16];
-      load_cols<64, 16>(tq + Lay::kP1 + 32 * (warp >> 2), p1);
-      load_cols<64, 16>(tq + Lay::kP2 + 32 * (warp >> 2), p2);
+      float p1[8], p2[8];
+      load_cols<64, 8>(tq + Lay::kP1 + 16 * up, p1);
+      load_cols<64, 8>(tq + Lay::kP2 + 16 * up, p2);
 #pragma unroll
-      for (int s = 0; s < 16; ++s) {
-        const int j = 16 * part + s;
+      for (int s = 0; s < 8; ++s) {
+        const int j = 8 * part + s;
         const float D = decay2((hi - scal[4 * kChunk + j]) + (lo - scal[5 * kChunk + j]));
         p1[s] = j <= row ? a.scale * D * p1[s] : 0.f;
         p2[s] = j < row ? -beta * D * p2[s] : 0.f;
       }
-#pragma unroll
-      for (int s = 0; s < 16; s += 8) {
-        uint8_t *to = smem + Lay::kFo + (2 * part + s / 8) * 1024 + row * 16;
-        put_parts(to, to + kSquare, make_float4(p1[s], p1[s + 1], p1[s + 2], p1[s + 3]), make_float4(p1[s + 4], p1[s + 5], p1[s + 6], p1[s + 7]));
-        put_parts(to + 2 * kSquare, to + 3 * kSquare, make_float4(p2[s], p2[s + 1], p2[s + 2], p2[s + 3]),
-                  make_float4(p2[s + 4], p2[s + 5], p2[s + 6], p2[s + 7]));
-      }
+      uint8_t *to = smem + Lay::kFo + part * 1024 + row * 16;
+      put_parts(to, to + kSquare, make_float4(p1[0], p1[1], p1[2], p1[3]), make_float4(p1[4], p1[5], p1[6], p1[7]));
+      put_parts(to + 2 * kSquare, to + 3 * kSquare, make_float4(p2[0], p2[1], p2[2], p2[3]), make_float4(p2[4], p2[5], p2[6], p2[7]));
       const float fq = a.scale * scal[row], fk = -beta * scal[row];
       float t[WN];
-      load_cols<64, WN>(tq + Lay::kI1 + 2 * WN * (warp >> 2), t);
+      load_cols<64, WN>(tq + Lay::kI1 + 2 * WN * up, t);
 #pragma unroll
       for (int n = 0; n < WN; ++n) dq[n] = fmaf(fq, t[n], dq[n]);
-      load_cols<64, WN>(tq + Lay::kI2 + 2 * WN * (warp >> 2), t);
+      load_cols<64, WN>(tq + Lay::kI2 + 2 * WN * up, t);
 #pragma unroll
       for (int n = 0; n < WN; ++n) dk[n] = fmaf(fk, t[n], dk[n]);
     }
@@ -290,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
       // dg: what reaches the chunk's end reaches every step of it; two steps a lane
       double s = (double)sdG[2 * lane] + (double)sdG[2 * lane + 1], end = 0;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) end += sxh[w];
+      for (int w = 0; w < 16; ++w) end += sxh[w];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const double dn = __shfl_down_sync(0xffffffffu, s, o);
@@ -312,13 +318,13 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
     {
       const float fade = scal[kChunk + row];
       float t[WN];
-      load_cols<64, WN>(tq + Lay::kUx + 2 * WN * (warp >> 2), t);
+      load_cols<64, WN>(tq + Lay::kUx + 2 * WN * up, t);
 #pragma unroll
       for (int n = 0; n < WN; ++n) dk[n] = fmaf(fade, t[n], dk[n]);
-      load_cols<64, WN>(tq + Lay::kI1 + 2 * WN * (warp >> 2), t);
+      load_cols<64, WN>(tq + Lay::kI1 + 2 * WN * up, t);
 #pragma unroll
       for (int n = 0; n < WN; ++n) dq[n] += t[n];
-      load_cols<64, WN>(tq + Lay::kI2 + 2 * WN * (warp >> 2), t);
+      load_cols<64, WN>(tq + Lay::kI2 + 2 * WN * up, t);
 #pragma unroll
       for (int n = 0; n < WN; ++n) dk[n] += t[n];
     }
