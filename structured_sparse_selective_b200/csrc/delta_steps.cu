@@ -388,26 +388,25 @@ __global__ void __launch_bounds__(128) delta_token_kernel(DeltaArgs a) {
   const float *h0 = a.h0 ? a.h0 + bh * N * P : nullptr;
   float *hf = a.h_final ? a.h_final + bh * N * P : nullptr;
   const bool wide = P % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.h0) | reinterpret_cast<uintptr_t>(a.h_final)) & 15) == 0;
+  // loads come from a valid place where there is nothing, without a branch around each
   float st[4 * J][4];
+  const auto row = [&](int i) { return 32 * (i / 4) + 4 * rg + (i & 3); };
+  if (h0 && wide) {
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int n = 32 * j + 4 * rg + r;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (h0 && n < N) {
-        const float *p = h0 + n * P + col;
-        if (wide) {
-          if (col < P) x = *reinterpret_cast<const float4 *>(p);
-        } else {
-          if (col < P) x.x = p[0];
-          if (col + 1 < P) x.y = p[1];
-          if (col + 2 < P) x.z = p[2];
-          if (col + 3 < P) x.w = p[3];
-        }
-      }
-      st[4 * j + r][0] = x.x; st[4 * j + r][1] = x.y; st[4 * j + r][2] = x.z; st[4 * j + r][3] = x.w;
+    for (int i = 0; i < 4 * J; ++i) {
+      const float4 x = *reinterpret_cast<const float4 *>(h0 + min(row(i), N - 1) * P + min(col, P - 4));
+      st[i][0] = x.x; st[i][1] = x.y; st[i][2] = x.z; st[i][3] = x.w;
     }
+  } else if (h0) {
+#pragma unroll
+    for (int i = 0; i < 4 * J; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) st[i][c] = h0[min(row(i), N - 1) * P + min(col + c, P - 1)];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4 * J; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) st[i][c] = 0.f;
   }
   float k[4 * J], q[4 * J], v[4] = {}, y[4] = {};
   float decay = 1.f, beta = 0.f;
@@ -415,15 +414,18 @@ __global__ void __launch_bounds__(128) delta_token_kernel(DeltaArgs a) {
     const T *kp = static_cast<const T *>(a.k) + (b * a.Hk + hk) * N, *qp = static_cast<const T *>(a.q) + (b * a.Hk + hk) * N;
 #pragma unroll
     for (int i = 0; i < 4 * J; ++i) {
-      const int n = 32 * (i / 4) + 4 * rg + (i & 3);
-      k[i] = n < N ? ldf(kp + n) : 0.f;
-      q[i] = n < N ? ldf(qp + n) * a.scale : 0.f;
+      k[i] = ldf(kp + min(row(i), N - 1));
+      q[i] = ldf(qp + min(row(i), N - 1));
     }
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (col + c < P) v[c] = ldf(static_cast<const T *>(a.v) + bh * P + col + c);
+    for (int c = 0; c < 4; ++c) v[c] = ldf(static_cast<const T *>(a.v) + bh * P + min(col + c, P - 1));
     decay = expf(clamp_gate(ldf(static_cast<const G *>(a.g) + bh)));
     beta = ldf(static_cast<const G *>(a.beta) + bh);
+#pragma unroll
+    for (int i = 0; i < 4 * J; ++i) {
+      k[i] = row(i) < N ? k[i] : 0.f;
+      q[i] = row(i) < N ? q[i] * a.scale : 0.f;
+    }
     float d[4] = {};
 #pragma unroll
     for (int i = 0; i < 4 * J; ++i)
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(128) delta_token_kernel(DeltaArgs a) {
   if (!hf) return;
 #pragma unroll
   for (int i = 0; i < 4 * J; ++i) {
-    const int n = 32 * (i / 4) + 4 * rg + (i & 3);
+    const int n = row(i);
     if (n >= N) continue;
     float *p = hf + n * P + col;
     if (wide) {
