@@ -20,7 +20,8 @@
 // gates are differences of fp32 sums over y.
 //
 // The chain K H -> Te -> K^T u is what a sequence waits for; it runs once a chunk, and the
-// other products fill the pipe in its pauses. Roles (12 warps): 8 keep the state (fp32, in
+// other products fill the pipe in its pauses. A product starts on the half of its depth
+// that four of the eight state warps have written, while the others still write. Roles (12 warps): 8 keep the state (fp32, in
 // registers: a row's n-range each) and do all elementwise work, a ninth issues the
 // products, two bring K, Q (16-byte cp.async into the operand order), V and the record
 // (one bulk copy) a chunk ahead into two stages, and one writes y from shared memory.
@@ -41,7 +42,8 @@ namespace {
 constexpr int kStateWarps = 8, kIssuer = 8, kLoader0 = 9, kLoaders = 2, kWriter = 11;
 constexpr int kThreads = 32 * (kWriter + 1);
 
-enum Bar { kFull0, kFull1, kFree0, kFree1, kH, kR, kU1, kU2, kDoneS, kDoneU, kDoneD, kDoneY, kOut, kOutFree, kEnd, kBars };
+// kH, kR, kU: [half], from the four warps that have that half of a row's columns.
+enum Bar { kFull0, kFull1, kFree0, kFree1, kH, kR = kH + 2, kU1 = kR + 2, kU2 = kU1 + 2, kDoneS, kDoneU, kDoneD, kDoneY, kOut, kOutFree, kEnd, kBars };
 
 template <int NP, int PM, bool SAVE>
 struct Layout {
@@ -68,6 +70,7 @@ template <int NP, int PM, bool SAVE>
 __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, bool wide, bool wide_v) {
   using Lay = Layout<NP, PM, SAVE>;
   constexpr int W = Lay::W, WN = Lay::WN;
+  constexpr bool kAhead = W == 16;
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::kBarOff);
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + kBars);
@@ -79,8 +82,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i) {
-      const bool state = i == kFree0 || i == kFree1 || i == kH || i == kR || i == kU1 || i == kU2 || i == kOut;
-      mbar_init(&bars[i], state ? kStateWarps : (i == kFull0 || i == kFull1) ? 32 * kLoaders + 1 : 1);
+      const bool half = i >= kH && i < kU2, state = i == kFree0 || i == kFree1 || i == kU2 || i == kOut;
+      mbar_init(&bars[i], half ? kStateWarps / 2 : state ? kStateWarps : (i == kFull0 || i == kFull1) ? 32 * kLoaders + 1 : 1);
     }
     mbar_fence_init();
   }
@@ -141,9 +144,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       const int live = (int)min((int64_t)kChunk, len - (int64_t)i * kChunk);
       const int64_t row0 = b * a.L + (int64_t)i * kChunk;
       using B = const __nv_bfloat16;
-      load_tile<NP / 8, kChunkGroup, 16>(st, static_cast<B *>(a.k), row0, a.Hk, hk, a.N, 0, live, wide, tid, 32 * kLoaders);
-      load_tile<NP / 8, kChunkGroup, 16>(st + Lay::kQ, static_cast<B *>(a.q), row0, a.Hk, hk, a.N, 0, live, wide, tid, 32 * kLoaders);
-      load_tile<PM / 8, 16, 2 * PM>(st + Lay::kVOff, static_cast<B *>(a.v), row0, a.H, h, a.P, p0, live, wide_v, tid, 32 * kLoaders);
+      load_tile<NP / 8, kChunkGroup, 16, 32 * kLoaders>(st, static_cast<B *>(a.k), row0, a.Hk, hk, a.N, 0, live, wide, tid);
+      load_tile<NP / 8, kChunkGroup, 16, 32 * kLoaders>(st + Lay::kQ, static_cast<B *>(a.q), row0, a.Hk, hk, a.N, 0, live, wide, tid);
+      load_tile<PM / 8, 16, 2 * PM, 32 * kLoaders>(st + Lay::kVOff, static_cast<B *>(a.v), row0, a.H, h, a.P, p0, live, wide_v, tid);
       cp_async_commit();
       cp_async_wait<0>();
       fence_proxy_async_smem();
@@ -161,17 +164,20 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       const uint64_t dk = smem_desc(sk, kChunkGroup, 128), dq = smem_desc(sq, kChunkGroup, 128), dkt = smem_desc(sk, 128, kChunkGroup),
                      dte = smem_desc(te, 1024, 128), da = smem_desc(sa, 1024, 128);
       wait_bar(&bars[kFull0 + s], (i >> 1) & 1, a.err, a.wait_ns);
-      wait_bar(&bars[kH], ph, a.err, a.wait_ns);
-      tc_fence_after();
-      if (elect_one()) {
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
+      for (int f = 0; f < 2; ++f) {
+        wait_bar(&bars[kH + f], ph, a.err, a.wait_ns);
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < NP / 16; ++ks)
-            mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kX + q * (NP / 2) + 8 * ks, dk + (2 * kChunkGroup * ks >> 4), idS, q + ks > 0);
-        mma_commit(&bars[kDoneS]);
+          for (int q = 0; q < 3; ++q)
+#pragma unroll
+            for (int ks = f * NP / 32; ks < (f + 1) * NP / 32; ++ks)
+              mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kX + q * (NP / 2) + 8 * ks, dk + (2 * kChunkGroup * ks >> 4), idS, f + q + ks > 0);
+          if (f == 1) mma_commit(&bars[kDoneS]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       // Q H into Yh, once the chunk before has been read out of it
       if (i >= 1) wait_bar(&bars[kFree0 + (s ^ 1)], ((i - 1) >> 1) & 1, a.err, a.wait_ns);
       tc_fence_after();
@@ -183,32 +189,38 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
             mma_bf16_ts(tbase + Lay::kYh, tbase + Lay::kX + q * (NP / 2) + 8 * ks, dq + (2 * kChunkGroup * ks >> 4), idS, q + ks > 0);
       }
       __syncwarp();
-      wait_bar(&bars[kR], ph, a.err, a.wait_ns);
-      tc_fence_after();
-      if (elect_one()) {
-        // R Te^T: parts (0,0) (1,0) (0,1) (2,0) (1,1) (0,2)
 #pragma unroll
-        for (int o = 0; o < 3; ++o)
+      for (int f = 0; f < 2; ++f) {
+        wait_bar(&bars[kR + f], ph, a.err, a.wait_ns);
+        tc_fence_after();
+        if (elect_one()) {
+          // R Te^T: parts (0,0) (1,0) (0,1) (2,0) (1,1) (0,2)
 #pragma unroll
-          for (int q = 0; q <= o; ++q)
+          for (int o = 0; o < 3; ++o)
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kD + (o - q) * 32 + 8 * ks, dte + ((q * kSquare + 2048 * ks) >> 4), idS,
-                          o + q + ks > 0);
-        mma_commit(&bars[kDoneU]);
+            for (int q = 0; q <= o; ++q)
+#pragma unroll
+              for (int ks = 2 * f; ks < 2 * f + 2; ++ks)
+                mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kD + (o - q) * 32 + 8 * ks, dte + ((q * kSquare + 2048 * ks) >> 4), idS,
+                            f + o + q + ks > 0);
+          if (f == 1) mma_commit(&bars[kDoneU]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      wait_bar(&bars[kU1], ph, a.err, a.wait_ns);
-      tc_fence_after();
-      if (elect_one()) {
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
+      for (int f = 0; f < 2; ++f) {
+        wait_bar(&bars[kU1 + f], ph, a.err, a.wait_ns);
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_ts(tbase + Lay::kD, tbase + Lay::kUd + q * 32 + 8 * ks, dkt + (256 * ks >> 4), idD, q + ks > 0);
-        mma_commit(&bars[kDoneD]);
+          for (int q = 0; q < 3; ++q)
+#pragma unroll
+            for (int ks = 2 * f; ks < 2 * f + 2; ++ks)
+              mma_bf16_ts(tbase + Lay::kD, tbase + Lay::kUd + q * 32 + 8 * ks, dkt + (256 * ks >> 4), idD, f + q + ks > 0);
+          if (f == 1) mma_commit(&bars[kDoneD]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       wait_bar(&bars[kU2], ph, a.err, a.wait_ns);
       tc_fence_after();
       if (elect_one()) {
@@ -247,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
     float st[WN];
 #pragma unroll
     for (int n = 0; n < WN; ++n) st[n] = (a.h0 && pin && n0 + n < N) ? a.h0[(bh * a.N + n0 + n) * a.P + p] : 0.f;
-    const auto ready = [&](Bar which) {
+    const auto ready = [&](int which) {
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -272,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
     };
     if (chunks > 0) {
       store_parts<PM, WN, 3>(tX, NP / 2, st);
-      ready(kH);
+      ready(kH + up);
     }
     for (int i = 0; i < chunks; ++i) {
       const int s = i & 1;
@@ -282,27 +294,34 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(stage + Lay::kVOff) + c0 * PM + row;
       if (SAVE) save_state(i);
       wait_bar(&bars[kFull0 + s], (i >> 1) & 1, a.err, a.wait_ns);
+      // what does not wait for a product is read ahead of it, where registers allow
+      float x[W], w[W], vv[kAhead ? W : 1];
+      if (kAhead) {
+        load_scalars<W>(w, scal + c0);
+#pragma unroll
+        for (int c = 0; c < W; ++c) vv[kAhead ? c : 0] = __bfloat162float(v[c * PM]);
+      }
       wait_bar(&bars[kDoneS], ph, a.err, a.wait_ns);
       tc_fence_after();
-      float x[W], w[W];
       load_cols<PM, W>(tZ, x);
-      load_scalars<W>(w, scal + c0);
+      if (!kAhead) load_scalars<W>(w, scal + c0);
 #pragma unroll
-      for (int c = 0; c < W; ++c) x[c] = fmaf(-w[c], x[c], __bfloat162float(v[c * PM]));
+      for (int c = 0; c < W; ++c) x[c] = fmaf(-w[c], x[c], kAhead ? vv[kAhead ? c : 0] : __bfloat162float(v[c * PM]));
       store_parts<PM, W, 3>(tR, 32, x);
-      ready(kR);
+      ready(kR + up);
+      if (kAhead) load_scalars<W>(w, scal + 2 * kChunk + c0);
       wait_bar(&bars[kDoneU], ph, a.err, a.wait_ns);
       tc_fence_after();
       load_cols<PM, W>(tZ, x);
       if (SAVE) save_rows(a.e, i, x);
-      load_scalars<W>(w, scal + 2 * kChunk + c0);
+      if (!kAhead) load_scalars<W>(w, scal + 2 * kChunk + c0);
 #pragma unroll
       for (int c = 0; c < W; ++c) x[c] *= w[c];
       load_scalars<W>(w, scal + kChunk + c0);
 #pragma unroll
       for (int c = 0; c < W; ++c) w[c] *= x[c];
       store_parts<PM, W, 3>(tUd, 32, w);
-      ready(kU1);
+      ready(kU1 + up);
       store_parts<PM, W, SAVE ? 3 : 2>(tUy, 32, x);
       ready(kU2);
       wait_bar(&bars[kDoneD], ph, a.err, a.wait_ns);
@@ -319,12 +338,18 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
 #pragma unroll
         for (int n = 0; n < WN; ++n) st[n] = fmaf(last, st[n], d[n]);
       }
-      // u's parts may lie where the state's go: the product with A has to be done too
-      wait_bar(&bars[kDoneY], ph, a.err, a.wait_ns);
-      tc_fence_after();
+      // where u's parts lie among those of the state, the product with A has to be done too
+      if (Lay::kUy < Lay::kD) {
+        wait_bar(&bars[kDoneY], ph, a.err, a.wait_ns);
+        tc_fence_after();
+      }
       if (i + 1 < chunks) {
         store_parts<PM, WN, 3>(tX, NP / 2, st);
-        ready(kH);
+        ready(kH + up);
+      }
+      if (Lay::kUy >= Lay::kD) {
+        wait_bar(&bars[kDoneY], ph, a.err, a.wait_ns);
+        tc_fence_after();
       }
       if (!SAVE) {
         load_cols<PM, W>(tYa, w);

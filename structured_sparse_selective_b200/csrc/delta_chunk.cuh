@@ -52,20 +52,28 @@ __device__ __forceinline__ uint4 gather8(const __nv_bfloat16 *p, int n) {
 }
 
 // The rows [row0, row0 + 64) of head `head` of x [rows][heads][n] as an operand in shared
-// memory, element (step c, column j): (j / 8) * GROUP + c * ROW + (j % 8) * 2, by `threads`
-// threads. WIDE: 16-byte asynchronous copies (n a multiple of 8, x aligned to 16 bytes).
-// Zeros behind the `live` rows and the n columns.
-template <int NG, int GROUP, int ROW>
+// memory, element (step c, column j): (j / 8) * GROUP + c * ROW + (j % 8) * 2, by THREADS
+// threads. `wide`: 16-byte asynchronous copies (n a multiple of 8, x aligned to 16 bytes).
+// Zeros behind the `live` rows and the n columns. A thread has one group of columns and
+// every THREADS / NG-th row: two additions a copy (with the place worked out for each copy
+// a chunk's copies took 4,000 to 8,000 cycles to ask for, longer than the chunk).
+template <int NG, int GROUP, int ROW, int THREADS>
 __device__ __forceinline__ void load_tile(uint8_t *dst, const __nv_bfloat16 *x, int64_t row0, int64_t heads, int64_t head, int64_t n,
-                                          int64_t n0, int live, bool wide, int tid, int threads) {
-  const int have = (int)min((int64_t)8 * NG, n - n0);
-  const __nv_bfloat16 *src = x + (row0 * heads + head) * n + n0;
-  const int64_t row = heads * n;
-  for (int k = tid; k < kChunk * NG; k += threads) {
-    const int c = k / NG, g = k % NG;
-    uint8_t *to = dst + g * GROUP + c * ROW;
-    if (wide && c < live && 8 * g < have) sm100::cp_async16(to, src + c * row + 8 * g);
-    else *reinterpret_cast<uint4 *>(to) = c < live ? gather8(src + c * row + 8 * g, have - 8 * g) : make_uint4(0, 0, 0, 0);
+                                          int64_t n0, int live, bool wide, int tid) {
+  constexpr int kStep = THREADS / NG;
+  static_assert(THREADS % NG == 0 && kChunk % kStep == 0, "whole rows");
+  const int g = tid % NG, c0 = tid / NG, have = (int)min((int64_t)8 * NG, n - n0);
+  const int64_t row = heads * n, step = kStep * row;
+  const __nv_bfloat16 *src = x + (row0 * heads + head) * n + n0 + 8 * g + c0 * row;
+  uint8_t *to = dst + g * GROUP + c0 * ROW;
+  if (wide && live == kChunk && 8 * g < have) {
+#pragma unroll
+    for (int c = 0; c < kChunk / kStep; ++c, src += step) sm100::cp_async16(to + c * kStep * ROW, src);
+  } else {
+    for (int c = c0; c < kChunk; c += kStep, src += step, to += kStep * ROW) {
+      if (wide && c < live && 8 * g < have) sm100::cp_async16(to, src);
+      else *reinterpret_cast<uint4 *>(to) = c < live && 8 * g < have ? gather8(src, have - 8 * g) : make_uint4(0, 0, 0, 0);
+    }
   }
 }
 

@@ -25,7 +25,8 @@ namespace {
 constexpr int kStateWarps = 8, kIssuer = 8, kLoader0 = 9, kLoaders = 2;
 constexpr int kThreads = 32 * (kLoader0 + kLoaders);
 
-enum Bar { kFull0, kFull1, kFree0, kFree1, kX, kR, kU, kDoneS, kDoneU, kDoneD, kEnd, kBars };
+// kX, kR, kU: [half], from the four warps that have that half of a row's columns.
+enum Bar { kFull0, kFull1, kFree0, kFree1, kX, kR = kX + 2, kU = kR + 2, kDoneS = kU + 2, kDoneU, kDoneD, kEnd, kBars };
 
 template <int NP, int PM>
 struct Layout {
@@ -56,8 +57,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i) {
-      const bool state = i == kFree0 || i == kFree1 || i == kX || i == kR || i == kU;
-      mbar_init(&bars[i], state ? kStateWarps : (i == kFull0 || i == kFull1) ? 32 * kLoaders + 1 : 1);
+      const bool half = i >= kX && i < kDoneS, state = i == kFree0 || i == kFree1;
+      mbar_init(&bars[i], half ? kStateWarps / 2 : state ? kStateWarps : (i == kFull0 || i == kFull1) ? 32 * kLoaders + 1 : 1);
     }
     mbar_fence_init();
   }
@@ -85,9 +86,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
       const int live = (int)min((int64_t)kChunk, len - (int64_t)chunk * kChunk);
       const int64_t row0 = b * a.L + (int64_t)chunk * kChunk;
       using B = const __nv_bfloat16;
-      load_tile<NP / 8, kChunkGroup, 16>(st, static_cast<B *>(a.k), row0, a.Hk, hk, a.N, 0, live, wide, tid, 32 * kLoaders);
-      load_tile<NP / 8, kChunkGroup, 16>(st + Lay::kTile, static_cast<B *>(a.q), row0, a.Hk, hk, a.N, 0, live, wide, tid, 32 * kLoaders);
-      load_tile<PM / 8, 16, 2 * PM>(st + Lay::kDyOff, static_cast<B *>(a.dy), row0, a.H, h, a.P, p0, live, wide_v, tid, 32 * kLoaders);
+      load_tile<NP / 8, kChunkGroup, 16, 32 * kLoaders>(st, static_cast<B *>(a.k), row0, a.Hk, hk, a.N, 0, live, wide, tid);
+      load_tile<NP / 8, kChunkGroup, 16, 32 * kLoaders>(st + Lay::kTile, static_cast<B *>(a.q), row0, a.Hk, hk, a.N, 0, live, wide, tid);
+      load_tile<PM / 8, 16, 2 * PM, 32 * kLoaders>(st + Lay::kDyOff, static_cast<B *>(a.dy), row0, a.H, h, a.P, p0, live, wide_v, tid);
       cp_async_commit();
       cp_async_wait<0>();
       fence_proxy_async_smem();
@@ -103,52 +104,61 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
       const uint64_t dk = smem_desc(sk, kChunkGroup, 128), dkt = smem_desc(sk, 128, kChunkGroup), dqt = smem_desc(sq, 128, kChunkGroup),
                      dtb = smem_desc(tb, 128, 1024), da = smem_desc(sa, 128, 1024);
       wait_bar(&bars[kFull0 + s], (i >> 1) & 1, a.err, a.wait_ns);
-      wait_bar(&bars[kX], ph, a.err, a.wait_ns);
-      tc_fence_after();
-      if (elect_one()) {
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
+      for (int f = 0; f < 2; ++f) {
+        wait_bar(&bars[kX + f], ph, a.err, a.wait_ns);
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < NP / 16; ++ks)
-            mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kP + q * (NP / 2) + 8 * ks, dk + (2 * kChunkGroup * ks >> 4), idS, q + ks > 0);
+          for (int q = 0; q < 3; ++q)
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
+            for (int ks = f * NP / 32; ks < (f + 1) * NP / 32; ++ks)
+              mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kP + q * (NP / 2) + 8 * ks, dk + (2 * kChunkGroup * ks >> 4), idS, f + q + ks > 0);
+          if (f == 1) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_ts(tbase + Lay::kA, tbase + Lay::kY + 8 * ks, da + ((q * kSquare + 256 * ks) >> 4), idT, q + ks > 0);
-        mma_commit(&bars[kDoneS]);
+            for (int q = 0; q < 3; ++q)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma_bf16_ts(tbase + Lay::kA, tbase + Lay::kY + 8 * ks, da + ((q * kSquare + 256 * ks) >> 4), idT, q + ks > 0);
+            mma_commit(&bars[kDoneS]);
+          }
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      wait_bar(&bars[kR], ph, a.err, a.wait_ns);
-      tc_fence_after();
-      if (elect_one()) {
 #pragma unroll
-        for (int o = 0; o < 3; ++o)
+      for (int f = 0; f < 2; ++f) {
+        wait_bar(&bars[kR + f], ph, a.err, a.wait_ns);
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-          for (int q = 0; q <= o; ++q)
+          for (int o = 0; o < 3; ++o)
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kD + (o - q) * 32 + 8 * ks, dtb + ((q * kSquare + 256 * ks) >> 4), idT,
-                          o + q + ks > 0);
-        mma_commit(&bars[kDoneU]);
+            for (int q = 0; q <= o; ++q)
+#pragma unroll
+              for (int ks = 2 * f; ks < 2 * f + 2; ++ks)
+                mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kD + (o - q) * 32 + 8 * ks, dtb + ((q * kSquare + 256 * ks) >> 4), idT,
+                            f + o + q + ks > 0);
+          if (f == 1) mma_commit(&bars[kDoneU]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      wait_bar(&bars[kU], ph, a.err, a.wait_ns);
-      tc_fence_after();
-      if (elect_one()) {
+      // kU also says that the half's parts of dY diag(exp G) are there
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
+      for (int f = 0; f < 2; ++f) {
+        wait_bar(&bars[kU + f], ph, a.err, a.wait_ns);
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_ts(tbase + Lay::kD, tbase + Lay::kP + q * 32 + 8 * ks, dkt + (256 * ks >> 4), idD, q + ks > 0);
+          for (int q = 0; q < 3; ++q)
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_ts(tbase + Lay::kD, tbase + Lay::kQ + q * 32 + 8 * ks, dqt + (256 * ks >> 4), idD, 1);
-        mma_commit(&bars[kDoneD]);
+            for (int ks = 2 * f; ks < 2 * f + 2; ++ks) {
+              mma_bf16_ts(tbase + Lay::kD, tbase + Lay::kQ + q * 32 + 8 * ks, dqt + (256 * ks >> 4), idD, f + q + ks > 0);
+              mma_bf16_ts(tbase + Lay::kD, tbase + Lay::kP + q * 32 + 8 * ks, dkt + (256 * ks >> 4), idD, 1);
+            }
+          if (f == 1) mma_commit(&bars[kDoneD]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
     if (chunks > 0) {
       if (elect_one()) mma_commit(&bars[kEnd]);
@@ -173,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
     float st[WN];
 #pragma unroll
     for (int n = 0; n < WN; ++n) st[n] = (a.dh_final && pin && n0 + n < N) ? a.dh_final[(bh * a.N + n0 + n) * a.P + p] : 0.f;
-    const auto ready = [&](Bar which) {
+    const auto ready = [&](int which) {
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -192,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
     if (chunks > 0) {
       store_parts<PM, WN, 3>(tX, NP / 2, st);
       store_dy(0);
-      ready(kX);
+      ready(kX + up);
     }
     for (int i = 0; i < chunks; ++i) {
       const int s = i & 1, chunk = chunks - 1 - i;
@@ -217,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
 #pragma unroll
       for (int c = 0; c < W; ++c) x[c] += w[c];
       store_parts<PM, W, 3>(tR, 32, x);
-      ready(kR);
+      ready(kR + up);
       // meanwhile scale dY diag(exp G); X's parts, whose place it may take, have been read
       load_scalars<W>(w, scal + c0);
 #pragma unroll
@@ -235,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
         g[c] *= -w[c];
       }
       store_parts<PM, W, 3>(tU, 32, g);
-      ready(kU);
+      ready(kU + up);
       {
         const int64_t t = (int64_t)chunk * kChunk + c0;
         const int n = (int)min((int64_t)W, len - t);
@@ -273,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
       if (i + 1 < chunks) {
         store_parts<PM, WN, 3>(tX, NP / 2, st);
         store_dy(i + 1);
-        ready(kX);
+        ready(kX + up);
       }
     }
     if (pin) {

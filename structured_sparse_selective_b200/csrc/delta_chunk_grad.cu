@@ -104,8 +104,8 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
     tmem_alloc(tslot, Lay::kCols);
     tmem_relinquish();
   }
-  load_tile<NP / 8, kChunkGroup, 16>(smem, static_cast<const B *>(a.k), row0, a.Hk, hk, a.N, 0, live, wide, tid, kThreads);
-  load_tile<NP / 8, kChunkGroup, 16>(smem + Lay::kKq, static_cast<const B *>(a.q), row0, a.Hk, hk, a.N, 0, live, wide, tid, kThreads);
+  load_tile<NP / 8, kChunkGroup, 16, kThreads>(smem, static_cast<const B *>(a.k), row0, a.Hk, hk, a.N, 0, live, wide, tid);
+  load_tile<NP / 8, kChunkGroup, 16, kThreads>(smem + Lay::kKq, static_cast<const B *>(a.q), row0, a.Hk, hk, a.N, 0, live, wide, tid);
   cp_async_commit();
   tc_fence_before();
   __syncthreads();
