@@ -48,7 +48,8 @@ enum Bar { kFull0, kFull1, kFree0, kFree1, kH, kR = kH + 2, kU1 = kR + 2, kU2 = 
 template <int NP, int PM, bool SAVE>
 struct Layout {
   // tensor memory, 32-bit columns: X holds the state's parts (K H and Q H read them), then
-  // u's parts; D the parts of R, then the update; Z first S, then E.
+  // u's parts; D the parts of R, then the update; Z has S, Ya first E, then U^T A^T. (E may
+  // not take S's place: its product starts while half of the warps still read S.)
   static constexpr int kX = 0, kXn = 3 * NP / 2;
   static constexpr int kD = kXn, kDn = NP > 96 ? NP : 96;
   static constexpr int kYh = kD + kDn, kYa = kYh + 64, kZ = kYa + 64;
@@ -126,6 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
     }
   } else if (warp >= kLoader0) {
     const int tid = threadIdx.x - 32 * kLoader0;
+    const bool copies = wide && wide_v && a.N == NP && a.P - p0 >= PM;  // nothing is written by the threads themselves
     for (int i = 0; i < chunks; ++i) {
       const int s = i & 1;
       if (i >= 2) wait_bar(&bars[kFree0 + s], ((i >> 1) - 1) & 1, a.err, a.wait_ns);
@@ -147,10 +149,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       load_tile<NP / 8, kChunkGroup, 16, 32 * kLoaders>(st, static_cast<B *>(a.k), row0, a.Hk, hk, a.N, 0, live, wide, tid);
       load_tile<NP / 8, kChunkGroup, 16, 32 * kLoaders>(st + Lay::kQ, static_cast<B *>(a.q), row0, a.Hk, hk, a.N, 0, live, wide, tid);
       load_tile<PM / 8, 16, 2 * PM, 32 * kLoaders>(st + Lay::kVOff, static_cast<B *>(a.v), row0, a.H, h, a.P, p0, live, wide_v, tid);
-      cp_async_commit();
-      cp_async_wait<0>();
-      fence_proxy_async_smem();
-      mbar_arrive(&bars[kFull0 + s]);
+      if (copies && live == kChunk) {  // on to the next chunk while the copies land
+        cp_async_arrive(&bars[kFull0 + s]);
+      } else {
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        mbar_arrive(&bars[kFull0 + s]);
+      }
     }
   } else if (warp == kIssuer) {
     // The whole warp goes through the loop and one lane issues: descriptors and addresses
@@ -164,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       const uint64_t dk = smem_desc(sk, kChunkGroup, 128), dq = smem_desc(sq, kChunkGroup, 128), dkt = smem_desc(sk, 128, kChunkGroup),
                      dte = smem_desc(te, 1024, 128), da = smem_desc(sa, 1024, 128);
       wait_bar(&bars[kFull0 + s], (i >> 1) & 1, a.err, a.wait_ns);
+      fence_proxy_async_smem();  // the loaders' writes, seen through the barrier, before the tensor core's reads
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
         wait_bar(&bars[kH + f], ph, a.err, a.wait_ns);
@@ -201,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
             for (int q = 0; q <= o; ++q)
 #pragma unroll
               for (int ks = 2 * f; ks < 2 * f + 2; ++ks)
-                mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kD + (o - q) * 32 + 8 * ks, dte + ((q * kSquare + 2048 * ks) >> 4), idS,
+                mma_bf16_ts(tbase + Lay::kYa, tbase + Lay::kD + (o - q) * 32 + 8 * ks, dte + ((q * kSquare + 2048 * ks) >> 4), idS,
                             f + o + q + ks > 0);
           if (f == 1) mma_commit(&bars[kDoneU]);
         }
@@ -267,20 +274,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
     };
     // SAVE: the state before chunk i (and behind the last), and 64 x p values of the chunk's steps
     const auto save_state = [&](int i) {
-      float *to = a.carry + ((bh * (a.nC + 1) + i) * a.N + n0) * a.Pp + p;
-      if (p >= a.Pp) return;
-#pragma unroll
-      for (int n = 0; n < WN; ++n, to += a.Pp)
-        if (n0 + n < N) *to = st[n];
+      store_rows<PM, WN>(a.carry + ((bh * (a.nC + 1) + i) * a.N + n0) * a.Pp + p, a.Pp, p < a.Pp ? N - n0 : 0, st);
     };
     const auto save_rows = [&](float *rows, int i, const float (&x)[W]) {
-      const int64_t t = (int64_t)i * kChunk + c0, step = a.H * a.Pp;
-      float *to = rows + ((b * a.L + t) * a.H + h) * a.Pp + p;
-      const int n = (int)min((int64_t)W, len - t);
-      if (p >= a.Pp) return;
-#pragma unroll
-      for (int c = 0; c < W; ++c, to += step)
-        if (c < n) *to = x[c];
+      const int64_t t = (int64_t)i * kChunk + c0;
+      store_rows<PM, W>(rows + (bh * a.L + t) * a.Pp + p, a.Pp, p < a.Pp ? (int)min((int64_t)W, len - t) : 0, x);
     };
     if (chunks > 0) {
       store_parts<PM, WN, 3>(tX, NP / 2, st);
@@ -312,8 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       if (kAhead) load_scalars<W>(w, scal + 2 * kChunk + c0);
       wait_bar(&bars[kDoneU], ph, a.err, a.wait_ns);
       tc_fence_after();
-      load_cols<PM, W>(tZ, x);
-      if (SAVE) save_rows(a.e, i, x);
+      load_cols<PM, W>(tYa, x);
       if (!kAhead) load_scalars<W>(w, scal + 2 * kChunk + c0);
 #pragma unroll
       for (int c = 0; c < W; ++c) x[c] *= w[c];
@@ -323,7 +320,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       store_parts<PM, W, 3>(tUd, 32, w);
       ready(kU1 + up);
       store_parts<PM, W, SAVE ? 3 : 2>(tUy, 32, x);
-      ready(kU2);
+      if (SAVE) {  // e is still in its accumulator: read again, behind what the chain waits for
+        float e[W];
+        load_cols<PM, W>(tYa, e);
+        ready(kU2);
+        save_rows(a.e, i, e);
+      } else {
+        ready(kU2);
+      }
       wait_bar(&bars[kDoneD], ph, a.err, a.wait_ns);
       tc_fence_after();
       const float last = scal[3 * kChunk];

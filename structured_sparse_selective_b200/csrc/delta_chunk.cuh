@@ -138,4 +138,18 @@ __device__ __forceinline__ void load_scalars(float (&v)[W], const float *p) {
   }
 }
 
+// x[0 .. n) to rows of `ld` floats at `to`, a column each lane. Rows of PM floats and all W of
+// them: the addresses are constants apart.
+template <int PM, int W>
+__device__ __forceinline__ void store_rows(float *to, int64_t ld, int n, const float (&x)[W]) {
+  if (n >= W && ld == PM) {
+#pragma unroll
+    for (int c = 0; c < W; ++c) to[c * PM] = x[c];
+  } else if (n > 0) {
+#pragma unroll
+    for (int c = 0; c < W; ++c)
+      if (c < n) to[c * ld] = x[c];
+  }
+}
+
 }  // namespace pdssm

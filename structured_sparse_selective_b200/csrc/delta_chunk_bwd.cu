@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
   // Turn i works on chunk chunks - 1 - i.
   if (warp >= kLoader0) {
     const int tid = threadIdx.x - 32 * kLoader0;
+    const bool copies = wide && wide_v && a.N == NP && a.P - p0 >= PM;  // nothing is written by the threads themselves
     for (int i = 0; i < chunks; ++i) {
       const int s = i & 1, chunk = chunks - 1 - i;
       if (i >= 2) wait_bar(&bars[kFree0 + s], ((i >> 1) - 1) & 1, a.err, a.wait_ns);
@@ -89,10 +90,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
       load_tile<NP / 8, kChunkGroup, 16, 32 * kLoaders>(st, static_cast<B *>(a.k), row0, a.Hk, hk, a.N, 0, live, wide, tid);
       load_tile<NP / 8, kChunkGroup, 16, 32 * kLoaders>(st + Lay::kTile, static_cast<B *>(a.q), row0, a.Hk, hk, a.N, 0, live, wide, tid);
       load_tile<PM / 8, 16, 2 * PM, 32 * kLoaders>(st + Lay::kDyOff, static_cast<B *>(a.dy), row0, a.H, h, a.P, p0, live, wide_v, tid);
-      cp_async_commit();
-      cp_async_wait<0>();
-      fence_proxy_async_smem();
-      mbar_arrive(&bars[kFull0 + s]);
+      if (copies && live == kChunk) {  // on to the next chunk while the copies land
+        cp_async_arrive(&bars[kFull0 + s]);
+      } else {
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        mbar_arrive(&bars[kFull0 + s]);
+      }
     }
   } else if (warp == kIssuer) {
     constexpr uint32_t idS = idesc_bf16_f32(PM, kChunk, false, false), idT = idesc_bf16_f32(PM, kChunk, false, true),
@@ -104,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
       const uint64_t dk = smem_desc(sk, kChunkGroup, 128), dkt = smem_desc(sk, 128, kChunkGroup), dqt = smem_desc(sq, 128, kChunkGroup),
                      dtb = smem_desc(tb, 128, 1024), da = smem_desc(sa, 128, 1024);
       wait_bar(&bars[kFull0 + s], (i >> 1) & 1, a.err, a.wait_ns);
+      fence_proxy_async_smem();  // the loaders' writes, seen through the barrier, before the tensor core's reads
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
         wait_bar(&bars[kX + f], ph, a.err, a.wait_ns);
@@ -125,23 +131,22 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
         }
         __syncwarp();
       }
+      // du takes the place of X^T K^T, so all warps have to have read that
+      wait_bar(&bars[kR], ph, a.err, a.wait_ns);
+      wait_bar(&bars[kR + 1], ph, a.err, a.wait_ns);
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        wait_bar(&bars[kR + f], ph, a.err, a.wait_ns);
-        tc_fence_after();
-        if (elect_one()) {
+        for (int o = 0; o < 3; ++o)
 #pragma unroll
-          for (int o = 0; o < 3; ++o)
+          for (int q = 0; q <= o; ++q)
 #pragma unroll
-            for (int q = 0; q <= o; ++q)
-#pragma unroll
-              for (int ks = 2 * f; ks < 2 * f + 2; ++ks)
-                mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kD + (o - q) * 32 + 8 * ks, dtb + ((q * kSquare + 256 * ks) >> 4), idT,
-                            f + o + q + ks > 0);
-          if (f == 1) mma_commit(&bars[kDoneU]);
-        }
-        __syncwarp();
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kD + (o - q) * 32 + 8 * ks, dtb + ((q * kSquare + 256 * ks) >> 4), idT,
+                          o + q + ks > 0);
+        mma_commit(&bars[kDoneU]);
       }
+      __syncwarp();
       // kU also says that the half's parts of dY diag(exp G) are there
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
@@ -210,12 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
       const uint8_t *stage = smem + s * Lay::kStage;
       const float *scal = reinterpret_cast<const float *>(stage + Lay::kRecOff + Lay::kRec - kScalars);
       const __nv_bfloat16 *dy = reinterpret_cast<const __nv_bfloat16 *>(stage + Lay::kDyOff) + c0 * PM + row;
-      if (p < a.Pp) {
-        float *to = a.xcarry + ((bh * a.nC + chunk) * a.N + n0) * a.Pp + p;
-#pragma unroll
-        for (int n = 0; n < WN; ++n, to += a.Pp)
-          if (n0 + n < N) *to = st[n];
-      }
+      store_rows<PM, WN>(a.xcarry + ((bh * a.nC + chunk) * a.N + n0) * a.Pp + p, a.Pp, p < a.Pp ? N - n0 : 0, st);
       wait_bar(&bars[kDoneS], ph, a.err, a.wait_ns);
       tc_fence_after();
       float x[W], w[W];
@@ -249,15 +249,12 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
       {
         const int64_t t = (int64_t)chunk * kChunk + c0;
         const int n = (int)min((int64_t)W, len - t);
-        float *to = a.du + ((b * a.L + t) * a.H + h) * a.Pp + p;
         __nv_bfloat16 *tv = dv + t * step;
-        const int64_t wide_step = a.H * a.Pp;
-        if (p < a.Pp) {
+        store_rows<PM, W>(a.du + (bh * a.L + t) * a.Pp + p, a.Pp, p < a.Pp ? n : 0, x);
+        if (pin && n >= W) {
 #pragma unroll
-          for (int c = 0; c < W; ++c, to += wide_step)
-            if (c < n) *to = x[c];
-        }
-        if (pin) {
+          for (int c = 0; c < W; ++c, tv += step) *tv = __float2bfloat16_rn(w[c]);
+        } else if (pin) {
 #pragma unroll
           for (int c = 0; c < W; ++c, tv += step)
             if (c < n) *tv = __float2bfloat16_rn(w[c]);

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (8 * g + 4 * s < Pp) {
-            const int64_t i = at * Pp + 8 * g + 4 * s;
+                const int64_t i = (bh * a.L + t0 + c) * Pp + 8 * g + 4 * s;
             e[s] = *reinterpret_cast<const float4 *>(a.e + i);
             du[s] = *reinterpret_cast<const float4 *>(a.du + i);
             y[s] = *reinterpret_cast<const float4 *>(a.y32 + i);

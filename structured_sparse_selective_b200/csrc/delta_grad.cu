@@ -164,8 +164,9 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaArgs a, int l
       const int t = i / Pp, p = i % Pp;
       const int64_t at = (row0 + t) * a.H + h;
       Y[t * ldp + p] = (t < live && p < P) ? load_any(a.dy, at * P + p, bf) : 0.f;
-      U[t * ldp + p] = t < live ? a.e[at * Pp + p] : 0.f;
-      R[t * ldp + p] = t < live ? a.du[at * Pp + p] : 0.f;
+      const int64_t row = bh * a.L + t0 + t;
+      U[t * ldp + p] = t < live ? a.e[row * Pp + p] : 0.f;
+      R[t * ldp + p] = t < live ? a.du[row * Pp + p] : 0.f;
     }
     for (int i = tid; i < 32 * J * Pp; i += kThreads) {
       const int n = i / Pp, p = i % Pp;

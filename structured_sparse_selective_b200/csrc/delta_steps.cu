@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_kerne
   load_column<J>(st, a.h0 ? a.h0 + bh * a.N * a.P + col : nullptr, l, N, a.P, in);
   __syncthreads();
   T *y = static_cast<T *>(a.y) + (b * a.L * a.H + h) * a.P + col;
-  float *e_out = SAVE ? a.e + (b * a.L * a.H + h) * a.Pp + col : nullptr;
-  const int64_t step = a.H * (SAVE ? a.Pp : a.P);
+  float *e_out = SAVE ? a.e + bh * a.L * a.Pp + col : nullptr;
+  const int64_t step = SAVE ? a.Pp : a.H * a.P;
   if (len > 0) {
     load_rows<J>(k, Tile<J>(smem, cols, 0).k, l);
 #pragma unroll
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_bwd_k
   load_column<J>(x, a.dh_final ? a.dh_final + bh * a.N * a.P + col : nullptr, l, N, a.P, in);
   __syncthreads();
   T *dv = static_cast<T *>(a.dv) + (b * a.L * a.H + h) * a.P + col;
-  float *du_out = a.du + (b * a.L * a.H + h) * a.Pp + col;
+  float *du_out = a.du + bh * a.L * a.Pp + col;
   pair2 k[R], q[R];
   if (tiles > 0) {
     const Tile<J> tile(smem, cols, 0);
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_bwd_k
     load_rows<J>(q, tile.q + s * kRow, l);
   }
   const bool writes_du = l == 0 && room, writes_dv = l == 0 && in;
-  const int64_t step_du = a.H * a.Pp, step_dv = a.H * a.P;
+  const int64_t step_du = a.Pp, step_dv = a.H * a.P;
   T *dv_at = dv + (len - 1) * step_dv;
   du_out += (len - 1) * step_du;
   int buf = 0;

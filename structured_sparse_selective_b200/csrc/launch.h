@@ -129,7 +129,7 @@ struct DeltaArgs {
   void *dq, *dk, *dv, *dg, *dbeta;
   float *dh0;
   // workspace: states before each chunk and adjoints behind it [Bt][H][nC][N][Pp],
-  // e_t and du_t [Bt][L][H][Pp]
+  // e_t and du_t [Bt][H][L][Pp] (a chunk's rows of a head lie together)
   float *carry, *xcarry, *e, *du;
   float *y32;  // chunked: y_t before its rounding, and carry has [nC + 1] states
   // chunked kernels: error word, a record for each chunk of each value head
