@@ -24,7 +24,7 @@
 // that four of the eight state warps have written, while the others still write. Roles (12 warps): 8 keep the state (fp32, in
 // registers: a row's n-range each) and do all elementwise work, a ninth issues the
 // products, two bring K, Q (16-byte cp.async into the operand order), V and the record
-// (one bulk copy) a chunk ahead into two stages, and one writes y from shared memory.
+// (bulk copies) ahead into two or three stages, and one writes y from shared memory.
 // Every wait is bounded; after a timeout a role goes on without waiting, on data inside
 // its buffers, and the last one waits for the tensor core before tensor memory is freed.
 #include <algorithm>
@@ -43,7 +43,7 @@ constexpr int kStateWarps = 8, kIssuer = 8, kLoader0 = 9, kLoaders = 2, kWriter 
 constexpr int kThreads = 32 * (kWriter + 1);
 
 // kH, kR, kU: [half], from the four warps that have that half of a row's columns.
-enum Bar { kFull0, kFull1, kFree0, kFree1, kH, kR = kH + 2, kU1 = kR + 2, kU2 = kU1 + 2, kDoneS, kDoneU, kDoneD, kDoneY, kOut, kOutFree, kEnd, kBars };
+enum Bar { kFull, kFree = kFull + 3, kH = kFree + 3, kR = kH + 2, kU1 = kR + 2, kU2 = kU1 + 2, kRead, kDoneS, kDoneU, kDoneD, kDoneY, kOut, kOutFree, kEnd, kBars };
 
 template <int NP, int PM, bool SAVE>
 struct Layout {
@@ -62,7 +62,9 @@ struct Layout {
   static constexpr int kRec = (3 + delta_a_parts(SAVE)) * kSquare + kScalars;
   static constexpr int kQ = (NP / 8) * kChunkGroup, kV = kChunk * PM * 2;  // V and Y: [step][p]
   static constexpr int kVOff = 2 * kQ, kRecOff = kVOff + kV, kStage = kRecOff + kRec;
-  static constexpr int kYOff = 2 * kStage, kBarOff = kYOff + (SAVE ? 0 : kV), kBytes = kBarOff + 8 * kBars + 16;
+  // three stages where they fit: loads have then two chunks' time
+  static constexpr int kY = SAVE ? 0 : kV, kStages = 3 * kStage + kY + 256 <= 227 * 1024 ? 3 : 2;
+  static constexpr int kYOff = kStages * kStage, kBarOff = kYOff + kY, kBytes = kBarOff + 8 * kBars + 16;
   // a thread's share of a row: W of 64 steps, WN of NP state values
   static constexpr int kParts = 256 / PM, W = kChunk / kParts, WN = NP / kParts;
 };
@@ -71,7 +73,6 @@ template <int NP, int PM, bool SAVE>
 __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, bool wide, bool wide_v) {
   using Lay = Layout<NP, PM, SAVE>;
   constexpr int W = Lay::W, WN = Lay::WN;
-  constexpr bool kAhead = W == 16;
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::kBarOff);
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + kBars);
@@ -83,8 +84,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i) {
-      const bool half = i >= kH && i < kU2, state = i == kFree0 || i == kFree1 || i == kU2 || i == kOut;
-      mbar_init(&bars[i], half ? kStateWarps / 2 : state ? kStateWarps : (i == kFull0 || i == kFull1) ? 32 * kLoaders + 1 : 1);
+      const bool half = i >= kH && i < kU2, state = (i >= kFree && i < kH) || i == kU2 || i == kRead || i == kOut;
+      mbar_init(&bars[i], half ? kStateWarps / 2 : state ? kStateWarps : i < kFree ? 32 * kLoaders + 1 : 1);
     }
     mbar_fence_init();
   }
@@ -128,35 +129,38 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
   } else if (warp >= kLoader0) {
     const int tid = threadIdx.x - 32 * kLoader0;
     const bool copies = wide && wide_v && a.N == NP && a.P - p0 >= PM;  // nothing is written by the threads themselves
-    for (int i = 0; i < chunks; ++i) {
-      const int s = i & 1;
-      if (i >= 2) wait_bar(&bars[kFree0 + s], ((i >> 1) - 1) & 1, a.err, a.wait_ns);
+    using B = const __nv_bfloat16;
+    for (int i = 0, s = 0, turn = 0; i < chunks; ++i) {
+      if (turn) wait_bar(&bars[kFree + s], (turn - 1) & 1, a.err, a.wait_ns);
       uint8_t *st = smem + s * Lay::kStage;
-      if (tid == 0) {
-        const uint8_t *rec = a.records + (bh * a.nC + i) * a.rec_bytes;
-        uint64_t *full = &bars[kFull0 + s];
-        mbar_expect_tx(full, Lay::kRec);
-        if (SAVE) {  // the record has Tb between Te and A
-          bulk_load(st + Lay::kRecOff, rec, 3 * kSquare, full);
-          bulk_load(st + Lay::kRecOff + 3 * kSquare, rec + 6 * kSquare, 3 * kSquare + kScalars, full);
-        } else {
-          bulk_load(st + Lay::kRecOff, rec, Lay::kRec, full);
-        }
-      }
+      uint64_t *full = &bars[kFull + s];
       const int live = (int)min((int64_t)kChunk, len - (int64_t)i * kChunk);
       const int64_t row0 = b * a.L + (int64_t)i * kChunk;
-      using B = const __nv_bfloat16;
+      const bool whole = copies && live == kChunk;
+      if (tid < 32) {
+        const uint8_t *rec = a.records + (bh * a.nC + i) * a.rec_bytes;
+        if (lane == 0) {
+          mbar_expect_tx(full, Lay::kRec);
+          if (SAVE) {  // the record has Tb between Te and A
+            bulk_load(st + Lay::kRecOff, rec, 3 * kSquare, full);
+            bulk_load(st + Lay::kRecOff + 3 * kSquare, rec + 6 * kSquare, 3 * kSquare + kScalars, full);
+          } else {
+            bulk_load(st + Lay::kRecOff, rec, Lay::kRec, full);
+          }
+        }
+      }
       load_tile<NP / 8, kChunkGroup, 16, 32 * kLoaders>(st, static_cast<B *>(a.k), row0, a.Hk, hk, a.N, 0, live, wide, tid);
       load_tile<NP / 8, kChunkGroup, 16, 32 * kLoaders>(st + Lay::kQ, static_cast<B *>(a.q), row0, a.Hk, hk, a.N, 0, live, wide, tid);
       load_tile<PM / 8, 16, 2 * PM, 32 * kLoaders>(st + Lay::kVOff, static_cast<B *>(a.v), row0, a.H, h, a.P, p0, live, wide_v, tid);
-      if (copies && live == kChunk) {  // on to the next chunk while the copies land
-        cp_async_arrive(&bars[kFull0 + s]);
+      if (whole) {
+        cp_async_arrive(full);  // on to the next chunk while the copies land
       } else {
         cp_async_commit();
         cp_async_wait<0>();
         fence_proxy_async_smem();
-        mbar_arrive(&bars[kFull0 + s]);
+        mbar_arrive(full);
       }
+      if (++s == Lay::kStages) s = 0, ++turn;
     }
   } else if (warp == kIssuer) {
     // The whole warp goes through the loop and one lane issues: descriptors and addresses
@@ -164,12 +168,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
     // twice the product itself).
     constexpr uint32_t idS = idesc_bf16_f32(PM, kChunk, false, false), idD = idesc_bf16_f32(PM, NP, false, true);
     const uint32_t base = smem_u32(smem);
-    for (int i = 0; i < chunks; ++i) {
-      const int s = i & 1;
+    for (int i = 0, s = 0, turn = 0; i < chunks; ++i) {
       const uint32_t ph = i & 1, sk = base + s * Lay::kStage, sq = sk + Lay::kQ, te = sk + Lay::kRecOff, sa = te + 3 * kSquare;
       const uint64_t dk = smem_desc(sk, kChunkGroup, 128), dq = smem_desc(sq, kChunkGroup, 128), dkt = smem_desc(sk, 128, kChunkGroup),
                      dte = smem_desc(te, 1024, 128), da = smem_desc(sa, 1024, 128);
-      wait_bar(&bars[kFull0 + s], (i >> 1) & 1, a.err, a.wait_ns);
+      wait_bar(&bars[kFull + s], turn & 1, a.err, a.wait_ns);
       fence_proxy_async_smem();  // the loaders' writes, seen through the barrier, before the tensor core's reads
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
         __syncwarp();
       }
       // Q H into Yh, once the chunk before has been read out of it
-      if (i >= 1) wait_bar(&bars[kFree0 + (s ^ 1)], ((i - 1) >> 1) & 1, a.err, a.wait_ns);
+      if (i >= 1) wait_bar(&bars[kRead], (i - 1) & 1, a.err, a.wait_ns);
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -244,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
         mma_commit(&bars[kDoneY]);
       }
       __syncwarp();
+      if (++s == Lay::kStages) s = 0, ++turn;
     }
     if (chunks > 0) {
       if (elect_one()) mma_commit(&bars[kEnd]);
@@ -280,38 +284,37 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       const int64_t t = (int64_t)i * kChunk + c0;
       store_rows<PM, W>(rows + (bh * a.L + t) * a.Pp + p, a.Pp, p < a.Pp ? (int)min((int64_t)W, len - t) : 0, x);
     };
+    // the thread's values of chunk i, two steps a register: read a product ahead of their use
+    uint32_t vv[W / 2];
+    const auto fetch_v = [&](int s, int turn) {
+      wait_bar(&bars[kFull + s], turn & 1, a.err, a.wait_ns);
+      const uint16_t *v = reinterpret_cast<const uint16_t *>(smem + s * Lay::kStage + Lay::kVOff) + c0 * PM + row;
+#pragma unroll
+      for (int c = 0; c < W / 2; ++c) vv[c] = v[2 * c * PM] | ((uint32_t)v[(2 * c + 1) * PM] << 16);
+    };
     if (chunks > 0) {
+      fetch_v(0, 0);
       store_parts<PM, WN, 3>(tX, NP / 2, st);
       ready(kH + up);
     }
-    for (int i = 0; i < chunks; ++i) {
-      const int s = i & 1;
+    for (int i = 0, s = 0, next = 0, turn = 0; i < chunks; ++i, s = next) {
       const uint32_t ph = i & 1;
       const uint8_t *stage = smem + s * Lay::kStage;
       const float *scal = reinterpret_cast<const float *>(stage + Lay::kRecOff + Lay::kRec - kScalars);
-      const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(stage + Lay::kVOff) + c0 * PM + row;
       if (SAVE) save_state(i);
-      wait_bar(&bars[kFull0 + s], (i >> 1) & 1, a.err, a.wait_ns);
-      // what does not wait for a product is read ahead of it, where registers allow
-      float x[W], w[W], vv[kAhead ? W : 1];
-      if (kAhead) {
-        load_scalars<W>(w, scal + c0);
-#pragma unroll
-        for (int c = 0; c < W; ++c) vv[kAhead ? c : 0] = __bfloat162float(v[c * PM]);
-      }
+      float x[W], w[W];
+      load_scalars<W>(w, scal + c0);
       wait_bar(&bars[kDoneS], ph, a.err, a.wait_ns);
       tc_fence_after();
       load_cols<PM, W>(tZ, x);
-      if (!kAhead) load_scalars<W>(w, scal + c0);
 #pragma unroll
-      for (int c = 0; c < W; ++c) x[c] = fmaf(-w[c], x[c], kAhead ? vv[kAhead ? c : 0] : __bfloat162float(v[c * PM]));
+      for (int c = 0; c < W; ++c) x[c] = fmaf(-w[c], x[c], c & 1 ? high_half(vv[c / 2]) : low_half(vv[c / 2]));
       store_parts<PM, W, 3>(tR, 32, x);
       ready(kR + up);
-      if (kAhead) load_scalars<W>(w, scal + 2 * kChunk + c0);
+      load_scalars<W>(w, scal + 2 * kChunk + c0);
       wait_bar(&bars[kDoneU], ph, a.err, a.wait_ns);
       tc_fence_after();
       load_cols<PM, W>(tYa, x);
-      if (!kAhead) load_scalars<W>(w, scal + 2 * kChunk + c0);
 #pragma unroll
       for (int c = 0; c < W; ++c) x[c] *= w[c];
       load_scalars<W>(w, scal + kChunk + c0);
@@ -328,6 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       } else {
         ready(kU2);
       }
+      if (++next == Lay::kStages) next = 0, ++turn;
+      if (i + 1 < chunks) fetch_v(next, turn);
       wait_bar(&bars[kDoneD], ph, a.err, a.wait_ns);
       tc_fence_after();
       const float last = scal[3 * kChunk];
@@ -355,35 +360,27 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
         wait_bar(&bars[kDoneY], ph, a.err, a.wait_ns);
         tc_fence_after();
       }
-      if (!SAVE) {
-        load_cols<PM, W>(tYa, w);
-        load_cols<PM, W>(tYh, x);
+      // y's scalars are read before the stage goes back to the loaders
+      float g[W];
+      load_scalars<W>(g, scal + c0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kFree + s]);
+      load_cols<PM, W>(tYa, w);
+      load_cols<PM, W>(tYh, x);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kRead]);
+#pragma unroll
+      for (int c = 0; c < W; ++c) x[c] = fmaf(a.scale * g[c], x[c], w[c]);
+      if (SAVE) {
+        save_rows(a.y32, i, x);
+      } else {
         if (i >= 1) wait_bar(&bars[kOutFree], (i - 1) & 1, a.err, a.wait_ns);
         __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(smem + Lay::kYOff) + c0 * PM + row;
 #pragma unroll
-        for (int c = 0; c < W; c += 4) {
-          const float4 g = *reinterpret_cast<const float4 *>(scal + c0 + c);
-          out[c * PM] = __float2bfloat16_rn(fmaf(a.scale * g.x, x[c], w[c]));
-          out[(c + 1) * PM] = __float2bfloat16_rn(fmaf(a.scale * g.y, x[c + 1], w[c + 1]));
-          out[(c + 2) * PM] = __float2bfloat16_rn(fmaf(a.scale * g.z, x[c + 2], w[c + 2]));
-          out[(c + 3) * PM] = __float2bfloat16_rn(fmaf(a.scale * g.w, x[c + 3], w[c + 3]));
-        }
-      }
-      if (SAVE) {
-        load_cols<PM, W>(tYh, x);
-        load_scalars<W>(w, scal + c0);
-#pragma unroll
-        for (int c = 0; c < W; ++c) x[c] *= a.scale * w[c];
-        load_cols<PM, W>(tYa, w);
-#pragma unroll
-        for (int c = 0; c < W; ++c) x[c] += w[c];
-        save_rows(a.y32, i, x);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bars[kFree0 + s]);
-        if (!SAVE) mbar_arrive(&bars[kOut]);
+        for (int c = 0; c < W; ++c) out[c * PM] = __float2bfloat16_rn(x[c]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kOut]);
       }
     }
     if (SAVE) save_state(chunks);

@@ -106,18 +106,22 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, uint32_
   return sm100::mbar_try_wait(bar, parity) || wait_slow(bar, parity, err, limit_ns);
 }
 
-// `n` fp32 values as packed bf16 parts 0 .. PARTS - 1 into columns col, col + stride, ...
-// of the thread's row (col already at the thread's or the warp's part).
+// W fp32 values as packed bf16 parts 0 .. PARTS - 1 into columns col, col + stride, ... of the
+// thread's row (col already at the thread's or the warp's part), 16 values at a time: the parts
+// of 64 at once would take 96 registers.
 template <int PM, int W, int PARTS>
 __device__ __forceinline__ void store_parts(uint32_t taddr, int stride, const float (&v)[W]) {
-  uint32_t p[3][W / 2];
 #pragma unroll
-  for (int i = 0; i < W / 2; ++i) {
-    if (PARTS == 3) split3(v[2 * i], v[2 * i + 1], p[0][i], p[1][i], p[2][i]);
-    else split2(v[2 * i], v[2 * i + 1], p[0][i], p[1][i]);
+  for (int j = 0; j < W; j += 16) {
+    uint32_t p[3][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (PARTS == 3) split3(v[j + 2 * i], v[j + 2 * i + 1], p[0][i], p[1][i], p[2][i]);
+      else split2(v[j + 2 * i], v[j + 2 * i + 1], p[0][i], p[1][i]);
+    }
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) sm100::TmemIo<PM, 8, W / 2>::st(taddr + q * stride + j / 2, p[q]);
   }
-#pragma unroll
-  for (int q = 0; q < PARTS; ++q) sm100::TmemIo<PM, W / 2>::st(taddr + q * stride, p[q]);
 }
 
 template <int PM, int W>

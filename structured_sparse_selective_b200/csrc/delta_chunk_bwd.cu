@@ -26,7 +26,7 @@ constexpr int kStateWarps = 8, kIssuer = 8, kLoader0 = 9, kLoaders = 2;
 constexpr int kThreads = 32 * (kLoader0 + kLoaders);
 
 // kX, kR, kU: [half], from the four warps that have that half of a row's columns.
-enum Bar { kFull0, kFull1, kFree0, kFree1, kX, kR = kX + 2, kU = kR + 2, kDoneS = kU + 2, kDoneU, kDoneD, kEnd, kBars };
+enum Bar { kFull, kFree = kFull + 3, kX = kFree + 3, kR = kX + 2, kU = kR + 2, kDoneS = kU + 2, kDoneU, kDoneD, kEnd, kBars };
 
 template <int NP, int PM>
 struct Layout {
@@ -38,7 +38,8 @@ struct Layout {
   static_assert(kY + 32 <= kCols, "columns");
   static constexpr int kTile = (NP / 8) * kChunkGroup, kDy = kChunk * PM * 2, kRec = 6 * kSquare + kScalars;
   static constexpr int kDyOff = 2 * kTile, kRecOff = kDyOff + kDy, kStage = kRecOff + kRec;
-  static constexpr int kBarOff = 2 * kStage, kBytes = kBarOff + 8 * kBars + 16;
+  static constexpr int kStages = 3 * kStage + 256 <= 227 * 1024 ? 3 : 2;  // three where they fit
+  static constexpr int kBarOff = kStages * kStage, kBytes = kBarOff + 8 * kBars + 16;
   static constexpr int kParts = 256 / PM, W = kChunk / kParts, WN = NP / kParts;
 };
 
@@ -57,8 +58,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i) {
-      const bool half = i >= kX && i < kDoneS, state = i == kFree0 || i == kFree1;
-      mbar_init(&bars[i], half ? kStateWarps / 2 : state ? kStateWarps : (i == kFull0 || i == kFull1) ? 32 * kLoaders + 1 : 1);
+      const bool half = i >= kX && i < kDoneS, state = i >= kFree && i < kX;
+      mbar_init(&bars[i], half ? kStateWarps / 2 : state ? kStateWarps : i < kFree ? 32 * kLoaders + 1 : 1);
     }
     mbar_fence_init();
   }
@@ -75,40 +76,43 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
   if (warp >= kLoader0) {
     const int tid = threadIdx.x - 32 * kLoader0;
     const bool copies = wide && wide_v && a.N == NP && a.P - p0 >= PM;  // nothing is written by the threads themselves
-    for (int i = 0; i < chunks; ++i) {
-      const int s = i & 1, chunk = chunks - 1 - i;
-      if (i >= 2) wait_bar(&bars[kFree0 + s], ((i >> 1) - 1) & 1, a.err, a.wait_ns);
+    using B = const __nv_bfloat16;
+    for (int i = 0, s = 0, turn = 0; i < chunks; ++i) {
+      const int chunk = chunks - 1 - i;
+      if (turn) wait_bar(&bars[kFree + s], (turn - 1) & 1, a.err, a.wait_ns);
       uint8_t *st = smem + s * Lay::kStage;
-      if (tid == 0) {
-        uint64_t *full = &bars[kFull0 + s];
-        mbar_expect_tx(full, Lay::kRec);
-        bulk_load(st + Lay::kRecOff, a.records + (bh * a.nC + chunk) * a.rec_bytes + 3 * kSquare, Lay::kRec, full);
-      }
+      uint64_t *full = &bars[kFull + s];
       const int live = (int)min((int64_t)kChunk, len - (int64_t)chunk * kChunk);
       const int64_t row0 = b * a.L + (int64_t)chunk * kChunk;
-      using B = const __nv_bfloat16;
+      const bool whole = copies && live == kChunk;
+      if (tid < 32) {
+        if (lane == 0) {
+          mbar_expect_tx(full, Lay::kRec);
+          bulk_load(st + Lay::kRecOff, a.records + (bh * a.nC + chunk) * a.rec_bytes + 3 * kSquare, Lay::kRec, full);
+        }
+      }
       load_tile<NP / 8, kChunkGroup, 16, 32 * kLoaders>(st, static_cast<B *>(a.k), row0, a.Hk, hk, a.N, 0, live, wide, tid);
       load_tile<NP / 8, kChunkGroup, 16, 32 * kLoaders>(st + Lay::kTile, static_cast<B *>(a.q), row0, a.Hk, hk, a.N, 0, live, wide, tid);
       load_tile<PM / 8, 16, 2 * PM, 32 * kLoaders>(st + Lay::kDyOff, static_cast<B *>(a.dy), row0, a.H, h, a.P, p0, live, wide_v, tid);
-      if (copies && live == kChunk) {  // on to the next chunk while the copies land
-        cp_async_arrive(&bars[kFull0 + s]);
+      if (whole) {
+        cp_async_arrive(full);  // on to the next chunk while the copies land
       } else {
         cp_async_commit();
         cp_async_wait<0>();
         fence_proxy_async_smem();
-        mbar_arrive(&bars[kFull0 + s]);
+        mbar_arrive(full);
       }
+      if (++s == Lay::kStages) s = 0, ++turn;
     }
   } else if (warp == kIssuer) {
     constexpr uint32_t idS = idesc_bf16_f32(PM, kChunk, false, false), idT = idesc_bf16_f32(PM, kChunk, false, true),
                        idD = idesc_bf16_f32(PM, NP, false, true);
     const uint32_t base = smem_u32(smem);
-    for (int i = 0; i < chunks; ++i) {
-      const int s = i & 1;
+    for (int i = 0, s = 0, turn = 0; i < chunks; ++i) {
       const uint32_t ph = i & 1, sk = base + s * Lay::kStage, sq = sk + Lay::kTile, tb = sk + Lay::kRecOff, sa = tb + 3 * kSquare;
       const uint64_t dk = smem_desc(sk, kChunkGroup, 128), dkt = smem_desc(sk, 128, kChunkGroup), dqt = smem_desc(sq, 128, kChunkGroup),
                      dtb = smem_desc(tb, 128, 1024), da = smem_desc(sa, 128, 1024);
-      wait_bar(&bars[kFull0 + s], (i >> 1) & 1, a.err, a.wait_ns);
+      wait_bar(&bars[kFull + s], turn & 1, a.err, a.wait_ns);
       fence_proxy_async_smem();  // the loaders' writes, seen through the barrier, before the tensor core's reads
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
@@ -164,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
         }
         __syncwarp();
       }
+      if (++s == Lay::kStages) s = 0, ++turn;
     }
     if (chunks > 0) {
       if (elect_one()) mma_commit(&bars[kEnd]);
@@ -195,9 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
       if (lane == 0) mbar_arrive(&bars[which]);
     };
     // dY of turn i as it is, an operand of dY^T A
-    const auto store_dy = [&](int i) {
-      const int s = i & 1;
-      wait_bar(&bars[kFull0 + s], (i >> 1) & 1, a.err, a.wait_ns);
+    const auto store_dy = [&](int s, int turn) {
+      wait_bar(&bars[kFull + s], turn & 1, a.err, a.wait_ns);
       const uint16_t *dy = reinterpret_cast<const uint16_t *>(smem + s * Lay::kStage + Lay::kDyOff) + c0 * PM + row;
       uint32_t r[W / 2];
 #pragma unroll
@@ -206,11 +210,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
     };
     if (chunks > 0) {
       store_parts<PM, WN, 3>(tX, NP / 2, st);
-      store_dy(0);
+      store_dy(0, 0);
       ready(kX + up);
     }
-    for (int i = 0; i < chunks; ++i) {
-      const int s = i & 1, chunk = chunks - 1 - i;
+    for (int i = 0, s = 0, next = 0, turn = 0; i < chunks; ++i, s = next) {
+      const int chunk = chunks - 1 - i;
       const uint32_t ph = i & 1;
       const uint8_t *stage = smem + s * Lay::kStage;
       const float *scal = reinterpret_cast<const float *>(stage + Lay::kRecOff + Lay::kRec - kScalars);
@@ -276,10 +280,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kFree0 + s]);
+      if (lane == 0) mbar_arrive(&bars[kFree + s]);
+      if (++next == Lay::kStages) next = 0, ++turn;
       if (i + 1 < chunks) {
         store_parts<PM, WN, 3>(tX, NP / 2, st);
-        store_dy(i + 1);
+        store_dy(next, turn);
         ready(kX + up);
       }
     }

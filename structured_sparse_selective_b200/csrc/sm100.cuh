@@ -374,12 +374,12 @@ __device__ __forceinline__ void bulk_load(void *smem_dst, const void *gmem_src, 
 
 // Loads and stores of W consecutive 32-bit columns a thread. M = 128: every lane its own
 // row (32x32b). M = 64: the rows are in the lower 16 lanes of each quarter; threads 0-15
-// of the warp reach columns [c, c + W), threads 16-31 the same lanes at [c + W, c + 2 W).
-template <int M, int W>
+// of the warp reach columns [c, c + W), threads 16-31 the same lanes at [c + SPLIT, c + SPLIT + W).
+template <int M, int W, int SPLIT = W>
 struct TmemIo;
 
-template <>
-struct TmemIo<128, 8> {
+template <int SPLIT>
+struct TmemIo<128, 8, SPLIT> {
   static __device__ __forceinline__ void ld(uint32_t taddr, uint32_t *v) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
@@ -392,8 +392,8 @@ struct TmemIo<128, 8> {
                  : "memory");
   }
 };
-template <>
-struct TmemIo<128, 16> {
+template <int SPLIT>
+struct TmemIo<128, 16, SPLIT> {
   static __device__ __forceinline__ void ld(uint32_t taddr, uint32_t *v) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
@@ -409,8 +409,8 @@ struct TmemIo<128, 16> {
                  : "memory");
   }
 };
-template <>
-struct TmemIo<128, 32> {
+template <int SPLIT>
+struct TmemIo<128, 32, SPLIT> {
   static __device__ __forceinline__ void ld(uint32_t taddr, uint32_t *v) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
@@ -430,39 +430,39 @@ struct TmemIo<128, 32> {
                  : "memory");
   }
 };
-template <>
-struct TmemIo<64, 8> {
+template <int SPLIT>
+struct TmemIo<64, 8, SPLIT> {
   static __device__ __forceinline__ void ld(uint32_t taddr, uint32_t *v) {
     asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "r"(taddr), "n"(8)
+                 : "r"(taddr), "n"(SPLIT)
                  : "memory");
   }
   static __device__ __forceinline__ void st(uint32_t taddr, const uint32_t *v) {
-    asm volatile("tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9};" ::"r"(taddr), "n"(8),
+    asm volatile("tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9};" ::"r"(taddr), "n"(SPLIT),
                  "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
   }
 };
-template <>
-struct TmemIo<64, 16> {
+template <int SPLIT>
+struct TmemIo<64, 16, SPLIT> {
   static __device__ __forceinline__ void ld(uint32_t taddr, uint32_t *v) {
     asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], %17;"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
                  "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
                  "=r"(v[15])
-                 : "r"(taddr), "n"(16)
+                 : "r"(taddr), "n"(SPLIT)
                  : "memory");
   }
   static __device__ __forceinline__ void st(uint32_t taddr, const uint32_t *v) {
     asm volatile("tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17};" ::"r"(taddr),
-                 "n"(16), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+                 "n"(SPLIT), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
                  "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
                  : "memory");
   }
 };
-template <>
-struct TmemIo<64, 32> {
+template <int SPLIT>
+struct TmemIo<64, 32, SPLIT> {
   static __device__ __forceinline__ void ld(uint32_t taddr, uint32_t *v) {
     asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32], %33;"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
@@ -470,12 +470,12 @@ struct TmemIo<64, 32> {
                  "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]),
                  "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]),
                  "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-                 : "r"(taddr), "n"(32)
+                 : "r"(taddr), "n"(SPLIT)
                  : "memory");
   }
   static __device__ __forceinline__ void st(uint32_t taddr, const uint32_t *v) {
     asm volatile("tcgen05.st.sync.aligned.16x32bx2.x32.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33};" ::"r"(taddr),
-                 "n"(32), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+                 "n"(SPLIT), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
                  "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
                  "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
                  "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
