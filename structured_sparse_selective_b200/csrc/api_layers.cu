@@ -78,7 +78,7 @@ pdssm_status run_norm(const pdssm_norm_problem *pb, QkNormArgs &a, int64_t rows,
 struct DeltaPlan {
   int64_t rows, slices, Pp, C, nC;
   bool chunked;  // by chunks on the tensor cores
-  size_t o_carry, o_xcarry, o_e, o_du, o_y32, o_rec, fwd_bytes, bwd_bytes;
+  size_t o_carry, o_xcarry, o_e, o_du, o_dyy, o_rec, fwd_bytes, bwd_bytes;
 };
 
 constexpr size_t kErrBytes = 256;
@@ -108,14 +108,14 @@ pdssm_status plan_delta(const pdssm_delta_problem *pb, DeltaPlan *pl) {
   p.chunked = chunks_apply(pb);
   p.C = p.chunked ? kChunk : delta_grad_chunk();
   p.nC = (pb->seqlen + p.C - 1) / p.C;
-  // backward: error word, states (chunked: one more a sequence), adjoints, e, du; chunked: y and the records
+  // backward: error word, states (chunked: one more a sequence), adjoints, e, du; chunked: <dy, y> and the records
   const size_t state = (size_t)(pb->N * p.Pp) * 4, steps = (size_t)(p.rows * pb->heads * p.Pp) * 4;
   size_t o = p.chunked ? kErrBytes : 0;
   p.o_carry = o; o = align256(o + (size_t)(p.slices * (p.nC + (p.chunked ? 1 : 0))) * state);
   p.o_xcarry = o; o = align256(o + (size_t)(p.slices * p.nC) * state);
   p.o_e = o; o = align256(o + steps);
   p.o_du = o; o = align256(o + steps);
-  p.o_y32 = o; o = align256(o + (p.chunked ? steps : 0));
+  p.o_dyy = o; o = align256(o + (p.chunked ? (size_t)(p.rows * pb->heads) * 16 : 0));
   p.o_rec = o; o = align256(o + (p.chunked ? (size_t)(p.slices * p.nC * delta_record_bytes(true)) : 0));
   p.bwd_bytes = o;
   p.fwd_bytes = p.chunked ? kErrBytes + (size_t)(p.slices * p.nC * delta_record_bytes(false)) : 0;
@@ -280,7 +280,7 @@ pdssm_status pdssm_delta_bwd(const pdssm_delta_problem *pb, const void *q, const
   a.du = reinterpret_cast<float *>(base + p.o_du);
   if (p.chunked) {
     a.err = static_cast<uint32_t *>(workspace);
-    a.y32 = reinterpret_cast<float *>(base + p.o_y32);
+    a.dyy = reinterpret_cast<float *>(base + p.o_dyy);
     a.records = reinterpret_cast<uint8_t *>(base + p.o_rec);
     a.rec_bytes = delta_record_bytes(true);
     a.wait_ns = wait_limit(pb);

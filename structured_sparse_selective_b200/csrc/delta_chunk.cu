@@ -17,7 +17,7 @@
 // the state, so that it is an fp32 state; two parts (16 bits) where only y is
 // reached, which is rounded to bf16 itself.
 // SAVE (the forward of a backward pass) keeps three everywhere, since gradients of the
-// gates are differences of fp32 sums over y.
+// gates are sums of <dy, y> in fp32; it writes these, e and the states instead of y.
 //
 // The chain K H -> Te -> K^T u is what a sequence waits for; it runs once a chunk, and the
 // other products fill the pipe in its pauses. A product starts on the half of its depth
@@ -43,7 +43,7 @@ constexpr int kStateWarps = 8, kIssuer = 8, kLoader0 = 9, kLoaders = 2, kWriter 
 constexpr int kThreads = 32 * (kWriter + 1);
 
 // kH, kR, kU: [half], from the four warps that have that half of a row's columns.
-enum Bar { kFull, kFree = kFull + 3, kH = kFree + 3, kR = kH + 2, kU1 = kR + 2, kU2 = kU1 + 2, kRead, kDoneS, kDoneU, kDoneD, kDoneY, kOut, kOutFree, kEnd, kBars };
+enum Bar { kFull, kFree = kFull + 3, kH = kFree + 3, kR = kH + 2, kU1 = kR + 2, kU2 = kU1 + 2, kRead, kDoneS, kDoneU, kDoneD, kDoneY, kOut, kOutFree, kDyFull, kDyFree, kEnd, kBars };
 
 template <int NP, int PM, bool SAVE>
 struct Layout {
@@ -62,8 +62,8 @@ struct Layout {
   static constexpr int kRec = (3 + delta_a_parts(SAVE)) * kSquare + kScalars;
   static constexpr int kQ = (NP / 8) * kChunkGroup, kV = kChunk * PM * 2;  // V and Y: [step][p]
   static constexpr int kVOff = 2 * kQ, kRecOff = kVOff + kV, kStage = kRecOff + kRec;
-  // three stages where they fit: loads have then two chunks' time
-  static constexpr int kY = SAVE ? 0 : kV, kStages = 3 * kStage + kY + 256 <= 227 * 1024 ? 3 : 2;
+  // three stages where they fit: loads have then two chunks' time; behind them y, or (SAVE) dY
+  static constexpr int kY = kV, kStages = 3 * kStage + kY + 256 <= 227 * 1024 ? 3 : 2;
   static constexpr int kYOff = kStages * kStage, kBarOff = kYOff + kY, kBytes = kBarOff + 8 * kBars + 16;
   // a thread's share of a row: W of 64 steps, WN of NP state values
   static constexpr int kParts = 256 / PM, W = kChunk / kParts, WN = NP / kParts;
@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i) {
-      const bool half = i >= kH && i < kU2, state = (i >= kFree && i < kH) || i == kU2 || i == kRead || i == kOut;
-      mbar_init(&bars[i], half ? kStateWarps / 2 : state ? kStateWarps : i < kFree ? 32 * kLoaders + 1 : 1);
+      const bool half = i >= kH && i < kU2, state = (i >= kFree && i < kH) || i == kU2 || i == kRead || i == kOut || i == kDyFree;
+      mbar_init(&bars[i], half ? kStateWarps / 2 : state ? kStateWarps : i < kFree ? 32 * kLoaders + 1 : i == kDyFull ? 32 * kLoaders : 1);
     }
     mbar_fence_init();
   }
@@ -130,6 +130,20 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
     const int tid = threadIdx.x - 32 * kLoader0;
     const bool copies = wide && wide_v && a.N == NP && a.P - p0 >= PM;  // nothing is written by the threads themselves
     using B = const __nv_bfloat16;
+    // SAVE: dY of chunk i, which is wanted at the chunk's end, comes behind the next chunk's stage
+    const auto load_dy = [&](int i) {
+      if (i >= 1) wait_bar(&bars[kDyFree], (i - 1) & 1, a.err, a.wait_ns);
+      const int live = (int)min((int64_t)kChunk, len - (int64_t)i * kChunk);
+      load_tile<PM / 8, 16, 2 * PM, 32 * kLoaders>(smem + Lay::kYOff, static_cast<B *>(a.dy), b * a.L + (int64_t)i * kChunk, a.H, h, a.P,
+                                                   p0, live, wide_v, tid);
+      if (copies && live == kChunk) {
+        cp_async_arrive(&bars[kDyFull]);
+      } else {
+        cp_async_commit();
+        cp_async_wait<0>();
+        mbar_arrive(&bars[kDyFull]);
+      }
+    };
     for (int i = 0, s = 0, turn = 0; i < chunks; ++i) {
       if (turn) wait_bar(&bars[kFree + s], (turn - 1) & 1, a.err, a.wait_ns);
       uint8_t *st = smem + s * Lay::kStage;
@@ -161,7 +175,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
         mbar_arrive(full);
       }
       if (++s == Lay::kStages) s = 0, ++turn;
+      if (SAVE && i >= 1) load_dy(i - 1);
     }
+    if (SAVE && chunks > 0) load_dy(chunks - 1);
   } else if (warp == kIssuer) {
     // The whole warp goes through the loop and one lane issues: descriptors and addresses
     // are then uniform (computed by one lane alone they cost about 70 cycles a product,
@@ -292,6 +308,19 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
 #pragma unroll
       for (int c = 0; c < W / 2; ++c) vv[c] = v[2 * c * PM] | ((uint32_t)v[(2 * c + 1) * PM] << 16);
     };
+    // y of chunk i, rounded, two steps a register, and its way to the writer
+    uint32_t yy[SAVE ? 1 : W / 2];
+    const auto put_y = [&](int i) {
+      if (i >= 1) wait_bar(&bars[kOutFree], (i - 1) & 1, a.err, a.wait_ns);
+      uint16_t *out = reinterpret_cast<uint16_t *>(smem + Lay::kYOff) + c0 * PM + row;
+#pragma unroll
+      for (int c = 0; c < (SAVE ? 1 : W / 2); ++c) {
+        out[2 * c * PM] = (uint16_t)yy[c];
+        out[(2 * c + 1) * PM] = (uint16_t)(yy[c] >> 16);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kOut]);
+    };
     if (chunks > 0) {
       fetch_v(0, 0);
       store_parts<PM, WN, 3>(tX, NP / 2, st);
@@ -311,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       for (int c = 0; c < W; ++c) x[c] = fmaf(-w[c], x[c], c & 1 ? high_half(vv[c / 2]) : low_half(vv[c / 2]));
       store_parts<PM, W, 3>(tR, 32, x);
       ready(kR + up);
+      if (!SAVE && i >= 1) put_y(i - 1);
       load_scalars<W>(w, scal + 2 * kChunk + c0);
       wait_bar(&bars[kDoneU], ph, a.err, a.wait_ns);
       tc_fence_after();
@@ -373,14 +403,29 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
 #pragma unroll
       for (int c = 0; c < W; ++c) x[c] = fmaf(a.scale * g[c], x[c], w[c]);
       if (SAVE) {
-        save_rows(a.y32, i, x);
-      } else {
-        if (i >= 1) wait_bar(&bars[kOutFree], (i - 1) & 1, a.err, a.wait_ns);
-        __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(smem + Lay::kYOff) + c0 * PM + row;
+        // <dy, y> of the warp's columns of p: products summed over its rows, a lane ends with one step's
+        wait_bar(&bars[kDyFull], ph, a.err, a.wait_ns);
+        const __nv_bfloat16 *dy = reinterpret_cast<const __nv_bfloat16 *>(smem + Lay::kYOff) + c0 * PM + row;
 #pragma unroll
-        for (int c = 0; c < W; ++c) out[c * PM] = __float2bfloat16_rn(x[c]);
+        for (int c = 0; c < W; ++c) x[c] *= __bfloat162float(dy[c * PM]);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kOut]);
+        if (lane == 0) mbar_arrive(&bars[kDyFree]);
+#pragma unroll
+        for (int o = W / 2; o >= 1; o >>= 1) {
+          const bool upper = lane & o;
+#pragma unroll
+          for (int c = 0; c < o; ++c) {
+            const float mine = upper ? x[c + o] : x[c], other = upper ? x[c] : x[c + o];
+            x[c] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+          }
+        }
+        const int64_t t = (int64_t)i * kChunk + c0 + (lane & (W - 1));
+        if (t < len) a.dyy[(bh * a.L + t) * 4 + quarter] = x[0];
+      } else {
+        // y goes to the writer in the next chunk's first pause, or at once behind the last
+#pragma unroll
+        for (int c = 0; c < W / 2; ++c) yy[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
+        if (i + 1 == chunks) put_y(i);
       }
     }
     if (SAVE) save_state(chunks);
@@ -403,7 +448,7 @@ cudaError_t launch_k(const DeltaArgs &a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const bool wide = a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && reinterpret_cast<uintptr_t>(a.k) % 16 == 0;
   const dim3 grid((unsigned)((a.P + PM - 1) / PM), (unsigned)a.H, (unsigned)a.Bt);
-  const bool wide_v = a.P % 8 == 0 && reinterpret_cast<uintptr_t>(a.v) % 16 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
+  const bool wide_v = a.P % 8 == 0 && reinterpret_cast<uintptr_t>(a.v) % 16 == 0 && reinterpret_cast<uintptr_t>(SAVE ? a.dy : a.y) % 16 == 0;
   kern<<<grid, kThreads, Lay::kBytes, st>>>(a, wide, wide_v);
   return cudaGetLastError();
 }

@@ -1,6 +1,6 @@
 // Gradients of queries, keys, decays and betas of the gated delta rule, chunk by chunk in
 // parallel (bf16 inputs), from what the chunked passes wrote: the states H at the chunks'
-// ends, the adjoints X there, and e, du, y in fp32 (csrc/delta_chunk.cu, delta_chunk_bwd.cu).
+// ends, the adjoints X there, e, du and <dy, y> in fp32 (csrc/delta_chunk.cu, delta_chunk_bwd.cu).
 //
 // With D_ij = exp(G_i - G_j), u = beta e, and for the chunk's rows
 //   F1_ij = scale D_ij <dy_i, u_j> (j <= i),   F2_ij = -beta_i D_ij <du_i, u_j> (j < i):
@@ -17,7 +17,7 @@
 // bf16 parts (16 bits; dq and dk are rounded to bf16). Row scalings are applied where an
 // accumulator is read, so each operand is stored once. The value heads that share a key
 // head are gone through in the block; their sum stays in registers.
-// What bounds it: HBM (e, du, y and the two states are fp32) and, for N = P = 128, one
+// What bounds it: HBM (e, du and the two states are fp32) and, for N = P = 128, one
 // block an SM whose loads and products alternate.
 #include <algorithm>
 
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
 #pragma unroll
     for (int k = 0; k < kChunk * PG / kThreads; ++k) {
       const int c = (tid + k * kThreads) / PG, g = tid % PG;
-      float4 e[2] = {}, du[2] = {}, y[2] = {};
+      float4 e[2] = {}, du[2] = {}, yy = make_float4(0.f, 0.f, 0.f, 0.f);
       uint4 dy = make_uint4(0, 0, 0, 0), v = dy;
       if (c < live) {
         const int64_t at = (row0 + c) * a.H + h;
@@ -140,9 +140,9 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
                 const int64_t i = (bh * a.L + t0 + c) * Pp + 8 * g + 4 * s;
             e[s] = *reinterpret_cast<const float4 *>(a.e + i);
             du[s] = *reinterpret_cast<const float4 *>(a.du + i);
-            y[s] = *reinterpret_cast<const float4 *>(a.y32 + i);
           }
         }
+        yy = *reinterpret_cast<const float4 *>(a.dyy + (bh * a.L + t0 + c) * 4);
         const B *pdy = static_cast<const B *>(a.dy) + at * P + 8 * g, *pv = static_cast<const B *>(a.v) + at * P + 8 * g;
         if (!wide_v) {
           dy = gather8(pdy, P - 8 * g);
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
       }
       const float beta = scal[2 * kChunk + c];
       float db = sum4(du[0], e[0], sum4(du[1], e[1], 0.f));
-      float dG = sum4(low4(dy), y[0], sum4(high4(dy), y[1], 0.f)) - beta * sum4(low4(v), du[0], sum4(high4(v), du[1], 0.f));
+      float dG = -beta * sum4(low4(v), du[0], sum4(high4(v), du[1], 0.f));
 #pragma unroll
       for (int o = PG / 2; o > 0; o >>= 1) {
         db += __shfl_xor_sync(0xffffffffu, db, o);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
       }
       if (g == 0) {
         sdb[c] = db;
-        sdG[c] = dG;
+        sdG[c] = dG + ((yy.x + yy.y) + (yy.z + yy.w));
       }
       const int off = g * kChunkGroup + c * 16;
       *reinterpret_cast<uint4 *>(smem + Lay::kYo + off) = dy;

@@ -131,7 +131,7 @@ struct DeltaArgs {
   // workspace: states before each chunk and adjoints behind it [Bt][H][nC][N][Pp],
   // e_t and du_t [Bt][H][L][Pp] (a chunk's rows of a head lie together)
   float *carry, *xcarry, *e, *du;
-  float *y32;  // chunked: y_t before its rounding, and carry has [nC + 1] states
+  float *dyy;  // chunked: <dy_t, y_t> in four parts [Bt][H][L][4]; carry has [nC + 1] states
   // chunked kernels: error word, a record for each chunk of each value head
   // (csrc/delta_chunk.cuh), limit of a role's wait
   uint32_t *err;
