@@ -17,7 +17,9 @@
 // the state, so that it is an fp32 state; two parts (16 bits) where only y is
 // reached, which is rounded to bf16 itself.
 // SAVE (the forward of a backward pass) keeps three everywhere, since gradients of the
-// gates are sums of <dy, y> in fp32; it writes these, e and the states instead of y.
+// gates are sums of <dy, y> in fp32; it writes these, e and the states instead of y. The
+// products of small parts come first: an accumulator that is still small loses less when
+// they are added to it.
 //
 // The chain K H -> Te -> K^T u is what a sequence waits for; it runs once a chunk, and the
 // other products fill the pipe in its pauses. A product starts on the half of its depth
@@ -196,10 +198,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int q = 0; q < 3; ++q)
+          for (int q = 2; q >= 0; --q)
 #pragma unroll
             for (int ks = f * NP / 32; ks < (f + 1) * NP / 32; ++ks)
-              mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kX + q * (NP / 2) + 8 * ks, dk + (2 * kChunkGroup * ks >> 4), idS, f + q + ks > 0);
+              mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kX + q * (NP / 2) + 8 * ks, dk + (2 * kChunkGroup * ks >> 4), idS, f + (2 - q) + ks > 0);
           if (f == 1) mma_commit(&bars[kDoneS]);
         }
         __syncwarp();
@@ -209,10 +211,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int q = 0; q < (SAVE ? 3 : 2); ++q)
+        for (int q = SAVE ? 2 : 1; q >= 0; --q)
 #pragma unroll
           for (int ks = 0; ks < NP / 16; ++ks)
-            mma_bf16_ts(tbase + Lay::kYh, tbase + Lay::kX + q * (NP / 2) + 8 * ks, dq + (2 * kChunkGroup * ks >> 4), idS, q + ks > 0);
+            mma_bf16_ts(tbase + Lay::kYh, tbase + Lay::kX + q * (NP / 2) + 8 * ks, dq + (2 * kChunkGroup * ks >> 4), idS,
+                        (SAVE ? 2 : 1) - q + ks > 0);
       }
       __syncwarp();
 #pragma unroll
@@ -220,15 +223,15 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
         wait_bar(&bars[kR + f], ph, a.err, a.wait_ns);
         tc_fence_after();
         if (elect_one()) {
-          // R Te^T: parts (0,0) (1,0) (0,1) (2,0) (1,1) (0,2)
+          // R Te^T: parts (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
 #pragma unroll
-          for (int o = 0; o < 3; ++o)
+          for (int o = 2; o >= 0; --o)
 #pragma unroll
             for (int q = 0; q <= o; ++q)
 #pragma unroll
               for (int ks = 2 * f; ks < 2 * f + 2; ++ks)
                 mma_bf16_ts(tbase + Lay::kYa, tbase + Lay::kD + (o - q) * 32 + 8 * ks, dte + ((q * kSquare + 2048 * ks) >> 4), idS,
-                            f + o + q + ks > 0);
+                            f + (2 - o) + q + ks > 0);
           if (f == 1) mma_commit(&bars[kDoneU]);
         }
         __syncwarp();
@@ -239,10 +242,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int q = 0; q < 3; ++q)
+          for (int q = 2; q >= 0; --q)
 #pragma unroll
             for (int ks = 2 * f; ks < 2 * f + 2; ++ks)
-              mma_bf16_ts(tbase + Lay::kD, tbase + Lay::kUd + q * 32 + 8 * ks, dkt + (256 * ks >> 4), idD, f + q + ks > 0);
+              mma_bf16_ts(tbase + Lay::kD, tbase + Lay::kUd + q * 32 + 8 * ks, dkt + (256 * ks >> 4), idD, f + (2 - q) + ks > 0);
           if (f == 1) mma_commit(&bars[kDoneD]);
         }
         __syncwarp();
@@ -251,14 +254,13 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int o = 0; o < 3; ++o)
+        for (int o = SAVE ? 2 : 1; o >= 0; --o)
 #pragma unroll
           for (int q = 0; q <= o; ++q) {
-            if (!SAVE && o > 1) continue;
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               mma_bf16_ts(tbase + Lay::kYa, tbase + Lay::kUy + (o - q) * 32 + 8 * ks, da + ((q * kSquare + 2048 * ks) >> 4), idS,
-                          o + q + ks > 0);
+                          (SAVE ? 2 : 1) - o + q + ks > 0);
           }
         mma_commit(&bars[kDoneY]);
       }

@@ -120,16 +120,16 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int q = 0; q < 3; ++q)
+          for (int q = 2; q >= 0; --q)
 #pragma unroll
             for (int ks = f * NP / 32; ks < (f + 1) * NP / 32; ++ks)
-              mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kP + q * (NP / 2) + 8 * ks, dk + (2 * kChunkGroup * ks >> 4), idS, f + q + ks > 0);
+              mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kP + q * (NP / 2) + 8 * ks, dk + (2 * kChunkGroup * ks >> 4), idS, f + (2 - q) + ks > 0);
           if (f == 1) {
 #pragma unroll
-            for (int q = 0; q < 3; ++q)
+            for (int q = 2; q >= 0; --q)
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
-                mma_bf16_ts(tbase + Lay::kA, tbase + Lay::kY + 8 * ks, da + ((q * kSquare + 256 * ks) >> 4), idT, q + ks > 0);
+                mma_bf16_ts(tbase + Lay::kA, tbase + Lay::kY + 8 * ks, da + ((q * kSquare + 256 * ks) >> 4), idT, (2 - q) + ks > 0);
             mma_commit(&bars[kDoneS]);
           }
         }
@@ -141,13 +141,13 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int o = 0; o < 3; ++o)
+        for (int o = 2; o >= 0; --o)
 #pragma unroll
           for (int q = 0; q <= o; ++q)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               mma_bf16_ts(tbase + Lay::kZ, tbase + Lay::kD + (o - q) * 32 + 8 * ks, dtb + ((q * kSquare + 256 * ks) >> 4), idT,
-                          o + q + ks > 0);
+                          (2 - o) + q + ks > 0);
         mma_commit(&bars[kDoneU]);
       }
       __syncwarp();
@@ -158,10 +158,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int q = 0; q < 3; ++q)
+          for (int q = 2; q >= 0; --q)
 #pragma unroll
             for (int ks = 2 * f; ks < 2 * f + 2; ++ks) {
-              mma_bf16_ts(tbase + Lay::kD, tbase + Lay::kQ + q * 32 + 8 * ks, dqt + (256 * ks >> 4), idD, f + q + ks > 0);
+              mma_bf16_ts(tbase + Lay::kD, tbase + Lay::kQ + q * 32 + 8 * ks, dqt + (256 * ks >> 4), idD, f + (2 - q) + ks > 0);
               mma_bf16_ts(tbase + Lay::kD, tbase + Lay::kP + q * 32 + 8 * ks, dkt + (256 * ks >> 4), idD, 1);
             }
           if (f == 1) mma_commit(&bars[kDoneD]);
