@@ -107,14 +107,12 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
   load_tile<NP / 8, kChunkGroup, 16, kThreads>(smem, static_cast<const B *>(a.k), row0, a.Hk, hk, a.N, 0, live, wide, tid);
   load_tile<NP / 8, kChunkGroup, 16, kThreads>(smem + Lay::kKq, static_cast<const B *>(a.q), row0, a.Hk, hk, a.N, 0, live, wide, tid);
   cp_async_commit();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tbase = __shfl_sync(0xffffffffu, *tslot, 0), sbase = smem_u32(smem);
+  const uint32_t sbase = smem_u32(smem);
+  uint32_t tbase = 0, tq = 0;
+  const bool whole = N == NP && Pp == PP && P == PP && wide_v;
 
   // the thread's row of an accumulator and its part of the columns
   const int quarter = warp & 3, row = 16 * quarter + (lane & 15), up = warp >> 2, part = 2 * up + (lane >> 4);
-  const uint32_t tq = tbase + ((uint32_t)(32 * quarter) << 16);
   float dq[WN] = {}, dk[WN] = {};
 
   for (int hh = 0; hh < r_heads; ++hh) {
@@ -122,39 +120,67 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
     const uint32_t ph = hh & 1;
     const float *carry = a.carry + (bh * (a.nC + 1) + chunk) * a.N * a.Pp;
     const float *xcarry = a.xcarry + (bh * a.nC + chunk) * a.N * a.Pp;
-    if (tid < kScalars / 16)
-      reinterpret_cast<float4 *>(scal)[tid] =
-          reinterpret_cast<const float4 *>(a.records + (bh * a.nC + chunk) * a.rec_bytes + a.rec_bytes - kScalars)[tid];
-    __syncthreads();
-    // rows: dy, du, u as operands, and the dot products of the gates' gradients
+    // What the first products need is asked for ahead of its use. A whole chunk of whole rows is loaded
+    // without conditions: a branch around each load makes them wait for one another.
+    constexpr int kRows = kChunk * PG / kThreads, kPer = NP * PG / kThreads;
+    const int g = tid % PG, r0 = tid / PG;
+    constexpr int kEvery = kThreads / PG;  // a thread's rows are kEvery apart
+    const float *rec = reinterpret_cast<const float *>(a.records + (bh * a.nC + chunk) * a.rec_bytes + a.rec_bytes - kScalars);
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 e[kRows][2], du[kRows][2], yy[kRows], sx[kPer][2];
+    uint4 dy[kRows], v[kRows];
+    float beta[kRows];
+    const auto fetch_rows = [&](bool all) {
 #pragma unroll
-    for (int k = 0; k < kChunk * PG / kThreads; ++k) {
-      const int c = (tid + k * kThreads) / PG, g = tid % PG;
-      float4 e[2] = {}, du[2] = {}, yy = make_float4(0.f, 0.f, 0.f, 0.f);
-      uint4 dy = make_uint4(0, 0, 0, 0), v = dy;
-      if (c < live) {
-        const int64_t at = (row0 + c) * a.H + h;
+      for (int k = 0; k < kRows; ++k) {
+        const int c = r0 + k * kEvery;
+        const bool on = all || c < live;
+        const int64_t row = bh * a.L + t0 + c, at = ((row0 + c) * a.H + h) * P + 8 * g;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (8 * g + 4 * s < Pp) {
-                const int64_t i = (bh * a.L + t0 + c) * Pp + 8 * g + 4 * s;
-            e[s] = *reinterpret_cast<const float4 *>(a.e + i);
-            du[s] = *reinterpret_cast<const float4 *>(a.du + i);
-          }
+          const bool here = all || (on && 8 * g + 4 * s < Pp);
+          e[k][s] = here ? *reinterpret_cast<const float4 *>(a.e + row * Pp + 8 * g + 4 * s) : none;
+          du[k][s] = here ? *reinterpret_cast<const float4 *>(a.du + row * Pp + 8 * g + 4 * s) : none;
         }
-        yy = *reinterpret_cast<const float4 *>(a.dyy + (bh * a.L + t0 + c) * 4);
-        const B *pdy = static_cast<const B *>(a.dy) + at * P + 8 * g, *pv = static_cast<const B *>(a.v) + at * P + 8 * g;
-        if (!wide_v) {
-          dy = gather8(pdy, P - 8 * g);
-          v = gather8(pv, P - 8 * g);
-        } else if (8 * g < P) {
-          dy = *reinterpret_cast<const uint4 *>(pdy);
-          v = *reinterpret_cast<const uint4 *>(pv);
+        yy[k] = on ? *reinterpret_cast<const float4 *>(a.dyy + row * 4) : none;
+        if (all || (wide_v && on && 8 * g < P)) {
+          dy[k] = *reinterpret_cast<const uint4 *>(static_cast<const B *>(a.dy) + at);
+          v[k] = *reinterpret_cast<const uint4 *>(static_cast<const B *>(a.v) + at);
+        } else {
+          dy[k] = gather8(static_cast<const B *>(a.dy) + at, on && !wide_v ? P - 8 * g : 0);
+          v[k] = gather8(static_cast<const B *>(a.v) + at, on && !wide_v ? P - 8 * g : 0);
         }
+        beta[k] = rec[2 * kChunk + c];
       }
-      const float beta = scal[2 * kChunk + c];
-      float db = sum4(du[0], e[0], sum4(du[1], e[1], 0.f));
-      float dG = -beta * sum4(low4(v), du[0], sum4(high4(v), du[1], 0.f));
+    };
+    // a state of the workspace into registers, and from there as operands
+    const auto fetch_state = [&](const float *from, float4 (&x)[kPer][2]) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int n = r0 + k * kEvery;
+          if (whole) x[k][s] = *reinterpret_cast<const float4 *>(from + n * PP + 8 * g + 4 * s);
+          else x[k][s] = n < N && 8 * g + 4 * s < Pp ? *reinterpret_cast<const float4 *>(from + n * Pp + 8 * g + 4 * s) : none;
+        }
+    };
+    const auto put_state = [&](const float4 (&x)[kPer][2]) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        uint8_t *to = smem + Lay::kHo + g * Lay::kHGroup + (r0 + k * kEvery) * 16;
+        put_parts(to, to + Lay::kH, x[k][0], x[k][1]);
+      }
+    };
+    if (whole && live == kChunk) fetch_rows(true);
+    else fetch_rows(false);
+    if (kRows == 1) fetch_state(carry, sx);
+    if (tid < kScalars / 16) reinterpret_cast<float4 *>(scal)[tid] = reinterpret_cast<const float4 *>(rec)[tid];
+    // rows: dy, du, u as operands, and the dot products of the gates' gradients
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int c = r0 + k * kEvery;
+      float db = sum4(du[k][0], e[k][0], sum4(du[k][1], e[k][1], 0.f));
+      float dG = -beta[k] * sum4(low4(v[k]), du[k][0], sum4(high4(v[k]), du[k][1], 0.f));
 #pragma unroll
       for (int o = PG / 2; o > 0; o >>= 1) {
         db += __shfl_xor_sync(0xffffffffu, db, o);
@@ -162,37 +188,24 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
       }
       if (g == 0) {
         sdb[c] = db;
-        sdG[c] = dG + ((yy.x + yy.y) + (yy.z + yy.w));
+        sdG[c] = dG + ((yy[k].x + yy[k].y) + (yy[k].z + yy[k].w));
       }
       const int off = g * kChunkGroup + c * 16;
-      *reinterpret_cast<uint4 *>(smem + Lay::kYo + off) = dy;
-      put_parts(smem + Lay::kDo + off, smem + Lay::kDo + Lay::kRow + off, du[0], du[1]);
-      put_parts(smem + Lay::kUo + off, smem + Lay::kUo + Lay::kRow + off, times(e[0], beta), times(e[1], beta));
+      *reinterpret_cast<uint4 *>(smem + Lay::kYo + off) = dy[k];
+      put_parts(smem + Lay::kDo + off, smem + Lay::kDo + Lay::kRow + off, du[k][0], du[k][1]);
+      put_parts(smem + Lay::kUo + off, smem + Lay::kUo + Lay::kRow + off, times(e[k][0], beta[k]), times(e[k][1], beta[k]));
     }
-    // a state of the workspace into registers, and from there as operands
-    constexpr int kPer = NP * PG / kThreads;
-    const auto fetch_state = [&](const float *from, float4 (&x)[kPer][2]) {
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int n = (tid + k * kThreads) / PG, g = tid % PG;
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-          x[k][s] = n < N && 8 * g + 4 * s < Pp ? *reinterpret_cast<const float4 *>(from + n * Pp + 8 * g + 4 * s) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-    };
-    const auto put_state = [&](const float4 (&x)[kPer][2]) {
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        uint8_t *to = smem + Lay::kHo + (tid % PG) * Lay::kHGroup + ((tid + k * kThreads) / PG) * 16;
-        put_parts(to, to + Lay::kH, x[k][0], x[k][1]);
-      }
-    };
-    float4 sx[kPer][2];
-    fetch_state(carry, sx);
+    if (kRows != 1) fetch_state(carry, sx);
     put_state(sx);
     cp_async_wait<0>();
     fence_proxy_async_smem();
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    if (hh == 0) {
+      tbase = __shfl_sync(0xffffffffu, *tslot, 0);
+      tq = tbase + ((uint32_t)(32 * quarter) << 16);
+    }
     constexpr uint32_t idS = idesc_bf16_f32(64, kChunk, false, false), idN = idesc_bf16_f32(64, NP, false, false);
     if (warp == 0) {
       if (elect_one()) {
