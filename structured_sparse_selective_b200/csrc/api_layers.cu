@@ -237,7 +237,7 @@ pdssm_status pdssm_delta_fwd(const pdssm_delta_problem *pb, const void *q, const
   a.wait_ns = wait_limit(pb);
   if (cudaMemsetAsync(a.err, 0, 4, cs) != cudaSuccess) return PDSSM_ERR_CUDA;
   if ((st = cuda_status(launch_delta_prep(a, false, cs))) != PDSSM_OK) return st;
-  return cuda_status(launch_delta_chunk(a, false, cs));
+  return cuda_status(launch_delta_chunk(a, cs));
 }
 
 pdssm_status pdssm_delta_bwd_workspace_size(const pdssm_delta_problem *pb, size_t *bytes) {
@@ -286,12 +286,10 @@ pdssm_status pdssm_delta_bwd(const pdssm_delta_problem *pb, const void *q, const
     a.wait_ns = wait_limit(pb);
     if (cudaMemsetAsync(a.err, 0, 4, cs) != cudaSuccess) return PDSSM_ERR_CUDA;
     if ((st = cuda_status(launch_delta_prep(a, true, cs))) != PDSSM_OK) return st;
-    if ((st = cuda_status(launch_delta_chunk(a, true, cs))) != PDSSM_OK) return st;
-    if ((st = cuda_status(launch_delta_chunk_bwd(a, cs))) != PDSSM_OK) return st;
+    if ((st = cuda_status(launch_delta_chunk_both(a, cs))) != PDSSM_OK) return st;
     return cuda_status(launch_delta_chunk_grad(a, cs));
   }
-  if (p.rows > 0 && (st = cuda_status(launch_delta_steps_save(a, cs))) != PDSSM_OK) return st;
-  if ((st = cuda_status(launch_delta_steps_bwd(a, cs))) != PDSSM_OK) return st;
+  if ((st = cuda_status(launch_delta_steps_both(a, cs))) != PDSSM_OK) return st;
   if (p.rows > 0) st = cuda_status(launch_delta_grad(a, cs));
   return st;
 }

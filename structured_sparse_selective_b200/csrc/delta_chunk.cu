@@ -33,6 +33,7 @@
 
 #include "delta.cuh"
 #include "delta_chunk.cuh"
+#include "delta_chunk_bwd.cuh"
 #include "sm100.cuh"
 
 namespace pdssm {
@@ -71,8 +72,9 @@ struct Layout {
   static constexpr int kParts = 256 / PM, W = kChunk / kParts, WN = NP / kParts;
 };
 
+// One sequence of one head, columns p0 ...
 template <int NP, int PM, bool SAVE>
-__global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, bool wide, bool wide_v) {
+__device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, int p0) {
   using Lay = Layout<NP, PM, SAVE>;
   constexpr int W = Lay::W, WN = Lay::WN;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -80,7 +82,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + kBars);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.H + h, hk = h / (a.H / a.Hk);
-  const int p0 = blockIdx.x * PM;
   const int64_t len = live_steps(a.lengths, b, a.L);
   const int chunks = __shfl_sync(0xffffffffu, (int)((len + kChunk - 1) / kChunk), 0);
 
@@ -442,32 +443,57 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, b
   if (warp == kIssuer) tmem_dealloc(tbase, Lay::kCols);
 }
 
-template <int NP, int PM, bool SAVE>
-cudaError_t launch_k(const DeltaArgs &a, cudaStream_t st) {
-  using Lay = Layout<NP, PM, SAVE>;
-  auto kern = delta_chunk_kernel<NP, PM, SAVE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
-  if (e != cudaSuccess) return e;
-  const bool wide = a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && reinterpret_cast<uintptr_t>(a.k) % 16 == 0;
-  const dim3 grid((unsigned)((a.P + PM - 1) / PM), (unsigned)a.H, (unsigned)a.Bt);
-  const bool wide_v = a.P % 8 == 0 && reinterpret_cast<uintptr_t>(a.v) % 16 == 0 && reinterpret_cast<uintptr_t>(SAVE ? a.dy : a.y) % 16 == 0;
-  kern<<<grid, kThreads, Lay::kBytes, st>>>(a, wide, wide_v);
-  return cudaGetLastError();
+enum What { kForward, kSave, kBack, kBoth };
+
+// kBoth: the states and the adjoints of a backward pass do not need one another, so their blocks
+// take turns in one launch.
+template <int NP, int PM, What WHAT>
+__global__ void __launch_bounds__(kThreads, 1) delta_chunk_kernel(DeltaArgs a, bool wide, bool wide_v) {
+  const int p0 = (WHAT == kBoth ? blockIdx.x >> 1 : blockIdx.x) * PM;
+  if (WHAT == kBack || (WHAT == kBoth && (blockIdx.x & 1))) chunk_bwd::run<NP, PM>(a, wide, wide_v, p0);
+  else run<NP, PM, WHAT != kForward>(a, wide, wide_v, p0);
+}
+
+bool all16(const void *x, const void *y) {
+  return ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) & 15) == 0;
+}
+
+template <int NP, int PM, What WHAT>
+cudaError_t launch_k(const DeltaArgs &a, const char *name, cudaStream_t st) {
+  auto kern = delta_chunk_kernel<NP, PM, WHAT>;
+  constexpr int kSave_ = Layout<NP, PM, true>::kBytes, kBack_ = chunk_bwd::Layout<NP, PM>::kBytes;
+  constexpr int kSmem = WHAT == kForward ? Layout<NP, PM, false>::kBytes
+                        : WHAT == kSave  ? kSave_
+                        : WHAT == kBack  ? kBack_
+                        : kSave_ > kBack_ ? kSave_ : kBack_;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess || (e = trace_before(st, name)) != cudaSuccess) return e;
+  const bool wide = a.N % 8 == 0 && all16(a.q, a.k), wide_v = a.P % 8 == 0 && all16(a.v, WHAT == kForward ? a.y : a.dy);
+  const dim3 grid((unsigned)((a.P + PM - 1) / PM) * (WHAT == kBoth ? 2 : 1), (unsigned)a.H, (unsigned)a.Bt);
+  kern<<<grid, kThreads, kSmem, st>>>(a, wide, wide_v);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : trace_after(st);
+}
+
+template <int NP, int PM>
+cudaError_t launch_n(const DeltaArgs &a, bool bwd, cudaStream_t st) {
+  if (!bwd) return launch_k<NP, PM, kForward>(a, "delta_chunk", st);
+  // One launch where all its blocks have an SM of their own (64 sequences of 2,048 steps, 128 x 128: 304 us
+  // together, 412 one after the other); beyond that the two kinds slow one another (256 sequences, 64 x 64:
+  // 490 and 424 us; 128 of 4,096 steps, 128 x 128: 1,078 and 834).
+  if (2 * a.Bt * a.H * ((a.P + PM - 1) / PM) <= 148) return launch_k<NP, PM, kBoth>(a, "delta_chunk_both", st);
+  cudaError_t e = launch_k<NP, PM, kSave>(a, "delta_chunk_save", st);
+  return e != cudaSuccess ? e : launch_k<NP, PM, kBack>(a, "delta_chunk_bwd", st);
+}
+
+cudaError_t launch(const DeltaArgs &a, bool bwd, cudaStream_t st) {
+  if (a.N <= 64) return a.P <= 64 ? launch_n<64, 64>(a, bwd, st) : launch_n<64, 128>(a, bwd, st);
+  return a.P <= 64 ? launch_n<128, 64>(a, bwd, st) : launch_n<128, 128>(a, bwd, st);
 }
 
 }  // namespace
 
-template <bool SAVE>
-static cudaError_t launch_s(const DeltaArgs &a, cudaStream_t st) {
-  if (a.N <= 64) return a.P <= 64 ? launch_k<64, 64, SAVE>(a, st) : launch_k<64, 128, SAVE>(a, st);
-  return a.P <= 64 ? launch_k<128, 64, SAVE>(a, st) : launch_k<128, 128, SAVE>(a, st);
-}
-
-cudaError_t launch_delta_chunk(const DeltaArgs &a, bool save, cudaStream_t st) {
-  cudaError_t e = trace_before(st, save ? "delta_chunk_save" : "delta_chunk");
-  if (e != cudaSuccess) return e;
-  e = save ? launch_s<true>(a, st) : launch_s<false>(a, st);
-  return e != cudaSuccess ? e : trace_after(st);
-}
+cudaError_t launch_delta_chunk(const DeltaArgs &a, cudaStream_t st) { return launch(a, false, st); }
+cudaError_t launch_delta_chunk_both(const DeltaArgs &a, cudaStream_t st) { return launch(a, true, st); }
 
 }  // namespace pdssm

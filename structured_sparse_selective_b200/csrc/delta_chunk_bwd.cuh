@@ -10,20 +10,18 @@
 // bf16 parts on the way to X, dY and the records' parts are exact as they are. The chain is
 // K X -> Tb -> K^T dv; dY^T A and Q^T dY run in its pauses.
 // Written: dv, du (fp32), X at each chunk's end, dh0.
-#include <algorithm>
+#pragma once
 
 #include "delta.cuh"
 #include "delta_chunk.cuh"
 #include "sm100.cuh"
 
 namespace pdssm {
+namespace chunk_bwd {
 
 using namespace sm100;
 
-namespace {
-
 constexpr int kStateWarps = 8, kIssuer = 8, kLoader0 = 9, kLoaders = 2;
-constexpr int kThreads = 32 * (kLoader0 + kLoaders);
 
 // kX, kR, kU: [half], from the four warps that have that half of a row's columns.
 enum Bar { kFull, kFree = kFull + 3, kX = kFree + 3, kR = kX + 2, kU = kR + 2, kDoneS = kU + 2, kDoneU, kDoneD, kEnd, kBars };
@@ -43,8 +41,9 @@ struct Layout {
   static constexpr int kParts = 256 / PM, W = kChunk / kParts, WN = NP / kParts;
 };
 
+// One sequence of one head, columns p0 ...
 template <int NP, int PM>
-__global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs a, bool wide, bool wide_v) {
+__device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, int p0) {
   using Lay = Layout<NP, PM>;
   constexpr int W = Lay::W, WN = Lay::WN;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -52,7 +51,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + kBars);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.H + h, hk = h / (a.H / a.Hk);
-  const int p0 = blockIdx.x * PM;
   const int64_t len = live_steps(a.lengths, b, a.L);
   const int chunks = __shfl_sync(0xffffffffu, (int)((len + kChunk - 1) / kChunk), 0);
 
@@ -73,7 +71,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
   const uint32_t tbase = __shfl_sync(0xffffffffu, *tslot, 0);
 
   // Turn i works on chunk chunks - 1 - i.
-  if (warp >= kLoader0) {
+  if (warp >= kLoader0 + kLoaders) {
+    // the block has one warp more than this needs
+  } else if (warp >= kLoader0) {
     const int tid = threadIdx.x - 32 * kLoader0;
     const bool copies = wide && wide_v && a.N == NP && a.P - p0 >= PM;  // nothing is written by the threads themselves
     using B = const __nv_bfloat16;
@@ -302,27 +302,5 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunk_bwd_kernel(DeltaArgs 
   if (warp == kIssuer) tmem_dealloc(tbase, Lay::kCols);
 }
 
-template <int NP, int PM>
-cudaError_t launch_k(const DeltaArgs &a, cudaStream_t st) {
-  using Lay = Layout<NP, PM>;
-  auto kern = delta_chunk_bwd_kernel<NP, PM>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
-  if (e != cudaSuccess) return e;
-  const bool wide = a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && reinterpret_cast<uintptr_t>(a.k) % 16 == 0;
-  const bool wide_v = a.P % 8 == 0 && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0;
-  const dim3 grid((unsigned)((a.P + PM - 1) / PM), (unsigned)a.H, (unsigned)a.Bt);
-  kern<<<grid, kThreads, Lay::kBytes, st>>>(a, wide, wide_v);
-  return cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_delta_chunk_bwd(const DeltaArgs &a, cudaStream_t st) {
-  cudaError_t e = trace_before(st, "delta_chunk_bwd");
-  if (e != cudaSuccess) return e;
-  if (a.N <= 64) e = a.P <= 64 ? launch_k<64, 64>(a, st) : launch_k<64, 128>(a, st);
-  else e = a.P <= 64 ? launch_k<128, 64>(a, st) : launch_k<128, 128>(a, st);
-  return e != cudaSuccess ? e : trace_after(st);
-}
-
+}  // namespace chunk_bwd
 }  // namespace pdssm

@@ -186,14 +186,15 @@ __device__ __forceinline__ float total(const pair2 (&s)[2]) {
   return (a + c) + (b + d);
 }
 
-// grid: (column groups, heads, batch); warps 0 .. warps - 1 compute, the others load.
-// SAVE: writes e_t and, every a.C steps, the state before them (for the backward pass).
+// One block: the columns p0 ... of head blockIdx.y of sequence blockIdx.z; warps 0 .. warps - 1
+// compute, the others load. SAVE: writes e_t and, every a.C steps, the state before them (for
+// the backward pass).
 template <int J, typename T, typename G, bool SAVE>
-__global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_kernel(DeltaArgs a) {
+__device__ __forceinline__ void forward(const DeltaArgs &a, int group) {
   constexpr int R = Rows<J>::R, LPC = Rows<J>::LPC, kRow = 32 * J;
   extern __shared__ __align__(16) float smem[];
   const int warps = blockDim.x / 32 - kLoaders, warp = threadIdx.x >> 5;
-  const int cols = warps * Rows<J>::kCols, p0 = blockIdx.x * cols;
+  const int cols = warps * Rows<J>::kCols, p0 = group * cols;
   const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.H + h;
   const int64_t len = live_steps(a.lengths, b, a.L);
   if (warp >= warps) {
@@ -282,11 +283,11 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_kerne
 // of each chunk of a.C steps, and dh0. A step is
 //   X += dy q,  du = k X (sums and shuffles),  X = a (X - w k).
 template <int J, typename T, typename G>
-__global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_bwd_kernel(DeltaArgs a) {
+__device__ __forceinline__ void backward(const DeltaArgs &a, int group) {
   constexpr int R = Rows<J>::R, LPC = Rows<J>::LPC, kRow = 32 * J;
   extern __shared__ __align__(16) float smem[];
   const int warps = blockDim.x / 32 - kLoaders, warp = threadIdx.x >> 5;
-  const int cols = warps * Rows<J>::kCols, p0 = blockIdx.x * cols;
+  const int cols = warps * Rows<J>::kCols, p0 = group * cols;
   const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.H + h;
   const int64_t len = live_steps(a.lengths, b, a.L);
   const int64_t tiles = (len + kTS - 1) / kTS;
@@ -370,6 +371,20 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_bwd_k
   if (!in) return;
   for (int64_t t = len + l; t < a.L; t += LPC) st_out(dv + t * a.H * a.P, 0.f);
   if (a.dh0) store_column<J>(x, a.dh0 + bh * a.N * a.P + col, l, N, a.P);
+}
+
+// grid: (column groups, heads, batch)
+template <int J, typename T, typename G>
+__global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_kernel(DeltaArgs a) {
+  forward<J, T, G, false>(a, blockIdx.x);
+}
+
+// The states and the adjoints of a backward pass do not need one another: their blocks take
+// turns, so that few sequences fill more SMs. grid: (2 x column groups, heads, batch)
+template <int J, typename T, typename G>
+__global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_both_kernel(DeltaArgs a) {
+  if (blockIdx.x & 1) backward<J, T, G>(a, blockIdx.x >> 1);
+  else forward<J, T, G, true>(a, blockIdx.x >> 1);
 }
 
 // ------------------------------------------------------------------ one token
@@ -470,7 +485,7 @@ __global__ void __launch_bounds__(128) delta_token_kernel(DeltaArgs a) {
   }
 }
 
-enum Which { kForward, kForwardSave, kBackward, kToken };
+enum Which { kForward, kBoth, kToken };
 
 template <int J, typename T, typename G>
 cudaError_t launch_jtg(const DeltaArgs &a, Which which, cudaStream_t st) {
@@ -485,10 +500,9 @@ cudaError_t launch_jtg(const DeltaArgs &a, Which which, cudaStream_t st) {
   const int all = (int)((a.P + kCols - 1) / kCols);
   int warps = std::min(all, kMaxWarps);
   while (warps > 2 && a.Bt * a.H * ((all + warps - 1) / warps) < 148) warps = (warps + 1) / 2;
-  const dim3 grid((unsigned)((all + warps - 1) / warps), (unsigned)a.H, (unsigned)a.Bt);
+  const dim3 grid((unsigned)((all + warps - 1) / warps) * (which == kBoth ? 2 : 1), (unsigned)a.H, (unsigned)a.Bt);
   const size_t smem = Tile<J>::bytes(warps * kCols);
-  auto kern = which == kForward ? delta_steps_kernel<J, T, G, false>
-                                : which == kForwardSave ? delta_steps_kernel<J, T, G, true> : delta_steps_bwd_kernel<J, T, G>;
+  auto kern = which == kForward ? delta_steps_kernel<J, T, G> : delta_steps_both_kernel<J, T, G>;
   kern<<<grid, 32 * (warps + kLoaders), smem, st>>>(a);
   return cudaGetLastError();
 }
@@ -513,7 +527,6 @@ cudaError_t launch(const DeltaArgs &a, Which which, const char *name, cudaStream
 cudaError_t launch_delta_steps(const DeltaArgs &a, cudaStream_t st) {
   return a.L == 1 ? launch(a, kToken, "delta_token", st) : launch(a, kForward, "delta_steps", st);
 }
-cudaError_t launch_delta_steps_save(const DeltaArgs &a, cudaStream_t st) { return launch(a, kForwardSave, "delta_steps_save", st); }
-cudaError_t launch_delta_steps_bwd(const DeltaArgs &a, cudaStream_t st) { return launch(a, kBackward, "delta_steps_bwd", st); }
+cudaError_t launch_delta_steps_both(const DeltaArgs &a, cudaStream_t st) { return launch(a, kBoth, "delta_steps_both", st); }
 
 }  // namespace pdssm

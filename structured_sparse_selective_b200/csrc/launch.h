@@ -141,15 +141,14 @@ struct DeltaArgs {
 };
 // Step by step, any size; the outputs y and h_final.
 cudaError_t launch_delta_steps(const DeltaArgs &a, cudaStream_t st);
-// The same steps, writing carry and e instead; and the adjoint's steps (dv, dh0, xcarry, du).
-cudaError_t launch_delta_steps_save(const DeltaArgs &a, cudaStream_t st);
-cudaError_t launch_delta_steps_bwd(const DeltaArgs &a, cudaStream_t st);
-// By chunks of 64 on the tensor cores (bf16 inputs): the chunks' records, then the state
-// and the outputs.
+// The same steps, writing carry and e instead, with the adjoint's steps (dv, dh0, xcarry, du).
+cudaError_t launch_delta_steps_both(const DeltaArgs &a, cudaStream_t st);
+// By chunks of 64 on the tensor cores (bf16 inputs): the chunks' records; the state and the
+// outputs, or (both) what a backward pass needs of the states, with the adjoints (dv, dh0,
+// xcarry, du); and the other gradients from what those wrote.
 cudaError_t launch_delta_prep(const DeltaArgs &a, bool bwd, cudaStream_t st);
-cudaError_t launch_delta_chunk(const DeltaArgs &a, bool save, cudaStream_t st);
-// The adjoint by chunks (dv, dh0, xcarry, du); and the other gradients from what both wrote.
-cudaError_t launch_delta_chunk_bwd(const DeltaArgs &a, cudaStream_t st);
+cudaError_t launch_delta_chunk(const DeltaArgs &a, cudaStream_t st);
+cudaError_t launch_delta_chunk_both(const DeltaArgs &a, cudaStream_t st);
 cudaError_t launch_delta_chunk_grad(const DeltaArgs &a, cudaStream_t st);
 // dq, dk, dg and dbeta of every chunk from its carries, e and du.
 int64_t delta_grad_chunk();
