@@ -118,16 +118,17 @@ __device__ __forceinline__ void write_parts(const float *x, const Gate *gate, ui
 
 template <int NP>
 struct Smem {
-  // the operand is read by the tensor core only until its product is done; X and W then take its place
-  static constexpr int kKq = (NP / 8) * kGroup, kXw = 4 * (kChunk * kLd + 32 * 36), kNt = kKq > kXw ? kKq : kXw;
+  // the operand is read by the tensor core only until its product is done; X then takes its place, and W
+  // that of N's upper triangle once it is solved
+  static constexpr int kKq = (NP / 8) * kGroup, kX = 4 * kChunk * kLd, kNt = kKq > kX ? kKq : kX;
   static constexpr int kGate = kNt + 4 * kChunk * kLd, kBar = kGate + 16 * kChunk, kBytes = kBar + 16;
 };
 
 template <int NP, bool BWD>
-__global__ void __launch_bounds__(kThreads, NP == 64 ? 5 : 4) delta_prep_kernel(DeltaArgs a, bool wide) {
+__global__ void __launch_bounds__(kThreads, NP == 64 ? 6 : 4) delta_prep_kernel(DeltaArgs a, bool wide) {
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *kq = smem;
-  float *x = reinterpret_cast<float *>(smem), *w = x + kChunk * kLd, *nt = reinterpret_cast<float *>(smem + Smem<NP>::kNt);
+  float *x = reinterpret_cast<float *>(smem), *nt = reinterpret_cast<float *>(smem + Smem<NP>::kNt), *w = nt;
   Gate *gate = reinterpret_cast<Gate *>(smem + Smem<NP>::kGate);
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + Smem<NP>::kBar);
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 1);
@@ -278,20 +279,20 @@ __global__ void __launch_bounds__(kThreads, NP == 64 ? 5 : 4) delta_prep_kernel(
         acc[0] = fmaf(l, u.x, acc[0]); acc[1] = fmaf(l, u.y, acc[1]); acc[2] = fmaf(l, u.z, acc[2]); acc[3] = fmaf(l, u.w, acc[3]);
         acc[4] = fmaf(l, v.x, acc[4]); acc[5] = fmaf(l, v.y, acc[5]); acc[6] = fmaf(l, v.z, acc[6]); acc[7] = fmaf(l, v.w, acc[7]);
       }
-      *reinterpret_cast<float4 *>(w + lane * 36 + 8 * warp) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      *reinterpret_cast<float4 *>(w + lane * 36 + 8 * warp + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      *reinterpret_cast<float4 *>(w + lane * kLd + 8 * warp) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      *reinterpret_cast<float4 *>(w + lane * kLd + 8 * warp + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
     }
     __syncthreads();
     {
       // rows 8 warp .. + 7 of column `lane`; X22 ends before its diagonal
       float acc[8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) acc[r] = w[(8 * warp + r) * 36 + lane];
+      for (int r = 0; r < 8; ++r) acc[r] = w[(8 * warp + r) * kLd + lane];
 #pragma unroll 2
       for (int m = 0; m < 8 * warp + 8; m += 4) {
         float u[4];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) u[s] = -gate[32 + m + s].beta * w[(m + s) * 36 + lane];
+        for (int s = 0; s < 4; ++s) u[s] = -gate[32 + m + s].beta * w[(m + s) * kLd + lane];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
           const float4 v = *reinterpret_cast<const float4 *>(x + (32 + 8 * warp + r) * kLd + 32 + m);
