@@ -78,17 +78,26 @@ pdssm_status run_norm(const pdssm_norm_problem *pb, QkNormArgs &a, int64_t rows,
 struct DeltaPlan {
   int64_t rows, slices, Pp, C, nC;
   bool chunked;  // by chunks on the tensor cores
-  size_t o_carry, o_xcarry, o_e, o_du, o_dyy, o_rec, fwd_bytes, bwd_bytes;
+  size_t o_carry, o_xcarry, o_e, o_du, o_dyy, o_rec, bytes;
 };
 
 constexpr size_t kErrBytes = 256;
 
-// bf16 sequences of more than a chunk go by chunks.
-bool chunks_apply(const pdssm_delta_problem *pb) {
-  return pb->in_t == PDSSM_BF16 && pb->seqlen > kChunk && !(pb->flags & PDSSM_FLAG_REFERENCE_PATH);
+// Whether a problem goes by chunks of 64 steps on the tensor cores, or step by step: bf16
+// inputs, and as measured (us; steps, chunks; N = P = 64 with 256 sequences, 128 x 64 with 2,048):
+//   forward   256: 32 steps 25, 29; 48 steps 35, 29; 64 steps 45, 27
+//             2,048: 8 steps 167, 187; 16 steps 235, 189; 32 steps 353, 191
+//   backward  256: 8 steps 56, 56; 16 steps 64, 57; 64 steps 140, 53
+//             2,048: 8 steps 829, 431
+// A chunk costs the same however few of its steps there are; steps cost their number, more
+// where four sequences or more share an SM.
+bool chunks_apply(const pdssm_delta_problem *pb, bool bwd) {
+  if (pb->in_t != PDSSM_BF16 || (pb->flags & PDSSM_FLAG_REFERENCE_PATH)) return false;
+  if (bwd) return pb->seqlen > 8;
+  return pb->seqlen > (pb->batch * pb->heads >= 4 * 148 ? 12 : 40);
 }
 
-pdssm_status plan_delta(const pdssm_delta_problem *pb, DeltaPlan *pl) {
+pdssm_status plan_delta(const pdssm_delta_problem *pb, bool bwd, DeltaPlan *pl) {
   if (!pb) return PDSSM_ERR_INVALID_ARG;
   if (pb->batch < 0 || pb->seqlen < 0 || pb->heads < 1 || pb->qk_heads < 1 || pb->heads % pb->qk_heads ||
       pb->N < 1 || pb->P < 1 || !isfinite(pb->scale) ||
@@ -105,20 +114,22 @@ pdssm_status plan_delta(const pdssm_delta_problem *pb, DeltaPlan *pl) {
   // more than 8 KiB a step), rows of Pp floats a step
   if (!mul_ok(pb->batch, pb->seqlen, &p.rows) || !mul_ok(p.slices, (pb->seqlen + kChunk) * 8192, &bytes))
     return PDSSM_ERR_UNSUPPORTED;
-  p.chunked = chunks_apply(pb);
+  p.chunked = chunks_apply(pb, bwd);
   p.C = p.chunked ? kChunk : delta_grad_chunk();
   p.nC = (pb->seqlen + p.C - 1) / p.C;
-  // backward: error word, states (chunked: one more a sequence), adjoints, e, du; chunked: <dy, y> and the records
-  const size_t state = (size_t)(pb->N * p.Pp) * 4, steps = (size_t)(p.rows * pb->heads * p.Pp) * 4;
+  const size_t records = p.chunked ? (size_t)(p.slices * p.nC * delta_record_bytes(bwd)) : 0;
   size_t o = p.chunked ? kErrBytes : 0;
-  p.o_carry = o; o = align256(o + (size_t)(p.slices * (p.nC + (p.chunked ? 1 : 0))) * state);
-  p.o_xcarry = o; o = align256(o + (size_t)(p.slices * p.nC) * state);
-  p.o_e = o; o = align256(o + steps);
-  p.o_du = o; o = align256(o + steps);
-  p.o_dyy = o; o = align256(o + (p.chunked ? (size_t)(p.rows * pb->heads) * 16 : 0));
-  p.o_rec = o; o = align256(o + (p.chunked ? (size_t)(p.slices * p.nC * delta_record_bytes(true)) : 0));
-  p.bwd_bytes = o;
-  p.fwd_bytes = p.chunked ? kErrBytes + (size_t)(p.slices * p.nC * delta_record_bytes(false)) : 0;
+  if (bwd) {
+    // error word, states (chunked: one more a sequence), adjoints, e, du; chunked: <dy, y> and the records
+    const size_t state = (size_t)(pb->N * p.Pp) * 4, steps = (size_t)(p.rows * pb->heads * p.Pp) * 4;
+    p.o_carry = o; o = align256(o + (size_t)(p.slices * (p.nC + (p.chunked ? 1 : 0))) * state);
+    p.o_xcarry = o; o = align256(o + (size_t)(p.slices * p.nC) * state);
+    p.o_e = o; o = align256(o + steps);
+    p.o_du = o; o = align256(o + steps);
+    p.o_dyy = o; o = align256(o + (p.chunked ? (size_t)(p.rows * pb->heads) * 16 : 0));
+  }
+  p.o_rec = o; o = align256(o + records);
+  p.bytes = o;
   *pl = p;
   return PDSSM_OK;
 }
@@ -206,9 +217,9 @@ pdssm_status pdssm_qk_norm_bwd(const pdssm_norm_problem *pb, const void *q, cons
 pdssm_status pdssm_delta_workspace_size(const pdssm_delta_problem *pb, size_t *bytes) {
   if (!bytes) return PDSSM_ERR_INVALID_ARG;
   DeltaPlan p;
-  pdssm_status st = plan_delta(pb, &p);
+  pdssm_status st = plan_delta(pb, false, &p);
   if (st != PDSSM_OK) return st;
-  *bytes = p.fwd_bytes;
+  *bytes = p.bytes;
   return PDSSM_OK;
 }
 
@@ -216,14 +227,14 @@ pdssm_status pdssm_delta_fwd(const pdssm_delta_problem *pb, const void *q, const
                              const void *g, const void *beta, const int32_t *lengths, const float *h0, void *y,
                              float *h_final, void *workspace, size_t workspace_bytes, pdssm_stream_t stream) {
   DeltaPlan p;
-  pdssm_status st = plan_delta(pb, &p);
+  pdssm_status st = plan_delta(pb, false, &p);
   if (st != PDSSM_OK) return st;
   const size_t es = dtype_size(pb->in_t), gs = dtype_size(pb->gate_t);
   if (p.rows * pb->heads > 0 && (!q || !k || !v || !g || !beta || !y)) return PDSSM_ERR_INVALID_ARG;
   if (!aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(y, es) || !aligned(g, gs) ||
       !aligned(beta, gs) || !aligned(lengths, 4) || !aligned(h0, 4) || !aligned(h_final, 4) || !aligned(workspace, 16))
     return PDSSM_ERR_INVALID_ARG;
-  if (p.fwd_bytes && (!workspace || workspace_bytes < p.fwd_bytes)) return PDSSM_ERR_WORKSPACE;
+  if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return PDSSM_ERR_WORKSPACE;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   OnDevice on(cs);
   if (on.status() != PDSSM_OK) return on.status();
@@ -232,7 +243,7 @@ pdssm_status pdssm_delta_fwd(const pdssm_delta_problem *pb, const void *q, const
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lengths = lengths; a.h0 = h0; a.y = y; a.h_final = h_final;
   if (!p.chunked) return cuda_status(launch_delta_steps(a, cs));
   a.err = static_cast<uint32_t *>(workspace);
-  a.records = static_cast<uint8_t *>(workspace) + kErrBytes;
+  a.records = static_cast<uint8_t *>(workspace) + p.o_rec;
   a.rec_bytes = delta_record_bytes(false);
   a.wait_ns = wait_limit(pb);
   if (cudaMemsetAsync(a.err, 0, 4, cs) != cudaSuccess) return PDSSM_ERR_CUDA;
@@ -243,9 +254,9 @@ pdssm_status pdssm_delta_fwd(const pdssm_delta_problem *pb, const void *q, const
 pdssm_status pdssm_delta_bwd_workspace_size(const pdssm_delta_problem *pb, size_t *bytes) {
   if (!bytes) return PDSSM_ERR_INVALID_ARG;
   DeltaPlan p;
-  pdssm_status st = plan_delta(pb, &p);
+  pdssm_status st = plan_delta(pb, true, &p);
   if (st != PDSSM_OK) return st;
-  *bytes = p.bwd_bytes;
+  *bytes = p.bytes;
   return PDSSM_OK;
 }
 
@@ -254,7 +265,7 @@ pdssm_status pdssm_delta_bwd(const pdssm_delta_problem *pb, const void *q, const
                              const float *dh_final, void *dq, void *dk, void *dv, void *dg, void *dbeta, float *dh0,
                              void *workspace, size_t workspace_bytes, pdssm_stream_t stream) {
   DeltaPlan p;
-  pdssm_status st = plan_delta(pb, &p);
+  pdssm_status st = plan_delta(pb, true, &p);
   if (st != PDSSM_OK) return st;
   const size_t es = dtype_size(pb->in_t), gs = dtype_size(pb->gate_t);
   if (p.rows * pb->heads > 0 &&
@@ -265,7 +276,7 @@ pdssm_status pdssm_delta_bwd(const pdssm_delta_problem *pb, const void *q, const
       !aligned(dbeta, gs) || !aligned(lengths, 4) || !aligned(h0, 4) || !aligned(dh_final, 4) || !aligned(dh0, 4) ||
       !aligned(workspace, 16))
     return PDSSM_ERR_INVALID_ARG;
-  if (p.bwd_bytes && (!workspace || workspace_bytes < p.bwd_bytes)) return PDSSM_ERR_WORKSPACE;
+  if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return PDSSM_ERR_WORKSPACE;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   OnDevice on(cs);
   if (on.status() != PDSSM_OK) return on.status();
