@@ -118,7 +118,7 @@ pdssm_status plan_delta(const pdssm_delta_problem *pb, bool bwd, DeltaPlan *pl) 
   p.C = p.chunked ? kChunk : delta_grad_chunk();
   p.nC = (pb->seqlen + p.C - 1) / p.C;
   const size_t records = p.chunked ? (size_t)(p.slices * p.nC * delta_record_bytes(bwd)) : 0;
-  size_t o = p.chunked ? kErrBytes : 0;
+  size_t o = p.chunked || bwd ? kErrBytes : 0;
   if (bwd) {
     // error word, states (chunked: one more a sequence), adjoints, e, du; chunked: <dy, y> and the records
     const size_t state = (size_t)(pb->N * p.Pp) * 4, steps = (size_t)(p.rows * pb->heads * p.Pp) * 4;
@@ -289,8 +289,8 @@ pdssm_status pdssm_delta_bwd(const pdssm_delta_problem *pb, const void *q, const
   a.xcarry = reinterpret_cast<float *>(base + p.o_xcarry);
   a.e = reinterpret_cast<float *>(base + p.o_e);
   a.du = reinterpret_cast<float *>(base + p.o_du);
+  a.err = static_cast<uint32_t *>(workspace);
   if (p.chunked) {
-    a.err = static_cast<uint32_t *>(workspace);
     a.dyy = reinterpret_cast<float *>(base + p.o_dyy);
     a.records = reinterpret_cast<uint8_t *>(base + p.o_rec);
     a.rec_bytes = delta_record_bytes(true);

@@ -101,6 +101,10 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
   tc_fence_after();
   const uint32_t tbase = __shfl_sync(0xffffffffu, *tslot, 0);
 
+  // A wait on another role that runs out (or a call in which one has) leaves the role going on through all
+  // its chunks, on whatever its buffers hold: addresses depend on no data. A loader uses a place again only
+  // when its own copies there have landed, and the block ends when copies and products have.
+
   if (warp == kWriter) {
     if (!SAVE) {
       // y of a chunk: from [step][p] in shared memory, 16 bytes a lane
@@ -148,7 +152,11 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       }
     };
     for (int i = 0, s = 0, turn = 0; i < chunks; ++i) {
-      if (turn) wait_bar(&bars[kFree + s], (turn - 1) & 1, a.err, a.wait_ns);
+      if (turn) {
+        if (a.wait_ns >= kShortNs) wait_bar(&bars[kFree + s], (turn - 1) & 1, a.err, a.wait_ns);
+        else wait_slow<false>(&bars[kFree + s], (turn - 1) & 1, a.err, a.wait_ns);
+        wait_own(&bars[kFull + s], (turn - 1) & 1, a.err);  // done for long, unless a wait has run out
+      }
       uint8_t *st = smem + s * Lay::kStage;
       uint64_t *full = &bars[kFull + s];
       const int live = (int)min((int64_t)kChunk, len - (int64_t)i * kChunk);
@@ -181,6 +189,9 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       if (SAVE && i >= 1) load_dy(i - 1);
     }
     if (SAVE && chunks > 0) load_dy(chunks - 1);
+    cp_async_commit();
+    cp_async_wait<0>();
+    for (int i = max(chunks - Lay::kStages, 0); i < chunks; ++i) wait_own(&bars[kFull + i % Lay::kStages], (i / Lay::kStages) & 1, a.err);
   } else if (warp == kIssuer) {
     // The whole warp goes through the loop and one lane issues: descriptors and addresses
     // are then uniform (computed by one lane alone they cost about 70 cycles a product,
@@ -271,7 +282,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
     if (chunks > 0) {
       if (elect_one()) mma_commit(&bars[kEnd]);
       __syncwarp();
-      wait_bar(&bars[kEnd], 0, a.err, 2000000000ull);
+      wait_own(&bars[kEnd], 0, a.err);
     }
   } else {
     // the state's warps

@@ -90,20 +90,35 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 
+constexpr uint64_t kShortNs = 1000000, kOwnNs = 2000000000ull;
+
 // Waits for the barrier's phase for at most limit_ns; then records the timeout and
 // returns false (the caller goes on without waiting, on data inside its buffers).
-static __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, uint32_t *err, uint64_t limit_ns) {
+// A wait on another role (OWN false) also ends when the call has run out of time anywhere.
+template <bool OWN>
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, uint32_t *err, uint64_t limit_ns) {
   const uint64_t t0 = now_ns();
-  while (!sm100::mbar_try_wait_sleep(bar, parity, 2000)) {
-    if (now_ns() - t0 > limit_ns) {
+  // the waiting instruction may sleep longer than a short limit
+  while (!(limit_ns < kShortNs ? sm100::mbar_test_wait(bar, parity) : sm100::mbar_try_wait_sleep(bar, parity, 2000))) {
+    if (now_ns() - t0 > limit_ns || (!OWN && (*reinterpret_cast<volatile uint32_t *>(err) & kErrTimeout))) {
       flag_error(err, kErrTimeout);
       return false;
     }
   }
   return true;
 }
+// On another role.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, uint32_t *err, uint64_t limit_ns) {
-  return sm100::mbar_try_wait(bar, parity) || wait_slow(bar, parity, err, limit_ns);
+  return sm100::mbar_try_wait(bar, parity) || wait_slow<false>(bar, parity, err, limit_ns);
+}
+// On the caller's own copies or products in flight. The tries in place rarely leave the call to be
+// made (the gradients' launch of 256 sequences of 2,048 steps, 64 x 64: 371 -> 330 us; in the chains
+// of the roles' waits the loop is slower, 150 -> 177 us).
+__device__ __forceinline__ void wait_own(uint64_t *bar, uint32_t parity, uint32_t *err) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (sm100::mbar_try_wait(bar, parity)) return;
+  wait_slow<true>(bar, parity, err, kOwnNs);
 }
 
 // W fp32 values as packed bf16 parts 0 .. PARTS - 1 into columns col, col + stride, ... of the

@@ -70,6 +70,8 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
   tc_fence_after();
   const uint32_t tbase = __shfl_sync(0xffffffffu, *tslot, 0);
 
+  // Waits that run out: as in delta_chunk.cu.
+
   // Turn i works on chunk chunks - 1 - i.
   if (warp >= kLoader0 + kLoaders) {
     // the block has one warp more than this needs
@@ -79,7 +81,11 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
     using B = const __nv_bfloat16;
     for (int i = 0, s = 0, turn = 0; i < chunks; ++i) {
       const int chunk = chunks - 1 - i;
-      if (turn) wait_bar(&bars[kFree + s], (turn - 1) & 1, a.err, a.wait_ns);
+      if (turn) {
+        if (a.wait_ns >= kShortNs) wait_bar(&bars[kFree + s], (turn - 1) & 1, a.err, a.wait_ns);
+        else wait_slow<false>(&bars[kFree + s], (turn - 1) & 1, a.err, a.wait_ns);
+        wait_own(&bars[kFull + s], (turn - 1) & 1, a.err);  // done for long, unless a wait has run out
+      }
       uint8_t *st = smem + s * Lay::kStage;
       uint64_t *full = &bars[kFull + s];
       const int live = (int)min((int64_t)kChunk, len - (int64_t)chunk * kChunk);
@@ -104,6 +110,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       }
       if (++s == Lay::kStages) s = 0, ++turn;
     }
+    for (int i = max(chunks - Lay::kStages, 0); i < chunks; ++i) wait_own(&bars[kFull + i % Lay::kStages], (i / Lay::kStages) & 1, a.err);
   } else if (warp == kIssuer) {
     constexpr uint32_t idS = idesc_bf16_f32(PM, kChunk, false, false), idT = idesc_bf16_f32(PM, kChunk, false, true),
                        idD = idesc_bf16_f32(PM, NP, false, true);
@@ -173,7 +180,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
     if (chunks > 0) {
       if (elect_one()) mma_commit(&bars[kEnd]);
       __syncwarp();
-      wait_bar(&bars[kEnd], 0, a.err, 2000000000ull);
+      wait_own(&bars[kEnd], 0, a.err);
     }
   } else {
     const int quarter = warp & 3, up = warp >> 2;

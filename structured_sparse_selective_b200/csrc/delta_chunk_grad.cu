@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
 #pragma unroll
       for (int k = 0; k < kPer; ++k) xh = sum4(sx[k][0], sh[k][0], sum4(sx[k][1], sh[k][1], xh));
     }
-    wait_bar(&bars[0], ph, a.err, 2000000000ull);
+    wait_own(&bars[0], ph, a.err);
     tc_fence_after();
     put_state(sx);
     {
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
         }
       }
     }
-    wait_bar(&bars[1], ph, a.err, 2000000000ull);
+    wait_own(&bars[1], ph, a.err);
     tc_fence_after();
     {
       const float fade = scal[kChunk + row];

@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, NP == 64 ? 6 : 4) delta_prep_kernel(
       out[160 + lane] = make_float2((float)(G[0] - (double)(float)G[0]), (float)(G[1] - (double)(float)G[1]));
       if (hh + 1 < r_heads) fetch_gates(h + 1);
     }
-    if (hh == 0) wait_bar(bar, 0, a.err, 2000000000ull);
+    if (hh == 0) wait_own(bar, 0, a.err);
     __syncthreads();
     tc_fence_after();
     // a thread has one row of the accumulator: rows of K K^T in threads 0-63, of Q K^T in 64-127;

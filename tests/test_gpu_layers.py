@@ -342,3 +342,159 @@ def test_a_layer_and_its_gradients_together(dt):
     # the next token from the state that the segment left
     nxt = {n: x[:, :1].contiguous() for n, x in a.items()}
     check_forward(pd.delta_forward(**nxt, h0=out["h_final"].clone()), nxt, out["h_final"])
+
+
+# ------------------------------------------------------- paths, pointers, sizes and failures
+
+PATHS = [  # batch, seqlen, qk_heads, heads, N, P: short and long runs with few blocks and with more than the SMs
+    (1, 9, 1, 1, 64, 64), (2, 12, 1, 2, 32, 16), (1, 41, 2, 2, 64, 64), (37, 13, 4, 16, 16, 8), (37, 12, 8, 16, 8, 4),
+    (5, 70, 4, 16, 64, 64), (5, 66, 4, 16, 64, 72), (5, 64, 8, 16, 72, 64), (3, 130, 2, 26, 65, 66),
+]
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("c", PATHS)
+def test_delta_on_every_path(c, dt):
+    a, h0 = delta_case(c, dt, seed=21)
+    check_forward(pd.delta_forward(**a, h0=h0), a, h0)
+    dy, dh = gradients_in(a)
+    check_backward(pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh), a, h0, dy, dh)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_delta_by_the_reference_path(dt):
+    a, h0 = delta_case((2, 150, 1, 2, 64, 40), dt)
+    dy, dh = gradients_in(a)
+    with pd.KernelTrace() as tr:
+        check_forward(pd.delta_forward(**a, h0=h0, flags=pd.FLAG_REFERENCE_PATH), a, h0)
+        check_backward(pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh, flags=pd.FLAG_REFERENCE_PATH), a, h0, dy, dh)
+    assert tr.names == ["delta_steps", "delta_steps_both", "delta_grad"]
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("L", [1, 11, 150])
+def test_delta_at_unaligned_pointers(dt, L):
+    a, h0 = delta_case((2, L, 1, 2, 64, 64), dt)
+    dy, dh = gradients_in(a)
+
+    def moved(x):  # one value behind an aligned address
+        room = torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")[1:].view(x.shape)
+        return room.copy_(x)
+
+    am, hm = {n: moved(x) for n, x in a.items()}, moved(h0)
+    check_forward(pd.delta_forward(**am, h0=hm, h_final=hm), a, h0)
+    hm = moved(h0)
+    check_backward(pd.delta_backward(**am, dy=moved(dy), h0=hm, dh_final=moved(dh)), a, h0, dy, dh)
+    # outputs too, through the entry points that take them
+    pb = pd._delta_problem(*(a[n] for n in ("q", "k", "v", "g", "beta")), h0, None, None, 0)[0]
+    ws = lambda n: torch.empty(max(1, n), dtype=torch.uint8, device="cuda")  # noqa: E731
+    y, hf = moved(a["v"]), moved(h0)
+    ins = [am[n] for n in ("q", "k", "v", "g", "beta")]
+    pd.pdssm_delta_fwd(pb, *ins, None, h0, y, hf, ws(pd.pdssm_delta_workspace_size(pb)))
+    check_forward({"y": y, "h_final": hf}, a, h0)
+    out = {"d" + n: moved(a[n]) for n in ("q", "k", "v", "g", "beta")} | {"dh0": moved(h0)}
+    pd.pdssm_delta_bwd(pb, *ins, None, h0, dy, dh, *out.values(), ws(pd.pdssm_delta_bwd_workspace_size(pb)))
+    check_backward(out, a, h0, dy, dh)
+
+
+@pytest.mark.parametrize("what", ["forward", "backward"])
+@pytest.mark.parametrize("c", [(2, 600, 1, 2, 64, 64), (2, 600, 1, 2, 128, 128), (5, 300, 2, 16, 128, 64)])
+def test_delta_short_waits_report_a_timeout_and_the_next_call_is_clean(c, what):
+    """The chunk kernels' waits of one role on another are bounded: with waits of a microsecond some run out, which is
+    reported, ends the call and leaves the device and the next call as they were."""
+    a, h0 = delta_case(c, torch.bfloat16)
+    dy, dh = gradients_in(a)
+    pb = pd._delta_problem(*(a[n] for n in ("q", "k", "v", "g", "beta")), h0, None, None, 0)[0]
+    size = pd.pdssm_delta_workspace_size(pb) if what == "forward" else pd.pdssm_delta_bwd_workspace_size(pb)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+
+    def call(flags):
+        if what == "forward":
+            return pd.delta_forward(**a, h0=h0, flags=flags, workspace=ws)
+        return pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh, flags=flags, workspace=ws)
+
+    clean = call(0)
+    assert pd.pdssm_read_device_check(ws) == 0
+    for _ in range(3):
+        call(pd.FLAG_SHORT_WAITS)
+        assert pd.pdssm_read_device_check(ws) == 6
+    again = call(0)
+    assert pd.pdssm_read_device_check(ws) == 0
+    for n in clean:
+        assert torch.equal(again[n], clean[n]), n
+
+
+def test_delta_error_word_of_a_path_without_waits():
+    a, h0 = delta_case((1, 20, 1, 1, 16, 16), torch.float32)
+    pb = pd._delta_problem(*(a[n] for n in ("q", "k", "v", "g", "beta")), h0, None, None, 0)[0]
+    ws = torch.full((pd.pdssm_delta_bwd_workspace_size(pb),), 255, dtype=torch.uint8, device="cuda")
+    dy, dh = gradients_in(a)
+    check_backward(pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh, workspace=ws, flags=pd.FLAG_SHORT_WAITS), a, h0, dy, dh)
+    assert pd.pdssm_read_device_check(ws) == 0
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_delta_values_that_are_not_finite_stay_in_their_sequences_and_heads(dt):
+    a, h0 = delta_case((3, 140, 1, 2, 64, 32), dt)
+    dy, dh = gradients_in(a)
+    want, wantb = pd.delta_forward(**a, h0=h0), pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh)
+    a["v"][1, 70, 1, 3] = float("nan")
+    a["k"][2, 3] = float("inf")
+    got, gotb = pd.delta_forward(**a, h0=h0), pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh)
+    torch.cuda.synchronize()
+    assert torch.equal(got["y"][0], want["y"][0]) and torch.equal(got["y"][1, :, 0], want["y"][1, :, 0])
+    keep = torch.arange(32, device="cuda") != 3  # a value's column keeps to itself
+    assert torch.equal(got["y"][1, :, 1][:, keep], want["y"][1, :, 1][:, keep]) and got["y"][1, 71:, 1, 3].isnan().all()
+    assert torch.equal(got["h_final"][0], want["h_final"][0])
+    for n in wantb:
+        assert torch.equal(gotb[n][0], wantb[n][0]), n
+    assert torch.equal(gotb["dv"][1, :, 0], wantb["dv"][1, :, 0])
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_delta_offsets_beyond_32_bits(dt):
+    """More than 2^31 values: the last sequence is the same, bit for bit, as it is alone (fp32: by steps)."""
+    Bt, L, Hk, H, N, P = 65, 2049, 1, 128, 16, 128
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=gen, dtype=dt)  # noqa: E731
+    a = dict(q=0.25 * rand(Bt, L, Hk, N), k=0.25 * rand(Bt, L, Hk, N), v=rand(Bt, L, H, P), g=-0.05 * rand(Bt, L, H).abs(),
+             beta=torch.sigmoid(rand(Bt, L, H)))
+    assert a["v"].numel() > 2 ** 31
+    dy = rand(Bt, L, H, P)
+    last = {n: x[-1:].contiguous() for n, x in a.items()}
+    out, alone = pd.delta_forward(**a), pd.delta_forward(**last)
+    assert torch.equal(out["y"][-1], alone["y"][0]) and torch.equal(out["h_final"][-1], alone["h_final"][0])
+    del out
+    out, alone = pd.delta_backward(**a, dy=dy), pd.delta_backward(**last, dy=dy[-1:].contiguous())
+    for n in alone:
+        assert torch.equal(out[n][-1], alone[n][0]), n
+    del out, a, dy
+    torch.cuda.empty_cache()
+
+
+def test_qk_norm_of_many_heads_and_offsets_beyond_32_bits():
+    # more heads than a block goes through at once
+    q, k, kw = norm_case((1, 2, 4500, 4099, 16, 8, False, "rms"), torch.float32)
+    out, back = pd.qk_norm(q, k, **kw), pd.qk_norm_backward(q, k, q, k, **kw)
+    for n, x in (("q", q), ("k", k)):
+        close(n, out[n], norm_oracle(x, kw, "w" + n), 16)
+        dx, dw = norm_oracle(x, kw, "w" + n, x)
+        xs = npy(x)  # S: the size of dx's two terms, as above
+        terms = np.sqrt(2) * np.abs(xs).max(-1, keepdims=True) * np.abs(npy(kw["w" + n])).max() / np.sqrt((xs ** 2).mean(-1, keepdims=True))
+        close("d" + n, back["d" + n], dx, 16, axes=(-1,), operands=np.maximum(1.0, terms))
+        close("dw" + n, back["dw" + n], dw, x.numel())
+    big = torch.randn(1, 2 ** 20 + 1, 16, 128, device="cuda", dtype=torch.bfloat16)
+    assert big.numel() > 2 ** 31
+    k, w = big[:, :, :1].contiguous(), torch.rand(128, device="cuda") + 0.5
+    freq, pos = torch.rand(32, device="cuda") * 0.1, torch.arange(2 ** 20 + 1, device="cuda", dtype=torch.int32)[None]
+    kw = dict(inv_freq=freq, wq=w)
+    out = pd.qk_norm(big, k, positions=pos, **kw)
+    alone = pd.qk_norm(big[:, -1:].contiguous(), k[:, -1:].contiguous(), positions=pos[:, -1:].contiguous(), **kw)
+    assert torch.equal(out["q"][:, -1:], alone["q"]) and torch.equal(out["k"][:, -1:], alone["k"])
+    del out
+    back = pd.qk_norm_backward(big, k, big, k, positions=pos, **kw)
+    alone = pd.qk_norm_backward(big[:, -1:].contiguous(), k[:, -1:].contiguous(), big[:, -1:].contiguous(), k[:, -1:].contiguous(),
+                                positions=pos[:, -1:].contiguous(), **kw)
+    assert torch.equal(back["dq"][:, -1:], alone["dq"]) and torch.equal(back["dk"][:, -1:], alone["dk"])
+    del back, big
+    torch.cuda.empty_cache()
