@@ -77,8 +77,8 @@ pdssm_status run_norm(const pdssm_norm_problem *pb, QkNormArgs &a, int64_t rows,
 
 struct DeltaPlan {
   int64_t rows, slices, Pp, C, nC;
-  bool chunked;  // by chunks on the tensor cores
-  size_t o_carry, o_xcarry, o_e, o_du, o_dyy, o_rec, bytes;
+  bool chunked, by_rows;  // by chunks on the tensor cores, or in fp32
+  size_t o_carry, o_xcarry, o_e, o_du, o_dyy, o_rec, o_heads, bytes;
 };
 
 constexpr size_t kErrBytes = 256;
@@ -95,6 +95,21 @@ bool chunks_apply(const pdssm_delta_problem *pb, bool bwd) {
   if (pb->in_t != PDSSM_BF16 || (pb->flags & PDSSM_FLAG_REFERENCE_PATH)) return false;
   if (bwd) return pb->seqlen > 8;
   return pb->seqlen > (pb->batch * pb->heads >= 4 * 148 ? 12 : 40);
+}
+
+// The same for fp32 inputs and chunks of 32 steps in fp32 (us; steps, chunks; S sequences x heads, N = P):
+//   forward   N = 64:  S = 8: 128 steps 30, 29; 512 steps 93, 46.  S = 64: 128 steps 31, 40; 512 steps 103, 90.
+//                      S = 128: 512 steps 126, 156.  S = 1024: 512 steps 902, 969.
+//             N = 128: S = 64: 64 steps 46, 50; 128 steps 85, 82.  S = 256: 128 steps 308, 240; 512 steps 1205, 864.
+//   backward  N = 64:  S = 64: 64 steps 46, 37; 128 steps 80, 53; 512 steps 268, 151.  S = 256: 512 steps 474, 491.
+//             N = 128: S = 64: 64 steps 92, 80; 512 steps 638, 450.  S = 256: 512 steps 2033, 1433.
+// A step's chain of shuffles is what few sequences wait for; many fill the SMs either way, and then
+// steps do fewer FMAs, unless a head is so large that its columns do not fit in a few registers a lane.
+bool rows_apply(const pdssm_delta_problem *pb, bool bwd) {
+  if (pb->in_t != PDSSM_F32 || (pb->flags & PDSSM_FLAG_REFERENCE_PATH)) return false;
+  if (pb->N > 64) return pb->seqlen > (bwd ? 64 : 96);
+  const int64_t slices = pb->batch * pb->heads;
+  return bwd ? slices <= 148 && pb->seqlen > 96 : slices <= 64 && pb->seqlen > 256;
 }
 
 pdssm_status plan_delta(const pdssm_delta_problem *pb, bool bwd, DeltaPlan *pl) {
@@ -115,10 +130,11 @@ pdssm_status plan_delta(const pdssm_delta_problem *pb, bool bwd, DeltaPlan *pl) 
   if (!mul_ok(pb->batch, pb->seqlen, &p.rows) || !mul_ok(p.slices, (pb->seqlen + kChunk) * 8192, &bytes))
     return PDSSM_ERR_UNSUPPORTED;
   p.chunked = chunks_apply(pb, bwd);
+  p.by_rows = rows_apply(pb, bwd);
   p.C = p.chunked ? kChunk : delta_grad_chunk();
   p.nC = (pb->seqlen + p.C - 1) / p.C;
   const size_t records = p.chunked ? (size_t)(p.slices * p.nC * delta_record_bytes(bwd)) : 0;
-  size_t o = p.chunked || bwd ? kErrBytes : 0;
+  size_t o = p.chunked || p.by_rows || bwd ? kErrBytes : 0;
   if (bwd) {
     // error word, states (chunked: one more a sequence), adjoints, e, du; chunked: <dy, y> and the records
     const size_t state = (size_t)(pb->N * p.Pp) * 4, steps = (size_t)(p.rows * pb->heads * p.Pp) * 4;
@@ -128,7 +144,8 @@ pdssm_status plan_delta(const pdssm_delta_problem *pb, bool bwd, DeltaPlan *pl) 
     p.o_du = o; o = align256(o + steps);
     p.o_dyy = o; o = align256(o + (p.chunked ? (size_t)(p.rows * pb->heads) * 16 : 0));
   }
-  p.o_rec = o; o = align256(o + records);
+  p.o_rec = o; o = align256(o + (p.by_rows ? (size_t)(pb->batch * pb->qk_heads * p.nC * delta_rows_key_bytes(pb->N)) : records));
+  p.o_heads = o; o = align256(o + (p.by_rows ? (size_t)(p.slices * p.nC * delta_rows_head_bytes(bwd)) : 0));
   p.bytes = o;
   *pl = p;
   return PDSSM_OK;
@@ -145,6 +162,18 @@ DeltaArgs delta_args(const pdssm_delta_problem *pb, const DeltaPlan &p) {
   a.in_t = pb->in_t; a.gate_t = pb->gate_t;
   a.scale = pb->scale;
   return a;
+}
+
+// Error word, records and wait limit of the kernels with roles.
+pdssm_status use_records(const pdssm_delta_problem *pb, const DeltaPlan &p, bool bwd, void *workspace, DeltaArgs &a, cudaStream_t cs) {
+  char *base = static_cast<char *>(workspace);
+  a.err = static_cast<uint32_t *>(workspace);
+  a.records = reinterpret_cast<uint8_t *>(base + p.o_rec);
+  a.rec_bytes = delta_record_bytes(bwd);
+  a.keys = reinterpret_cast<float *>(base + p.o_rec);
+  a.heads = reinterpret_cast<float *>(base + p.o_heads);
+  a.wait_ns = wait_limit(pb);
+  return cudaMemsetAsync(a.err, 0, 4, cs) == cudaSuccess ? PDSSM_OK : PDSSM_ERR_CUDA;
 }
 
 }  // namespace
@@ -241,12 +270,9 @@ pdssm_status pdssm_delta_fwd(const pdssm_delta_problem *pb, const void *q, const
   if (p.slices == 0) return PDSSM_OK;
   DeltaArgs a = delta_args(pb, p);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lengths = lengths; a.h0 = h0; a.y = y; a.h_final = h_final;
-  if (!p.chunked) return cuda_status(launch_delta_steps(a, cs));
-  a.err = static_cast<uint32_t *>(workspace);
-  a.records = static_cast<uint8_t *>(workspace) + p.o_rec;
-  a.rec_bytes = delta_record_bytes(false);
-  a.wait_ns = wait_limit(pb);
-  if (cudaMemsetAsync(a.err, 0, 4, cs) != cudaSuccess) return PDSSM_ERR_CUDA;
+  if (!p.chunked && !p.by_rows) return cuda_status(launch_delta_steps(a, cs));
+  if ((st = use_records(pb, p, false, workspace, a, cs)) != PDSSM_OK) return st;
+  if (p.by_rows) return cuda_status(launch_delta_rows(a, false, cs));
   if ((st = cuda_status(launch_delta_prep(a, false, cs))) != PDSSM_OK) return st;
   return cuda_status(launch_delta_chunk(a, cs));
 }
@@ -289,18 +315,19 @@ pdssm_status pdssm_delta_bwd(const pdssm_delta_problem *pb, const void *q, const
   a.xcarry = reinterpret_cast<float *>(base + p.o_xcarry);
   a.e = reinterpret_cast<float *>(base + p.o_e);
   a.du = reinterpret_cast<float *>(base + p.o_du);
-  a.err = static_cast<uint32_t *>(workspace);
+  if (p.chunked || p.by_rows) {
+    if ((st = use_records(pb, p, true, workspace, a, cs)) != PDSSM_OK) return st;
+  } else {
+    a.err = static_cast<uint32_t *>(workspace);
+  }
   if (p.chunked) {
     a.dyy = reinterpret_cast<float *>(base + p.o_dyy);
-    a.records = reinterpret_cast<uint8_t *>(base + p.o_rec);
-    a.rec_bytes = delta_record_bytes(true);
-    a.wait_ns = wait_limit(pb);
-    if (cudaMemsetAsync(a.err, 0, 4, cs) != cudaSuccess) return PDSSM_ERR_CUDA;
     if ((st = cuda_status(launch_delta_prep(a, true, cs))) != PDSSM_OK) return st;
     if ((st = cuda_status(launch_delta_chunk_both(a, cs))) != PDSSM_OK) return st;
     return cuda_status(launch_delta_chunk_grad(a, cs));
   }
-  if ((st = cuda_status(launch_delta_steps_both(a, cs))) != PDSSM_OK) return st;
+  st = cuda_status(p.by_rows ? launch_delta_rows(a, true, cs) : launch_delta_steps_both(a, cs));
+  if (st != PDSSM_OK) return st;
   if (p.rows > 0) st = cuda_status(launch_delta_grad(a, cs));
   return st;
 }

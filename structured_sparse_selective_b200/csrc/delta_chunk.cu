@@ -101,9 +101,11 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
   tc_fence_after();
   const uint32_t tbase = __shfl_sync(0xffffffffu, *tslot, 0);
 
-  // A wait on another role that runs out (or a call in which one has) leaves the role going on through all
-  // its chunks, on whatever its buffers hold: addresses depend on no data. A loader uses a place again only
-  // when its own copies there have landed, and the block ends when copies and products have.
+  // Every wait of a role on another is bounded. When one has run out, anywhere in the launch, all waits that
+  // are not over end, and each role leaves its loop at its next unfinished wait, a warp (the loaders) as one:
+  // nothing works on operands that are not there. The loaders and the issuer then wait for their own
+  // copies and products, and the block ends.
+  const auto wait = [&](int which, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(&bars[which], parity, a.err, a.wait_ns)); };
 
   if (warp == kWriter) {
     if (!SAVE) {
@@ -113,7 +115,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       const uint8_t *tile = smem + Lay::kYOff;
       const int P = (int)min((int64_t)PM, a.P - p0);
       for (int i = 0; i < chunks; ++i) {
-        wait_bar(&bars[kOut], i & 1, a.err, a.wait_ns);
+        if (!wait(kOut, i & 1)) break;
         const int live = (int)min((int64_t)kChunk, len - (int64_t)i * kChunk);
         __nv_bfloat16 *dst = y + (int64_t)i * kChunk * step;
         constexpr int G = PM / 8, kRows = 32 / G;
@@ -137,9 +139,15 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
     const int tid = threadIdx.x - 32 * kLoader0;
     const bool copies = wide && wide_v && a.N == NP && a.P - p0 >= PM;  // nothing is written by the threads themselves
     using B = const __nv_bfloat16;
+    const auto go_on = [&](int which, uint32_t parity) {
+      return all_of<32 * kLoaders>(wait_bar(&bars[which], parity, a.err, a.wait_ns));
+    };
+    int issued = 0, dys = 0;
+    // a short limit runs out here: nothing has been asked for yet
+    if (a.wait_ns < kShortNs && chunks > 0) all_of<32 * kLoaders>(wait_slow<false>(&bars[kFull], 0, a.err, a.wait_ns));
     // SAVE: dY of chunk i, which is wanted at the chunk's end, comes behind the next chunk's stage
     const auto load_dy = [&](int i) {
-      if (i >= 1) wait_bar(&bars[kDyFree], (i - 1) & 1, a.err, a.wait_ns);
+      if (i >= 1 && !go_on(kDyFree, (i - 1) & 1)) return false;
       const int live = (int)min((int64_t)kChunk, len - (int64_t)i * kChunk);
       load_tile<PM / 8, 16, 2 * PM, 32 * kLoaders>(smem + Lay::kYOff, static_cast<B *>(a.dy), b * a.L + (int64_t)i * kChunk, a.H, h, a.P,
                                                    p0, live, wide_v, tid);
@@ -150,13 +158,11 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
         cp_async_wait<0>();
         mbar_arrive(&bars[kDyFull]);
       }
+      ++dys;
+      return true;
     };
     for (int i = 0, s = 0, turn = 0; i < chunks; ++i) {
-      if (turn) {
-        if (a.wait_ns >= kShortNs) wait_bar(&bars[kFree + s], (turn - 1) & 1, a.err, a.wait_ns);
-        else wait_slow<false>(&bars[kFree + s], (turn - 1) & 1, a.err, a.wait_ns);
-        wait_own(&bars[kFull + s], (turn - 1) & 1, a.err);  // done for long, unless a wait has run out
-      }
+      if (turn && !go_on(kFree + s, (turn - 1) & 1)) break;
       uint8_t *st = smem + s * Lay::kStage;
       uint64_t *full = &bars[kFull + s];
       const int live = (int)min((int64_t)kChunk, len - (int64_t)i * kChunk);
@@ -186,12 +192,12 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
         mbar_arrive(full);
       }
       if (++s == Lay::kStages) s = 0, ++turn;
-      if (SAVE && i >= 1) load_dy(i - 1);
+      ++issued;
+      if (SAVE && i >= 1 && !load_dy(i - 1)) break;
     }
-    if (SAVE && chunks > 0) load_dy(chunks - 1);
-    cp_async_commit();
-    cp_async_wait<0>();
-    for (int i = max(chunks - Lay::kStages, 0); i < chunks; ++i) wait_own(&bars[kFull + i % Lay::kStages], (i / Lay::kStages) & 1, a.err);
+    if (SAVE && chunks > 0 && issued == chunks) load_dy(chunks - 1);
+    if (SAVE && dys > 0) wait_own(&bars[kDyFull], (dys - 1) & 1, a.err);
+    for (int i = max(issued - Lay::kStages, 0); i < issued; ++i) wait_own(&bars[kFull + i % Lay::kStages], (i / Lay::kStages) & 1, a.err);
   } else if (warp == kIssuer) {
     // The whole warp goes through the loop and one lane issues: descriptors and addresses
     // are then uniform (computed by one lane alone they cost about 70 cycles a product,
@@ -202,11 +208,11 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       const uint32_t ph = i & 1, sk = base + s * Lay::kStage, sq = sk + Lay::kQ, te = sk + Lay::kRecOff, sa = te + 3 * kSquare;
       const uint64_t dk = smem_desc(sk, kChunkGroup, 128), dq = smem_desc(sq, kChunkGroup, 128), dkt = smem_desc(sk, 128, kChunkGroup),
                      dte = smem_desc(te, 1024, 128), da = smem_desc(sa, 1024, 128);
-      wait_bar(&bars[kFull + s], turn & 1, a.err, a.wait_ns);
+      if (!wait(kFull + s, turn & 1)) goto issued_all;
       fence_proxy_async_smem();  // the loaders' writes, seen through the barrier, before the tensor core's reads
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        wait_bar(&bars[kH + f], ph, a.err, a.wait_ns);
+        if (!wait(kH + f, ph)) goto issued_all;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -219,7 +225,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
         __syncwarp();
       }
       // Q H into Yh, once the chunk before has been read out of it
-      if (i >= 1) wait_bar(&bars[kRead], (i - 1) & 1, a.err, a.wait_ns);
+      if (i >= 1 && !wait(kRead, (i - 1) & 1)) goto issued_all;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -232,7 +238,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       __syncwarp();
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        wait_bar(&bars[kR + f], ph, a.err, a.wait_ns);
+        if (!wait(kR + f, ph)) goto issued_all;
         tc_fence_after();
         if (elect_one()) {
           // R Te^T: parts (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
@@ -250,7 +256,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       }
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        wait_bar(&bars[kU1 + f], ph, a.err, a.wait_ns);
+        if (!wait(kU1 + f, ph)) goto issued_all;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -262,7 +268,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
         }
         __syncwarp();
       }
-      wait_bar(&bars[kU2], ph, a.err, a.wait_ns);
+      if (!wait(kU2, ph)) goto issued_all;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -279,6 +285,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       __syncwarp();
       if (++s == Lay::kStages) s = 0, ++turn;
     }
+  issued_all:
     if (chunks > 0) {
       if (elect_one()) mma_commit(&bars[kEnd]);
       __syncwarp();
@@ -317,15 +324,16 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
     // the thread's values of chunk i, two steps a register: read a product ahead of their use
     uint32_t vv[W / 2];
     const auto fetch_v = [&](int s, int turn) {
-      wait_bar(&bars[kFull + s], turn & 1, a.err, a.wait_ns);
+      if (!wait(kFull + s, turn & 1)) return false;
       const uint16_t *v = reinterpret_cast<const uint16_t *>(smem + s * Lay::kStage + Lay::kVOff) + c0 * PM + row;
 #pragma unroll
       for (int c = 0; c < W / 2; ++c) vv[c] = v[2 * c * PM] | ((uint32_t)v[(2 * c + 1) * PM] << 16);
+      return true;
     };
     // y of chunk i, rounded, two steps a register, and its way to the writer
     uint32_t yy[SAVE ? 1 : W / 2];
     const auto put_y = [&](int i) {
-      if (i >= 1) wait_bar(&bars[kOutFree], (i - 1) & 1, a.err, a.wait_ns);
+      if (i >= 1 && !wait(kOutFree, (i - 1) & 1)) return false;
       uint16_t *out = reinterpret_cast<uint16_t *>(smem + Lay::kYOff) + c0 * PM + row;
 #pragma unroll
       for (int c = 0; c < (SAVE ? 1 : W / 2); ++c) {
@@ -334,9 +342,10 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kOut]);
+      return true;
     };
     if (chunks > 0) {
-      fetch_v(0, 0);
+      if (!fetch_v(0, 0)) goto state_done;
       store_parts<PM, WN, 3>(tX, NP / 2, st);
       ready(kH + up);
     }
@@ -347,16 +356,16 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       if (SAVE) save_state(i);
       float x[W], w[W];
       load_scalars<W>(w, scal + c0);
-      wait_bar(&bars[kDoneS], ph, a.err, a.wait_ns);
+      if (!wait(kDoneS, ph)) goto state_done;
       tc_fence_after();
       load_cols<PM, W>(tZ, x);
 #pragma unroll
       for (int c = 0; c < W; ++c) x[c] = fmaf(-w[c], x[c], c & 1 ? high_half(vv[c / 2]) : low_half(vv[c / 2]));
       store_parts<PM, W, 3>(tR, 32, x);
       ready(kR + up);
-      if (!SAVE && i >= 1) put_y(i - 1);
+      if (!SAVE && i >= 1 && !put_y(i - 1)) goto state_done;
       load_scalars<W>(w, scal + 2 * kChunk + c0);
-      wait_bar(&bars[kDoneU], ph, a.err, a.wait_ns);
+      if (!wait(kDoneU, ph)) goto state_done;
       tc_fence_after();
       load_cols<PM, W>(tYa, x);
 #pragma unroll
@@ -376,8 +385,8 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
         ready(kU2);
       }
       if (++next == Lay::kStages) next = 0, ++turn;
-      if (i + 1 < chunks) fetch_v(next, turn);
-      wait_bar(&bars[kDoneD], ph, a.err, a.wait_ns);
+      if (i + 1 < chunks && !fetch_v(next, turn)) goto state_done;
+      if (!wait(kDoneD, ph)) goto state_done;
       tc_fence_after();
       const float last = scal[3 * kChunk];
       {
@@ -393,7 +402,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       }
       // where u's parts lie among those of the state, the product with A has to be done too
       if (Lay::kUy < Lay::kD) {
-        wait_bar(&bars[kDoneY], ph, a.err, a.wait_ns);
+        if (!wait(kDoneY, ph)) goto state_done;
         tc_fence_after();
       }
       if (i + 1 < chunks) {
@@ -401,7 +410,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
         ready(kH + up);
       }
       if (Lay::kUy >= Lay::kD) {
-        wait_bar(&bars[kDoneY], ph, a.err, a.wait_ns);
+        if (!wait(kDoneY, ph)) goto state_done;
         tc_fence_after();
       }
       // y's scalars are read before the stage goes back to the loaders
@@ -418,7 +427,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       for (int c = 0; c < W; ++c) x[c] = fmaf(a.scale * g[c], x[c], w[c]);
       if (SAVE) {
         // <dy, y> of the warp's columns of p: products summed over its rows, a lane ends with one step's
-        wait_bar(&bars[kDyFull], ph, a.err, a.wait_ns);
+        if (!wait(kDyFull, ph)) goto state_done;
         const __nv_bfloat16 *dy = reinterpret_cast<const __nv_bfloat16 *>(smem + Lay::kYOff) + c0 * PM + row;
 #pragma unroll
         for (int c = 0; c < W; ++c) x[c] *= __bfloat162float(dy[c * PM]);
@@ -439,9 +448,11 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
         // y goes to the writer in the next chunk's first pause, or at once behind the last
 #pragma unroll
         for (int c = 0; c < W / 2; ++c) yy[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
-        if (i + 1 == chunks) put_y(i);
+        if (i + 1 == chunks && !put_y(i)) goto state_done;
       }
     }
+  state_done:
+    tmem_wait_st();
     if (SAVE) save_state(chunks);
     if (!SAVE && pin && a.h_final) {
 #pragma unroll

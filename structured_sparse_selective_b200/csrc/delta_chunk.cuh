@@ -92,15 +92,14 @@ __device__ __forceinline__ uint64_t now_ns() {
 
 constexpr uint64_t kShortNs = 1000000, kOwnNs = 2000000000ull;
 
-// Waits for the barrier's phase for at most limit_ns; then records the timeout and
-// returns false (the caller goes on without waiting, on data inside its buffers).
+// Waits for the barrier's phase for at most limit_ns; then records the timeout and returns false.
 // A wait on another role (OWN false) also ends when the call has run out of time anywhere.
 template <bool OWN>
 __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, uint32_t *err, uint64_t limit_ns) {
   const uint64_t t0 = now_ns();
   // the waiting instruction may sleep longer than a short limit
   while (!(limit_ns < kShortNs ? sm100::mbar_test_wait(bar, parity) : sm100::mbar_try_wait_sleep(bar, parity, 2000))) {
-    if (now_ns() - t0 > limit_ns || (!OWN && (*reinterpret_cast<volatile uint32_t *>(err) & kErrTimeout))) {
+    if (now_ns() - t0 >= limit_ns || (!OWN && (*reinterpret_cast<volatile uint32_t *>(err) & kErrTimeout))) {
       flag_error(err, kErrTimeout);
       return false;
     }
@@ -119,6 +118,18 @@ __device__ __forceinline__ void wait_own(uint64_t *bar, uint32_t parity, uint32_
   for (int i = 0; i < 32; ++i)
     if (sm100::mbar_try_wait(bar, parity)) return;
   wait_slow<true>(bar, parity, err, kOwnNs);
+}
+
+// True in all THREADS of some whole warps (by a barrier of their own) if ok is true in all.
+template <int THREADS>
+__device__ __forceinline__ bool all_of(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "n"(THREADS)
+      : "memory");
+  return r != 0;
 }
 
 // W fp32 values as packed bf16 parts 0 .. PARTS - 1 into columns col, col + stride, ... of the

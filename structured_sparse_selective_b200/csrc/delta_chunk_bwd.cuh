@@ -70,7 +70,11 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
   tc_fence_after();
   const uint32_t tbase = __shfl_sync(0xffffffffu, *tslot, 0);
 
-  // Waits that run out: as in delta_chunk.cu.
+  // Every wait of a role on another is bounded. When one has run out, anywhere in the launch, all waits that
+  // are not over end, and each role leaves its loop at its next unfinished wait, a warp (the loaders) as one:
+  // nothing works on operands that are not there. The loaders and the issuer then wait for their own
+  // copies and products, and the block ends.
+  const auto wait = [&](int which, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(&bars[which], parity, a.err, a.wait_ns)); };
 
   // Turn i works on chunk chunks - 1 - i.
   if (warp >= kLoader0 + kLoaders) {
@@ -79,13 +83,15 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
     const int tid = threadIdx.x - 32 * kLoader0;
     const bool copies = wide && wide_v && a.N == NP && a.P - p0 >= PM;  // nothing is written by the threads themselves
     using B = const __nv_bfloat16;
+    const auto go_on = [&](int which, uint32_t parity) {
+      return all_of<32 * kLoaders>(wait_bar(&bars[which], parity, a.err, a.wait_ns));
+    };
+    int issued = 0;
+    // a short limit runs out here: nothing has been asked for yet
+    if (a.wait_ns < kShortNs && chunks > 0) all_of<32 * kLoaders>(wait_slow<false>(&bars[kFull], 0, a.err, a.wait_ns));
     for (int i = 0, s = 0, turn = 0; i < chunks; ++i) {
       const int chunk = chunks - 1 - i;
-      if (turn) {
-        if (a.wait_ns >= kShortNs) wait_bar(&bars[kFree + s], (turn - 1) & 1, a.err, a.wait_ns);
-        else wait_slow<false>(&bars[kFree + s], (turn - 1) & 1, a.err, a.wait_ns);
-        wait_own(&bars[kFull + s], (turn - 1) & 1, a.err);  // done for long, unless a wait has run out
-      }
+      if (turn && !go_on(kFree + s, (turn - 1) & 1)) break;
       uint8_t *st = smem + s * Lay::kStage;
       uint64_t *full = &bars[kFull + s];
       const int live = (int)min((int64_t)kChunk, len - (int64_t)chunk * kChunk);
@@ -109,8 +115,9 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
         mbar_arrive(full);
       }
       if (++s == Lay::kStages) s = 0, ++turn;
+      ++issued;
     }
-    for (int i = max(chunks - Lay::kStages, 0); i < chunks; ++i) wait_own(&bars[kFull + i % Lay::kStages], (i / Lay::kStages) & 1, a.err);
+    for (int i = max(issued - Lay::kStages, 0); i < issued; ++i) wait_own(&bars[kFull + i % Lay::kStages], (i / Lay::kStages) & 1, a.err);
   } else if (warp == kIssuer) {
     constexpr uint32_t idS = idesc_bf16_f32(PM, kChunk, false, false), idT = idesc_bf16_f32(PM, kChunk, false, true),
                        idD = idesc_bf16_f32(PM, NP, false, true);
@@ -119,11 +126,11 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       const uint32_t ph = i & 1, sk = base + s * Lay::kStage, sq = sk + Lay::kTile, tb = sk + Lay::kRecOff, sa = tb + 3 * kSquare;
       const uint64_t dk = smem_desc(sk, kChunkGroup, 128), dkt = smem_desc(sk, 128, kChunkGroup), dqt = smem_desc(sq, 128, kChunkGroup),
                      dtb = smem_desc(tb, 128, 1024), da = smem_desc(sa, 128, 1024);
-      wait_bar(&bars[kFull + s], turn & 1, a.err, a.wait_ns);
+      if (!wait(kFull + s, turn & 1)) goto issued_all;
       fence_proxy_async_smem();  // the loaders' writes, seen through the barrier, before the tensor core's reads
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        wait_bar(&bars[kX + f], ph, a.err, a.wait_ns);
+        if (!wait(kX + f, ph)) goto issued_all;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -143,8 +150,8 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
         __syncwarp();
       }
       // du takes the place of X^T K^T, so all warps have to have read that
-      wait_bar(&bars[kR], ph, a.err, a.wait_ns);
-      wait_bar(&bars[kR + 1], ph, a.err, a.wait_ns);
+      if (!wait(kR, ph)) goto issued_all;
+      if (!wait(kR + 1, ph)) goto issued_all;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -161,7 +168,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       // kU also says that the half's parts of dY diag(exp G) are there
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        wait_bar(&bars[kU + f], ph, a.err, a.wait_ns);
+        if (!wait(kU + f, ph)) goto issued_all;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -177,6 +184,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       }
       if (++s == Lay::kStages) s = 0, ++turn;
     }
+  issued_all:
     if (chunks > 0) {
       if (elect_one()) mma_commit(&bars[kEnd]);
       __syncwarp();
@@ -208,16 +216,17 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
     };
     // dY of turn i as it is, an operand of dY^T A
     const auto store_dy = [&](int s, int turn) {
-      wait_bar(&bars[kFull + s], turn & 1, a.err, a.wait_ns);
+      if (!wait(kFull + s, turn & 1)) return false;
       const uint16_t *dy = reinterpret_cast<const uint16_t *>(smem + s * Lay::kStage + Lay::kDyOff) + c0 * PM + row;
       uint32_t r[W / 2];
 #pragma unroll
       for (int c = 0; c < W / 2; ++c) r[c] = dy[2 * c * PM] | ((uint32_t)dy[(2 * c + 1) * PM] << 16);
       TmemIo<PM, W / 2>::st(tY, r);
+      return true;
     };
     if (chunks > 0) {
       store_parts<PM, WN, 3>(tX, NP / 2, st);
-      store_dy(0, 0);
+      if (!store_dy(0, 0)) goto state_done;
       ready(kX + up);
     }
     for (int i = 0, s = 0, next = 0, turn = 0; i < chunks; ++i, s = next) {
@@ -227,7 +236,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       const float *scal = reinterpret_cast<const float *>(stage + Lay::kRecOff + Lay::kRec - kScalars);
       const __nv_bfloat16 *dy = reinterpret_cast<const __nv_bfloat16 *>(stage + Lay::kDyOff) + c0 * PM + row;
       store_rows<PM, WN>(a.xcarry + ((bh * a.nC + chunk) * a.N + n0) * a.Pp + p, a.Pp, p < a.Pp ? N - n0 : 0, st);
-      wait_bar(&bars[kDoneS], ph, a.err, a.wait_ns);
+      if (!wait(kDoneS, ph)) goto state_done;
       tc_fence_after();
       float x[W], w[W];
       load_cols<PM, W>(tZ, x);
@@ -244,7 +253,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
 #pragma unroll
       for (int c = 0; c < W; ++c) x[c] = a.scale * w[c] * __bfloat162float(dy[c * PM]);
       store_parts<PM, W, 3>(tQ, 32, x);
-      wait_bar(&bars[kDoneU], ph, a.err, a.wait_ns);
+      if (!wait(kDoneU, ph)) goto state_done;
       tc_fence_after();
       load_cols<PM, W>(tZ, x);
       float g[W];
@@ -272,7 +281,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
         }
       }
       const float last = scal[3 * kChunk];
-      wait_bar(&bars[kDoneD], ph, a.err, a.wait_ns);
+      if (!wait(kDoneD, ph)) goto state_done;
       tc_fence_after();
       {
         float d[WN];
@@ -291,10 +300,12 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       if (++next == Lay::kStages) next = 0, ++turn;
       if (i + 1 < chunks) {
         store_parts<PM, WN, 3>(tX, NP / 2, st);
-        store_dy(next, turn);
+        if (!store_dy(next, turn)) goto state_done;
         ready(kX + up);
       }
     }
+  state_done:
+    tmem_wait_st();
     if (pin) {
       for (int64_t t = len + part; t < a.L; t += Lay::kParts) dv[t * step] = __float2bfloat16_rn(0.f);
       if (a.dh0) {

@@ -138,11 +138,16 @@ struct DeltaArgs {
   uint8_t *records;
   int64_t rec_bytes;
   uint64_t wait_ns;
+  float *keys, *heads;  // records of the fp32 chunks (csrc/delta_rows.cu), by key head and by value head
 };
 // Step by step, any size; the outputs y and h_final.
 cudaError_t launch_delta_steps(const DeltaArgs &a, cudaStream_t st);
 // The same steps, writing carry and e instead, with the adjoint's steps (dv, dh0, xcarry, du).
 cudaError_t launch_delta_steps_both(const DeltaArgs &a, cudaStream_t st);
+// By chunks of 32 in fp32 (fp32 inputs), forwards or the two passes of a backward call, records first.
+cudaError_t launch_delta_rows(const DeltaArgs &a, bool bwd, cudaStream_t st);
+int64_t delta_rows_key_bytes(int64_t N);
+int64_t delta_rows_head_bytes(bool bwd);
 // By chunks of 64 on the tensor cores (bf16 inputs): the chunks' records; the state and the
 // outputs, or (both) what a backward pass needs of the states, with the adjoints (dv, dh0,
 // xcarry, du); and the other gradients from what those wrote.

@@ -218,7 +218,7 @@ def test_delta_without_states(dt):
 
 
 @pytest.mark.parametrize("dt", TYPES)
-@pytest.mark.parametrize("L", [1, 40, 200])
+@pytest.mark.parametrize("L", [1, 40, 200, 300])
 def test_delta_lengths_leave_the_padding_out(dt, L):
     c = (5, L, 1, 2, 64, 40)
     a, h0 = delta_case(c, dt)
@@ -243,7 +243,7 @@ def test_delta_lengths_leave_the_padding_out(dt, L):
 
 
 @pytest.mark.parametrize("dt", TYPES)
-@pytest.mark.parametrize("L", [3, 90, 150])
+@pytest.mark.parametrize("L", [3, 90, 150, 300])
 def test_delta_gates_of_minus_infinity_drop_the_state(dt, L):
     a, h0 = delta_case((1, L, 1, 2, 64, 64), dt)
     a["g"][:, L // 2] = -float("inf")
@@ -283,7 +283,7 @@ def test_delta_of_nothing():
 
 
 @pytest.mark.parametrize("dt", TYPES)
-@pytest.mark.parametrize("L", [1, 150])
+@pytest.mark.parametrize("L", [1, 150, 300])
 def test_delta_in_graphs_on_streams_and_twice(dt, L):
     a, h0 = delta_case((2, L, 1, 2, 64, 64), dt)
     dy, dh = gradients_in(a)
@@ -349,6 +349,7 @@ def test_a_layer_and_its_gradients_together(dt):
 PATHS = [  # batch, seqlen, qk_heads, heads, N, P: short and long runs with few blocks and with more than the SMs
     (1, 9, 1, 1, 64, 64), (2, 12, 1, 2, 32, 16), (1, 41, 2, 2, 64, 64), (37, 13, 4, 16, 16, 8), (37, 12, 8, 16, 8, 4),
     (5, 70, 4, 16, 64, 64), (5, 66, 4, 16, 64, 72), (5, 64, 8, 16, 72, 64), (3, 130, 2, 26, 65, 66),
+    (5, 100, 4, 16, 72, 64), (9, 100, 4, 16, 64, 64), (4, 260, 4, 16, 40, 128), (4, 260, 8, 16, 24, 100), (2, 260, 1, 1, 32, 33),
 ]
 
 
@@ -372,7 +373,7 @@ def test_delta_by_the_reference_path(dt):
 
 
 @pytest.mark.parametrize("dt", TYPES)
-@pytest.mark.parametrize("L", [1, 11, 150])
+@pytest.mark.parametrize("L", [1, 11, 150, 300])
 def test_delta_at_unaligned_pointers(dt, L):
     a, h0 = delta_case((2, L, 1, 2, 64, 64), dt)
     dy, dh = gradients_in(a)
@@ -398,11 +399,12 @@ def test_delta_at_unaligned_pointers(dt, L):
 
 
 @pytest.mark.parametrize("what", ["forward", "backward"])
-@pytest.mark.parametrize("c", [(2, 600, 1, 2, 64, 64), (2, 600, 1, 2, 128, 128), (5, 300, 2, 16, 128, 64)])
-def test_delta_short_waits_report_a_timeout_and_the_next_call_is_clean(c, what):
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("c", [(2, 600, 1, 2, 64, 64), (2, 600, 1, 2, 128, 128), (5, 300, 2, 16, 128, 64), (1, 300, 1, 1, 8, 2)])
+def test_delta_short_waits_report_a_timeout_and_the_next_call_is_clean(c, dt, what):
     """The chunk kernels' waits of one role on another are bounded: with waits of a microsecond some run out, which is
     reported, ends the call and leaves the device and the next call as they were."""
-    a, h0 = delta_case(c, torch.bfloat16)
+    a, h0 = delta_case(c, dt)
     dy, dh = gradients_in(a)
     pb = pd._delta_problem(*(a[n] for n in ("q", "k", "v", "g", "beta")), h0, None, None, 0)[0]
     size = pd.pdssm_delta_workspace_size(pb) if what == "forward" else pd.pdssm_delta_bwd_workspace_size(pb)
@@ -435,7 +437,7 @@ def test_delta_error_word_of_a_path_without_waits():
 
 @pytest.mark.parametrize("dt", TYPES)
 def test_delta_values_that_are_not_finite_stay_in_their_sequences_and_heads(dt):
-    a, h0 = delta_case((3, 140, 1, 2, 64, 32), dt)
+    a, h0 = delta_case((3, 300, 1, 2, 64, 32), dt)
     dy, dh = gradients_in(a)
     want, wantb = pd.delta_forward(**a, h0=h0), pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh)
     a["v"][1, 70, 1, 3] = float("nan")
@@ -451,21 +453,21 @@ def test_delta_values_that_are_not_finite_stay_in_their_sequences_and_heads(dt):
     assert torch.equal(gotb["dv"][1, :, 0], wantb["dv"][1, :, 0])
 
 
-@pytest.mark.parametrize("dt", TYPES)
-def test_delta_offsets_beyond_32_bits(dt):
-    """More than 2^31 values: the last sequence is the same, bit for bit, as it is alone (fp32: by steps)."""
-    Bt, L, Hk, H, N, P = 65, 2049, 1, 128, 16, 128
+@pytest.mark.parametrize("dt,N,flags", [(torch.bfloat16, 16, 0), (torch.float32, 16, pd.FLAG_REFERENCE_PATH), (torch.float32, 72, 0)])
+def test_delta_offsets_beyond_32_bits(dt, N, flags):
+    """More than 2^31 values: the last sequence is the same, bit for bit, as it is alone (each case takes one path at any size)."""
+    Bt, L, Hk, H, P = 65, 2049, 1, 128, 128
     gen = torch.Generator(device="cuda").manual_seed(5)
     rand = lambda *s: torch.randn(*s, device="cuda", generator=gen, dtype=dt)  # noqa: E731
-    a = dict(q=0.25 * rand(Bt, L, Hk, N), k=0.25 * rand(Bt, L, Hk, N), v=rand(Bt, L, H, P), g=-0.05 * rand(Bt, L, H).abs(),
+    a = dict(q=N ** -0.5 * rand(Bt, L, Hk, N), k=N ** -0.5 * rand(Bt, L, Hk, N), v=rand(Bt, L, H, P), g=-0.05 * rand(Bt, L, H).abs(),
              beta=torch.sigmoid(rand(Bt, L, H)))
     assert a["v"].numel() > 2 ** 31
     dy = rand(Bt, L, H, P)
     last = {n: x[-1:].contiguous() for n, x in a.items()}
-    out, alone = pd.delta_forward(**a), pd.delta_forward(**last)
+    out, alone = pd.delta_forward(**a, flags=flags), pd.delta_forward(**last, flags=flags)
     assert torch.equal(out["y"][-1], alone["y"][0]) and torch.equal(out["h_final"][-1], alone["h_final"][0])
     del out
-    out, alone = pd.delta_backward(**a, dy=dy), pd.delta_backward(**last, dy=dy[-1:].contiguous())
+    out, alone = pd.delta_backward(**a, dy=dy, flags=flags), pd.delta_backward(**last, dy=dy[-1:].contiguous(), flags=flags)
     for n in alone:
         assert torch.equal(out[n][-1], alone[n][0]), n
     del out, a, dy
