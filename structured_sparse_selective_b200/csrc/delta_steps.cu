@@ -1,5 +1,5 @@
 // The gated delta rule step by step (formulas in delta.cuh), forwards and backwards:
-// short runs, fp32 inputs and every size, and one kernel for a single token.
+// short runs, fp32 inputs with many sequences, and one kernel for a single token.
 //
 // The columns of H are independent of one another. A column's rows are spread over LPC
 // lanes of a warp, in registers for the whole sequence, so k^T H and q^T H are a few sums
