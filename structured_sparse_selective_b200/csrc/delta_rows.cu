@@ -14,9 +14,12 @@
 // The columns p are independent of one another, so in the second kernel a warp has CW of them and
 // goes through the chunks on its own, without a barrier between warps: the left operand's rows
 // (steps; rows of the state) lie on the lanes, the right one's values are broadcast from the warp's
-// own shared memory, two terms of a sum an instruction (fma.rn.f32x2). The first warp also asks for
-// the records, a bulk copy each, up to two chunks ahead.
-// What bounds it: with few sequences the five products' latencies, one after the other (about 2,200
+// own shared memory, two terms of a sum an instruction (fma.rn.f32x2). One warp more asks for the
+// records, a bulk copy each, up to three chunks ahead; in blocks of eight, whose registers leave no room
+// for a ninth, the first warp does, which waits for the others for it (32 sequences of 18,000 steps,
+// 32 x 32: 650 us so, 545 with the warp more; two blocks instead of eight warps make a second round of
+// blocks: 2 x 2,048 steps x 32 heads of 128 x 128 took 1,035 us in blocks of six, 690 in blocks of eight).
+// What bounds it: with few sequences the five products' latencies, one after the other (about 1,850
 // cycles a chunk of 32 steps, against 5,000 for 32 steps by csrc/delta_steps.cu); with many the FMA pipe
 // and the shared-memory reads (a broadcast and a quarter of a row read for every 2 x CW FMAs).
 #include <algorithm>
@@ -293,12 +296,12 @@ __host__ __device__ constexpr int stage_keys(int NP, What what) { return (what =
 __host__ __device__ constexpr int stage_heads(What what) { return (what == kSave ? 1 : 2) * kTri + kScal; }
 __host__ __device__ constexpr int stage_values(int NP, What what) { return stage_keys(NP, what) + stage_heads(what); }
 
-// One sequence of one head, columns p0 = CW * (group * warps + warp) ...
-template <int J, int CW, What WHAT>
-__device__ __forceinline__ void run(const DeltaArgs &a, int group, int stages, bool aligned) {
+// One sequence of one head, columns p0 = CW * (group * warps + warp) ... OWN: the copies have a warp of their own.
+template <int J, int CW, What WHAT, bool OWN>
+__device__ __forceinline__ void run(const DeltaArgs &a, int group, int warps, int stages, bool aligned) {
   constexpr int NP = 32 * J, kStage = stage_values(NP, WHAT);
   extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem);  // full and free of each stage
   float *stage0 = reinterpret_cast<float *>(smem + 128);
   const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.H + h, hk = h / (a.H / a.Hk);
@@ -312,7 +315,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, int group, int stages, b
   }
   __syncthreads();
 
-  // Warp 0 copies the records of chunk i (of the order they are gone through) into their stage.
+  // A lane copies the records of chunk i (of the order they are gone through) into their stage.
   const float *keys = a.keys + (b * a.Hk + hk) * a.nC * key_values(NP);
   const float *heads = a.heads + bh * a.nC * head_values(WHAT != kForward) + (WHAT == kBack ? kTri : 0);
   const auto refill = [&](int64_t i, int s, int turn) {
@@ -326,10 +329,24 @@ __device__ __forceinline__ void run(const DeltaArgs &a, int group, int stages, b
     bulk_load(st, keys + chunk * key_values(NP), 4 * stage_keys(NP, WHAT), &bars[s]);
     bulk_load(st + stage_keys(NP, WHAT), heads + chunk * head_values(WHAT != kForward), 4 * stage_heads(WHAT), &bars[s]);
   };
-  const bool copies = threadIdx.x == 0;
+  const auto drain = [&](int s, int turn) {  // s, turn: those of the next chunk if there were one
+    for (int i = 0; i < stages; ++i)         // the last use of each stage
+      if (turn - (i >= s) >= 0) wait_own(&bars[i], (turn - (i >= s)) & 1, a.err);
+  };
   // a short limit runs out here: nothing has been asked for yet
+  const bool copies = warp == (OWN ? warps : 0) && lane == 0;
   if (copies && chunks > 0 && a.wait_ns < kShortNs) wait_slow<false>(&bars[0], 0, a.err, a.wait_ns);
-  if (copies)
+  if (OWN && warp == warps) {
+    if (!copies) return;
+    int s = 0, turn = 0;
+    for (int64_t i = 0; i < chunks; ++i) {
+      refill(i, s, turn);
+      if (++s == stages) s = 0, ++turn;
+    }
+    drain(s, turn);
+    return;
+  }
+  if (!OWN && copies)
     for (int i = 0; i < min((int64_t)(stages - 1), chunks); ++i) refill(i, i, 0);
 
   float *hs = stage0 + stages * kStage + warp * Warp<CW>::values(NP, WHAT);  // the state's values
@@ -356,8 +373,9 @@ __device__ __forceinline__ void run(const DeltaArgs &a, int group, int stages, b
   if (chunks > 0) fetch(WHAT == kBack ? chunks - 1 : 0);
   int s = 0, turn = 0;
   for (int64_t i = 0; i < chunks; ++i) {
-    // the stage of the chunk before, which the other warps are done with in a moment
-    if (copies && i + stages - 1 < chunks) refill(i + stages - 1, s ? s - 1 : stages - 1, s ? turn + 1 : turn);
+    // without a warp for the copies: into the stage of the chunk before, which the other warps are done
+    // with in a moment
+    if (!OWN && copies && i + stages - 1 < chunks) refill(i + stages - 1, s ? s - 1 : stages - 1, s ? turn + 1 : turn);
     const int64_t chunk = WHAT == kBack ? chunks - 1 - i : i, t = chunk * kC + lane;
     const float *key = stage0 + s * kStage, *head = key + stage_keys(NP, WHAT);
     const float4 *K = reinterpret_cast<const float4 *>(key) + lane, *KT = reinterpret_cast<const float4 *>(key + kC * NP) + lane,
@@ -470,9 +488,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, int group, int stages, b
     if (lane == 0) mbar_arrive(&bars[kMaxStages + s]);
     if (++s == stages) s = 0, ++turn;
   }
-  if (copies)  // nothing is in flight any more, unless a wait has run out
-    for (int i = 0; i < stages; ++i)  // the last use of each stage
-      if (turn - (i >= s) >= 0) wait_own(&bars[i], (turn - (i >= s)) & 1, a.err);
+  if (!OWN && copies) drain(s, turn);
   if (WHAT != kSave) {
     float *out = WHAT == kBack ? a.dh0 : a.h_final;
 #pragma unroll
@@ -486,27 +502,27 @@ __device__ __forceinline__ void run(const DeltaArgs &a, int group, int stages, b
   }
 }
 
-template <int J, int CW>
-__global__ void __launch_bounds__(32 * kMaxWarps, 1) delta_rows_kernel(DeltaArgs a, int stages, bool aligned) {
-  run<J, CW, kForward>(a, blockIdx.x, stages, aligned);
+template <int J, int CW, bool OWN>
+__global__ void __launch_bounds__(32 * kMaxWarps, 1) delta_rows_kernel(DeltaArgs a, int warps, int stages, bool aligned) {
+  run<J, CW, kForward, OWN>(a, blockIdx.x, warps, stages, aligned);
 }
 
 // The states and the adjoints of a backward pass do not need one another: their blocks take turns.
-template <int J, int CW>
-__global__ void __launch_bounds__(32 * kMaxWarps, 1) delta_rows_both_kernel(DeltaArgs a, int stages, bool aligned) {
-  if (blockIdx.x & 1) run<J, CW, kBack>(a, blockIdx.x >> 1, stages, aligned);
-  else run<J, CW, kSave>(a, blockIdx.x >> 1, stages, aligned);
+template <int J, int CW, bool OWN>
+__global__ void __launch_bounds__(32 * kMaxWarps, 1) delta_rows_both_kernel(DeltaArgs a, int warps, int stages, bool aligned) {
+  if (blockIdx.x & 1) run<J, CW, kBack, OWN>(a, blockIdx.x >> 1, warps, stages, aligned);
+  else run<J, CW, kSave, OWN>(a, blockIdx.x >> 1, warps, stages, aligned);
 }
 
 template <int J, int CW>
 cudaError_t launch_jc(const DeltaArgs &a, bool bwd, const char *name, cudaStream_t st) {
   constexpr int NP = 32 * J;
   const int all = (int)((a.Pp + CW - 1) / CW);  // the padded columns of the workspace rows are written too
-  // the warps of a block share its records; with few sequences the columns are spread over more
-  // blocks as long as each has an SM
-  int warps = std::min(all, kMaxWarps);
+  // the warps of a block share its records: as few as give one block an SM, or eight
   const int64_t slices = a.Bt * a.H * (bwd ? 2 : 1);
-  while (warps > 1 && slices * ((all + warps / 2 - 1) / (warps / 2)) <= 148) warps /= 2;
+  int warps = 1;
+  while (warps < kMaxWarps && slices * ((all + warps - 1) / warps) > 148) ++warps;
+  warps = std::min(warps, all);
   const auto bytes = [&](int stages) {
     const int f = 4 * (stages * stage_values(NP, kForward) + warps * Warp<CW>::values(NP, kForward));
     const int s = 4 * (stages * stage_values(NP, kSave) + warps * Warp<CW>::values(NP, kSave));
@@ -514,14 +530,16 @@ cudaError_t launch_jc(const DeltaArgs &a, bool bwd, const char *name, cudaStream
     return 128 + (bwd ? std::max(s, k) : f);
   };
   const int stages = bytes(kMaxStages) <= 227 * 1024 ? kMaxStages : 2, smem = bytes(stages);
-  auto kern = bwd ? delta_rows_both_kernel<J, CW> : delta_rows_kernel<J, CW>;
+  const bool own = warps < kMaxWarps;
+  auto kern = bwd ? (own ? delta_rows_both_kernel<J, CW, true> : delta_rows_both_kernel<J, CW, false>)
+                  : (own ? delta_rows_kernel<J, CW, true> : delta_rows_kernel<J, CW, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess || (e = trace_before(st, name)) != cudaSuccess) return e;
   uintptr_t all16 = reinterpret_cast<uintptr_t>(a.v) | reinterpret_cast<uintptr_t>(bwd ? a.dy : a.y);
   all16 |= reinterpret_cast<uintptr_t>(a.h0) | reinterpret_cast<uintptr_t>(a.h_final) | reinterpret_cast<uintptr_t>(a.dv) |
            reinterpret_cast<uintptr_t>(a.dh_final) | reinterpret_cast<uintptr_t>(a.dh0);
   const dim3 grid((unsigned)((all + warps - 1) / warps) * (bwd ? 2 : 1), (unsigned)a.H, (unsigned)a.Bt);
-  kern<<<grid, 32 * warps, smem, st>>>(a, stages, a.P % 4 == 0 && all16 % 16 == 0);
+  kern<<<grid, 32 * (warps + own), smem, st>>>(a, warps, stages, a.P % 4 == 0 && all16 % 16 == 0);
   e = cudaGetLastError();
   return e != cudaSuccess ? e : trace_after(st);
 }
@@ -536,7 +554,7 @@ cudaError_t launch_j(const DeltaArgs &a, bool bwd, cudaStream_t st) {
   if ((e = cudaGetLastError()) != cudaSuccess || (e = trace_after(st)) != cudaSuccess) return e;
   const char *name = bwd ? "delta_rows_both" : "delta_rows";
   // eight columns a warp read less for each FMA; four or two make more warps where there are few
-  // (32 sequences of 18,000 steps, 32 x 32: 703 us with four, 652 with two)
+  // (32 sequences of 18,000 steps, 32 x 32, without a warp for the copies: 703 us with four, 652 with two)
   const int64_t of4 = a.Bt * a.H * ((a.P + 3) / 4) * (bwd ? 2 : 1);
   if (of4 <= 2 * 148) return launch_jc<J, 2>(a, bwd, name, st);
   if (of4 <= 8 * 148) return launch_jc<J, 4>(a, bwd, name, st);
