@@ -567,6 +567,7 @@ int64_t delta_rows_key_bytes(int64_t N) { return 4 * (int64_t)key_values(N <= 32
 int64_t delta_rows_head_bytes(bool bwd) { return 4 * (int64_t)head_values(bwd); }
 
 cudaError_t launch_delta_rows(const DeltaArgs &a, bool bwd, cudaStream_t st) {
+  if (a.C != kC) return cudaErrorInvalidValue;
   return a.N <= 32 ? launch_j<1>(a, bwd, st) : a.N <= 64 ? launch_j<2>(a, bwd, st) : launch_j<4>(a, bwd, st);
 }
 
