@@ -315,35 +315,38 @@ __device__ __forceinline__ void run(const DeltaArgs &a, int group, int warps, in
   }
   __syncthreads();
 
-  // A lane copies the records of chunk i (of the order they are gone through) into their stage.
+  // A lane copies the records of chunk i (of the order they are gone through) into their stage. Every wait of a
+  // role on another is bounded: when one has run out, anywhere in the launch, the lane asks for nothing more and
+  // each warp leaves its chunks at its next unfinished wait, so that nothing works on records that are not there.
   const float *keys = a.keys + (b * a.Hk + hk) * a.nC * key_values(NP);
   const float *heads = a.heads + bh * a.nC * head_values(WHAT != kForward) + (WHAT == kBack ? kTri : 0);
+  int64_t asked = 0;  // chunks whose records the lane has asked for
+  bool going = true;
   const auto refill = [&](int64_t i, int s, int turn) {
     const int64_t chunk = WHAT == kBack ? chunks - 1 - i : i;
-    if (turn) {
-      wait_bar(&bars[kMaxStages + s], (turn - 1) & 1, a.err, a.wait_ns);
-      wait_own(&bars[s], (turn - 1) & 1, a.err);  // done for long, unless a wait has run out
-    }
+    // all warps are done with the stage, hence its copies have landed
+    going = going && (!turn || wait_bar(&bars[kMaxStages + s], (turn - 1) & 1, a.err, a.wait_ns));
+    if (!going) return;
     float *st = stage0 + s * kStage;
     mbar_expect_tx(&bars[s], 4 * kStage);
     bulk_load(st, keys + chunk * key_values(NP), 4 * stage_keys(NP, WHAT), &bars[s]);
     bulk_load(st + stage_keys(NP, WHAT), heads + chunk * head_values(WHAT != kForward), 4 * stage_heads(WHAT), &bars[s]);
+    ++asked;
   };
-  const auto drain = [&](int s, int turn) {  // s, turn: those of the next chunk if there were one
-    for (int i = 0; i < stages; ++i)         // the last use of each stage
-      if (turn - (i >= s) >= 0) wait_own(&bars[i], (turn - (i >= s)) & 1, a.err);
+  const auto drain = [&]() {  // the last copies into each stage have landed
+    for (int64_t i = max(asked - stages, (int64_t)0); i < asked; ++i) wait_own(&bars[i % stages], (i / stages) & 1, a.err);
   };
-  // a short limit runs out here: nothing has been asked for yet
   const bool copies = warp == (OWN ? warps : 0) && lane == 0;
-  if (copies && chunks > 0 && a.wait_ns < kShortNs) wait_slow<false>(&bars[0], 0, a.err, a.wait_ns);
+  // a short limit runs out here: nothing has been asked for yet
+  if (copies && chunks > 0 && a.wait_ns < kShortNs) going = wait_slow<false>(&bars[0], 0, a.err, a.wait_ns);
   if (OWN && warp == warps) {
     if (!copies) return;
     int s = 0, turn = 0;
-    for (int64_t i = 0; i < chunks; ++i) {
+    for (int64_t i = 0; i < chunks && going; ++i) {
       refill(i, s, turn);
       if (++s == stages) s = 0, ++turn;
     }
-    drain(s, turn);
+    drain();
     return;
   }
   if (!OWN && copies)
@@ -393,7 +396,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, int group, int warps, in
       if (WHAT == kBack && n < N) store_cols_f32<CW>(a.xcarry + ((bh * a.nC + chunk) * N + n) * a.Pp + p0, st[j], n_room, true);
     }
     __syncwarp();
-    wait_bar(&bars[s], turn & 1, a.err, a.wait_ns);
+    if (!__all_sync(0xffffffffu, wait_bar(&bars[s], turn & 1, a.err, a.wait_ns))) break;
     const float grow = scal[lane], fade = scal[kC + lane], beta = scal[2 * kC + lane], last = scal[3 * kC];
     if constexpr (WHAT != kBack) {
       float y[CW];
@@ -488,7 +491,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, int group, int warps, in
     if (lane == 0) mbar_arrive(&bars[kMaxStages + s]);
     if (++s == stages) s = 0, ++turn;
   }
-  if (!OWN && copies) drain(s, turn);
+  if (!OWN && copies) drain();
   if (WHAT != kSave) {
     float *out = WHAT == kBack ? a.dh0 : a.h_final;
 #pragma unroll
