@@ -428,8 +428,9 @@ pdssm_status pdssm_qk_norm_bwd(const pdssm_norm_problem *pb, const void *q, cons
  * gives the same bits. A value that is not finite reaches, by chunks, earlier outputs of its
  * own chunk too, but no other sequence, and one of v no other column of P.
  *   workspace pdssm_delta_workspace_size bytes, 16-byte aligned; may be NULL for 0. Larger than 0
- *            (by chunks): an error word, which pdssm_read_device_check reads (PDSSM_ERR_TIMEOUT;
- *            the outputs of that call are unspecified then), and a record for each chunk.
+ *            (by chunks): an error word, which pdssm_read_device_check reads, and a record for each
+ *            chunk. After PDSSM_ERR_TIMEOUT what the call could not finish is NaN: y (up to a
+ *            sequence's length) and h_final of each value head that has a step and saw the wait run out.
  * Calls that may run at the same time need workspaces of their own (two captured
  * graphs that may be replayed side by side too). pdssm_qk_norm, pdssm_delta_fwd and
  * their backward calls may be captured; the stream's device is current then.
@@ -460,7 +461,8 @@ pdssm_status pdssm_delta_fwd(const pdssm_delta_problem *pb, const void *q, const
  * Each gradient has the type of what it belongs to and is rounded once. Rows behind a
  * sequence's length get zeros. No atomics: the same call gives the same bits.
  *   workspace pdssm_delta_bwd_workspace_size bytes, 16-byte aligned: an error word as above (on
- *            every path), and for each value head the states and adjoints at the chunks' ends
+ *            every path; after PDSSM_ERR_TIMEOUT dq, dk, dg and dbeta are NaN, and dv and dh0 where they
+ *            could not be finished), and for each value head the states and adjoints at the chunks' ends
  *            (2 * N * P floats every 64 steps for bf16 inputs by chunks, else every 32), two rows
  *            of P floats a step and, by chunks, the chunks' records (74 KiB every 64 steps; in
  *            fp32 12.5 KiB every 32 and for each key head 12 to 48 KiB).

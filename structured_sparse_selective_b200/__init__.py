@@ -714,7 +714,8 @@ def delta_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     rest is padding. scale: N ** -0.5 by default. Results: "y" like v and, unless ``want_h_final`` is false,
     "h_final", written to ``h_final`` where given, which may be ``h0`` itself. ``workspace``: at least
     ``pdssm_delta_workspace_size`` bytes, one for each call that may run at the same time (allocated when None;
-    a size of 0 needs none); ``pdssm_read_device_check`` reads its error word."""
+    a size of 0 needs none); ``pdssm_read_device_check`` reads its error word. What a call whose bounded waits
+    ran out could not finish is NaN."""
     pb, key = _delta_problem(q, k, v, g, beta, h0, scale, lengths, flags)
     y = torch.empty_like(v)
     new = [y]

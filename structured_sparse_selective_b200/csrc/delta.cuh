@@ -34,6 +34,16 @@ __device__ __forceinline__ void store_any(void *p, int64_t i, bool bf16, float v
   else static_cast<float *>(p)[i] = v;
 }
 
+// Whether a wait of the call has run out so far, anywhere in it.
+__device__ __forceinline__ bool timed_out(const uint32_t *err) { return *static_cast<const volatile uint32_t *>(err) & kErrTimeout; }
+
+// NaN over `rows` rows of `cols` values, `ld` apart, from value `at` of p on (nothing where p is null), by `threads`
+// threads: what a call whose waits ran out gives back instead of values that are not finished.
+static __device__ __noinline__ void fill_nan(void *p, bool bf16, int64_t at, int64_t rows, int64_t ld, int cols, int tid, int threads) {
+  if (!p || cols <= 0) return;
+  for (int64_t i = tid; i < rows * cols; i += threads) store_any(p, at + i / cols * ld + i % cols, bf16, __int_as_float(0x7fffffff));
+}
+
 // Two fp32 values in one register pair; one instruction works on both.
 using pair2 = unsigned long long;
 __device__ __forceinline__ pair2 pack2(float a, float b) {

@@ -113,11 +113,11 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, uint32_
 // On the caller's own copies or products in flight. The tries in place rarely leave the call to be
 // made (the gradients' launch of 256 sequences of 2,048 steps, 64 x 64: 371 -> 330 us; in the chains
 // of the roles' waits the loop is slower, 150 -> 177 us).
-__device__ __forceinline__ void wait_own(uint64_t *bar, uint32_t parity, uint32_t *err) {
+__device__ __forceinline__ bool wait_own(uint64_t *bar, uint32_t parity, uint32_t *err) {
 #pragma unroll 1
   for (int i = 0; i < 32; ++i)
-    if (sm100::mbar_try_wait(bar, parity)) return;
-  wait_slow<true>(bar, parity, err, kOwnNs);
+    if (sm100::mbar_try_wait(bar, parity)) return true;
+  return wait_slow<true>(bar, parity, err, kOwnNs);
 }
 
 // True in all THREADS of some whole warps (by a barrier of their own) if ok is true in all.

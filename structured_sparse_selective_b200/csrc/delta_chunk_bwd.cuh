@@ -316,8 +316,12 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
     }
   }
   tc_fence_before();
-  __syncthreads();
+  const bool bad = __syncthreads_or(timed_out(a.err));
   if (warp == kIssuer) tmem_dealloc(tbase, Lay::kCols);
+  if (bad && len > 0) {
+    fill_nan(a.dv, true, (b * a.L * a.H + h) * a.P + p0, len, a.H * a.P, (int)min((int64_t)PM, a.P - p0), threadIdx.x, blockDim.x);
+    fill_nan(a.dh0, false, bh * a.N * a.P + p0, a.N, a.P, (int)min((int64_t)PM, a.P - p0), threadIdx.x, blockDim.x);
+  }
 }
 
 }  // namespace chunk_bwd

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
   float *scal = reinterpret_cast<float *>(smem + Lay::kScal), *sdG = reinterpret_cast<float *>(smem + Lay::kRed), *sdb = sdG + kChunk,
         *sxh = sdb + kChunk;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::kBar);
-  uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 2);
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 2), *bad = tslot + 1;  // bad: a wait of the call has run out
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int64_t chunk = blockIdx.x, hk = blockIdx.y, b = blockIdx.z, t0 = chunk * kChunk;
   const int64_t len = live_steps(a.lengths, b, a.L), row0 = b * a.L + t0;
@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
     mbar_init(&bars[0], 1);
     mbar_init(&bars[1], 1);
     mbar_fence_init();
+    *bad = timed_out(a.err);
   }
   if (warp == 0) {
     tmem_alloc(tslot, Lay::kCols);
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
 #pragma unroll
       for (int k = 0; k < kPer; ++k) xh = sum4(sx[k][0], sh[k][0], sum4(sx[k][1], sh[k][1], xh));
     }
-    wait_own(&bars[0], ph, a.err);
+    if (!wait_own(&bars[0], ph, a.err)) *bad = 1;
     tc_fence_after();
     put_state(sx);
     {
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
         }
       }
     }
-    wait_own(&bars[1], ph, a.err);
+    if (!wait_own(&bars[1], ph, a.err)) *bad = 1;
     tc_fence_after();
     {
       const float fade = scal[kChunk + row];
@@ -378,6 +379,12 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tbase, Lay::kCols);
+  if (*bad) {
+    fill_nan(a.dq, true, (row0 * a.Hk + hk) * N, live, a.Hk * N, N, tid, kThreads);
+    fill_nan(a.dk, true, (row0 * a.Hk + hk) * N, live, a.Hk * N, N, tid, kThreads);
+    fill_nan(a.dg, gb, row0 * a.H + hk * r_heads, live, a.H, r_heads, tid, kThreads);
+    fill_nan(a.dbeta, gb, row0 * a.H + hk * r_heads, live, a.H, r_heads, tid, kThreads);
+  }
 }
 
 template <int NP, int PP>

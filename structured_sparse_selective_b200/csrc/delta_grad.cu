@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaArgs a, int l
     }
     return;
   }
+  if (tid == 0) swarp[9] = timed_out(a.err) ? 1.f : 0.f;
   for (int i = tid; i < kC * 32 * J; i += kThreads) {
     const int t = i / (32 * J), n = i % (32 * J);
     const bool on = t < live && n < N;
@@ -317,6 +318,13 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaArgs a, int l
       store_any(a.dq, at, bf, t < live ? a.scale * dq[r][j] : 0.f);
       store_any(a.dk, at, bf, t < live ? dk[r][j] : 0.f);
     }
+  }
+  __syncthreads();
+  if (swarp[9] != 0.f) {
+    fill_nan(a.dq, bf, (row0 * a.Hk + hk) * N, live, a.Hk * N, N, tid, kThreads);
+    fill_nan(a.dk, bf, (row0 * a.Hk + hk) * N, live, a.Hk * N, N, tid, kThreads);
+    fill_nan(a.dg, gb, row0 * a.H + hk * r_heads, live, a.H, r_heads, tid, kThreads);
+    fill_nan(a.dbeta, gb, row0 * a.H + hk * r_heads, live, a.H, r_heads, tid, kThreads);
   }
 }
 

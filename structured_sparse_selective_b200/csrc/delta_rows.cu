@@ -494,10 +494,16 @@ __device__ __forceinline__ void run(const DeltaArgs &a, int group, int warps, in
   if (!OWN && copies) drain();
   if (WHAT != kSave) {
     float *out = WHAT == kBack ? a.dh0 : a.h_final;
+    const bool bad = len > 0 && __any_sync(0xffffffffu, timed_out(a.err));
+    if (bad) {
+      __syncwarp();
+      fill_nan(WHAT == kBack ? a.dv : a.y, false, (b * a.L * a.H + h) * a.P + p0, len, step, n_in, lane, 32);
+      fill_nan(out, false, bh * N * a.P + p0, N, a.P, n_in, lane, 32);
+    }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int n = 32 * j + lane;
-      if (out && n < N) store_cols_f32<CW>(out + (bh * N + n) * a.P + p0, st[j], n_in, aligned);
+      if (out && n < N && !bad) store_cols_f32<CW>(out + (bh * N + n) * a.P + p0, st[j], n_in, aligned);
     }
     const float zero[CW] = {};
     float *rows = static_cast<float *>(WHAT == kBack ? a.dv : a.y) + (b * a.L * a.H + h) * a.P + p0;

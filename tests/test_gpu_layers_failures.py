@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import structured_sparse_selective_b200 as pd
-from tests.test_gpu_layers import delta_case, gradients_in
+from tests.test_gpu_layers import TYPES, delta_case, gradients_in
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,37 @@ def test_no_warp_computes_in_fp32_after_a_wait_has_run_out(c):
     y, dv = forward(ins, pb, h0)["y"], backward(ins, pb, h0, dy, dh)["dv"]
     for x in (y, dv):
         assert ((x == SEVEN) | x.isnan()).all()
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("c", CASES)
+def test_a_timeout_leaves_nan_where_values_are_not_finished(c, dt):
+    a, h0, dy, dh, ins, pb = setup(c, dt)
+    out = forward(ins, pb, h0) | backward(ins, pb, h0, dy, dh)
+    for n, x in out.items():
+        assert x.isnan().all(), n
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_a_timeout_leaves_padding_and_sequences_without_steps_as_they_are(dt):
+    L = 600
+    a, h0, dy, dh, ins, pb = setup((4, L, 1, 2, 64, 64), dt)
+    lengths = torch.tensor([L, 0, 450, 1], dtype=torch.int32, device="cuda")
+    out, back = forward(ins, pb, h0, lengths), backward(ins, pb, h0, dy, dh, lengths)
+    assert torch.equal(out["h_final"][1], h0[1]) and torch.equal(back["dh0"][1], dh[1])
+    for b, n in enumerate(lengths.tolist()):
+        for name, x in {"y": out["y"], **back}.items():
+            if name != "dh0":
+                assert x[b, :n].isnan().all() and not x[b, n:].any(), (name, b)
+        if n:
+            assert out["h_final"][b].isnan().all() and back["dh0"][b].isnan().all()
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_a_timeout_shows_in_the_default_call(dt):
+    """The wrapper keeps the workspace it allocates to itself: the outputs say that the call was not finished."""
+    a, h0, dy, dh, _, _ = setup((1, 400, 1, 2, 72, 64), dt)
+    out = pd.delta_forward(**a, h0=h0, flags=pd.FLAG_SHORT_WAITS)
+    out |= pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh, flags=pd.FLAG_SHORT_WAITS)
+    for n, x in out.items():
+        assert x.isnan().all(), n
