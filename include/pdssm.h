@@ -431,6 +431,7 @@ pdssm_status pdssm_qk_norm_bwd(const pdssm_norm_problem *pb, const void *q, cons
  *            (by chunks): an error word, which pdssm_read_device_check reads, and a record for each
  *            chunk. After PDSSM_ERR_TIMEOUT what the call could not finish is NaN: y (up to a
  *            sequence's length) and h_final of each value head that has a step and saw the wait run out.
+ *            A workspace of 4 bytes or more that is passed where 0 are needed gets the error word too.
  * Calls that may run at the same time need workspaces of their own (two captured
  * graphs that may be replayed side by side too). pdssm_qk_norm, pdssm_delta_fwd and
  * their backward calls may be captured; the stream's device is current then.

@@ -164,16 +164,20 @@ DeltaArgs delta_args(const pdssm_delta_problem *pb, const DeltaPlan &p) {
   return a;
 }
 
-// Error word, records and wait limit of the kernels with roles.
+// The error word, cleared, of a call that launches nothing.
+pdssm_status clear_error(uint32_t *err, cudaStream_t cs) {
+  return !err || cudaMemsetAsync(err, 0, 4, cs) == cudaSuccess ? PDSSM_OK : PDSSM_ERR_CUDA;
+}
+
+// Records and wait limit of the kernels with roles, and their error word cleared.
 pdssm_status use_records(const pdssm_delta_problem *pb, const DeltaPlan &p, bool bwd, void *workspace, DeltaArgs &a, cudaStream_t cs) {
   char *base = static_cast<char *>(workspace);
-  a.err = static_cast<uint32_t *>(workspace);
   a.records = reinterpret_cast<uint8_t *>(base + p.o_rec);
   a.rec_bytes = delta_record_bytes(bwd);
   a.keys = reinterpret_cast<float *>(base + p.o_rec);
   a.heads = reinterpret_cast<float *>(base + p.o_heads);
   a.wait_ns = wait_limit(pb);
-  return cudaMemsetAsync(a.err, 0, 4, cs) == cudaSuccess ? PDSSM_OK : PDSSM_ERR_CUDA;
+  return clear_error(a.err, cs);
 }
 
 }  // namespace
@@ -267,8 +271,11 @@ pdssm_status pdssm_delta_fwd(const pdssm_delta_problem *pb, const void *q, const
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   OnDevice on(cs);
   if (on.status() != PDSSM_OK) return on.status();
-  if (p.slices == 0) return PDSSM_OK;
+  // a workspace larger than needed has the word too
+  uint32_t *err = workspace_bytes >= 4 ? static_cast<uint32_t *>(workspace) : nullptr;
+  if (p.slices == 0) return clear_error(err, cs);
   DeltaArgs a = delta_args(pb, p);
+  a.err = err;
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lengths = lengths; a.h0 = h0; a.y = y; a.h_final = h_final;
   if (!p.chunked && !p.by_rows) return cuda_status(launch_delta_steps(a, cs));
   if ((st = use_records(pb, p, false, workspace, a, cs)) != PDSSM_OK) return st;
@@ -306,8 +313,9 @@ pdssm_status pdssm_delta_bwd(const pdssm_delta_problem *pb, const void *q, const
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   OnDevice on(cs);
   if (on.status() != PDSSM_OK) return on.status();
-  if (p.slices == 0) return PDSSM_OK;
+  if (p.slices == 0) return clear_error(static_cast<uint32_t *>(workspace), cs);
   DeltaArgs a = delta_args(pb, p);
+  a.err = static_cast<uint32_t *>(workspace);
   char *base = static_cast<char *>(workspace);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lengths = lengths; a.h0 = h0; a.dy = dy; a.dh_final = dh_final;
   a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dh0 = dh0;
@@ -315,11 +323,7 @@ pdssm_status pdssm_delta_bwd(const pdssm_delta_problem *pb, const void *q, const
   a.xcarry = reinterpret_cast<float *>(base + p.o_xcarry);
   a.e = reinterpret_cast<float *>(base + p.o_e);
   a.du = reinterpret_cast<float *>(base + p.o_du);
-  if (p.chunked || p.by_rows) {
-    if ((st = use_records(pb, p, true, workspace, a, cs)) != PDSSM_OK) return st;
-  } else {
-    a.err = static_cast<uint32_t *>(workspace);
-  }
+  if ((p.chunked || p.by_rows) && (st = use_records(pb, p, true, workspace, a, cs)) != PDSSM_OK) return st;
   if (p.chunked) {
     a.dyy = reinterpret_cast<float *>(base + p.o_dyy);
     if ((st = cuda_status(launch_delta_prep(a, true, cs))) != PDSSM_OK) return st;

@@ -373,9 +373,15 @@ __device__ __forceinline__ void backward(const DeltaArgs &a, int group) {
   if (a.dh0) store_column<J>(x, a.dh0 + bh * a.N * a.P + col, l, N, a.P);
 }
 
+// Nothing here waits for another role: the error word of a workspace, if there is one, says so.
+__device__ __forceinline__ void clear_error(const DeltaArgs &a) {
+  if (a.err && threadIdx.x + blockIdx.x + blockIdx.y + blockIdx.z == 0) *a.err = 0;
+}
+
 // grid: (column groups, heads, batch)
 template <int J, typename T, typename G>
 __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_kernel(DeltaArgs a) {
+  clear_error(a);
   forward<J, T, G, false>(a, blockIdx.x);
 }
 
@@ -383,7 +389,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_kerne
 // turns, so that few sequences fill more SMs. grid: (2 x column groups, heads, batch)
 template <int J, typename T, typename G>
 __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_both_kernel(DeltaArgs a) {
-  if (threadIdx.x + blockIdx.x + blockIdx.y + blockIdx.z == 0) *a.err = 0;  // nothing here waits for another role
+  clear_error(a);
   if (blockIdx.x & 1) backward<J, T, G>(a, blockIdx.x >> 1);
   else forward<J, T, G, true>(a, blockIdx.x >> 1);
 }
@@ -396,6 +402,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_both_
 // their own; k^T H and q^T H are finished by three shuffles.
 template <int J, typename T, typename G>
 __global__ void __launch_bounds__(128) delta_token_kernel(DeltaArgs a) {
+  clear_error(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane >> 2;
   const int col = (blockIdx.x * (blockDim.x >> 5) + warp) * 16 + 4 * (lane & 3);
   const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.H + h, hk = h / (a.H / a.Hk);

@@ -82,3 +82,35 @@ def test_a_timeout_shows_in_the_default_call(dt):
     out |= pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh, flags=pd.FLAG_SHORT_WAITS)
     for n, x in out.items():
         assert x.isnan().all(), n
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_the_error_word_is_that_of_the_last_call(dt):
+    """One workspace for a prompt and the tokens behind it: what the prompt left in the word is not the token's."""
+    a, h0, dy, dh, ins, pb = setup((2, 600, 1, 2, 64, 64), dt)
+    ws = torch.full((pd.pdssm_delta_bwd_workspace_size(pb),), 255, dtype=torch.uint8, device="cuda")
+    for L in (1, 5, 0):  # a token, steps, nothing
+        pd.delta_forward(**a, h0=h0, flags=pd.FLAG_SHORT_WAITS, workspace=ws)
+        assert pd.pdssm_read_device_check(ws) == TIMEOUT
+        short = {n: x[:, :L].contiguous() for n, x in a.items()}
+        pd.delta_forward(**short, h0=h0, workspace=ws)
+        assert pd.pdssm_read_device_check(ws) == OK, L
+    # no sequences at all, in either direction, on a buffer that nobody has cleared
+    for L in (1, 600):
+        none = {n: x[:0, :L].contiguous() for n, x in a.items()}
+        ws.fill_(255)
+        pd.delta_forward(**none, workspace=ws)
+        assert pd.pdssm_read_device_check(ws) == OK
+        ws.fill_(255)
+        pd.delta_backward(**none, dy=none["v"], workspace=ws)
+        assert pd.pdssm_read_device_check(ws) == OK
+
+
+def test_a_workspace_where_none_is_needed_may_be_smaller_than_the_error_word():
+    a, h0, *_ = setup((2, 1, 1, 2, 64, 64), torch.float32)
+    room = torch.full((32,), 255, dtype=torch.uint8, device="cuda")
+    want = pd.delta_forward(**a, h0=h0)
+    got = pd.delta_forward(**a, h0=h0, workspace=room[:3])
+    assert torch.equal(got["y"], want["y"]) and (room == 255).all()
+    pd.delta_forward(**a, h0=h0, workspace=room)
+    assert not room[:4].any() and (room[4:] == 255).all()
