@@ -203,11 +203,23 @@ def _ptr(t: Optional[torch.Tensor], device: Optional[torch.device] = None):
     return ctypes.c_void_p(t.data_ptr()) if t.numel() > 0 else ctypes.c_void_p(t.data_ptr() or 0)
 
 
-def _stream(stream, device) -> ctypes.c_void_p:
+def _handle(stream, index: int) -> int:
+    """The stream's handle; None: the current stream of CUDA device ``index``."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    return ctypes.c_void_p(handle)
+        return torch._C._cuda_getCurrentRawStream(index)
+    if getattr(stream, "device_index", index) != index:
+        raise ValueError(f"stream of cuda:{stream.device_index}, tensors on cuda:{index}")
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _launch(fn, index: int, stream, *args) -> int:
+    """fn(*args, stream handle) with CUDA device ``index`` current: the handle of a default stream is 0 on every
+    device, and the library takes it for the current device's."""
+    handle = _handle(stream, index)
+    if index == torch._C._cuda_getDevice():
+        return fn(*args, handle)
+    with torch.cuda.device(index):
+        return fn(*args, handle)
 
 
 def make_problem(logits: torch.Tensor, d: torch.Tensor, B: torch.Tensor, x: torch.Tensor,
@@ -233,7 +245,7 @@ def pdssm_workspace_size(pb: Problem) -> int:
 
 def pdssm_select(pb: Problem, logits: torch.Tensor, s: torch.Tensor, stream=None) -> None:
     dev = logits.device
-    _check(_lib.pdssm_select(ctypes.byref(pb), _ptr(logits, dev), _ptr(s, dev), _stream(stream, dev)),
+    _check(_launch(_lib.pdssm_select, dev.index, stream, ctypes.byref(pb), _ptr(logits, dev), _ptr(s, dev)),
            "pdssm_select")
 
 
@@ -241,31 +253,33 @@ def pdssm_scan_fwd(pb: Problem, s, idx, d, B, C, x, h0, y, h_final, prod_idx, pr
                    stream=None) -> None:
     dev = idx.device
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(_lib.pdssm_scan_fwd(
+    _check(_launch(
+        _lib.pdssm_scan_fwd, dev.index, stream,
         ctypes.byref(pb), _ptr(s, dev), _ptr(idx, dev), _ptr(d, dev), _ptr(B, dev), _ptr(C, dev),
         _ptr(x, dev), _ptr(h0, dev), _ptr(y, dev), _ptr(h_final, dev), _ptr(prod_idx, dev),
-        _ptr(prod_val, dev), _ptr(workspace, dev), ws_bytes, _stream(stream, dev)), "pdssm_scan_fwd")
+        _ptr(prod_val, dev), _ptr(workspace, dev), ws_bytes), "pdssm_scan_fwd")
 
 
 def pdssm_forward(pb: Problem, logits, idx, d, B, C, x, h0, y, h_final, prod_idx, prod_val, s_out,
                   workspace, stream=None) -> None:
     dev = idx.device
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(_lib.pdssm_forward(
+    _check(_launch(
+        _lib.pdssm_forward, dev.index, stream,
         ctypes.byref(pb), _ptr(logits, dev), _ptr(idx, dev), _ptr(d, dev), _ptr(B, dev), _ptr(C, dev),
         _ptr(x, dev), _ptr(h0, dev), _ptr(y, dev), _ptr(h_final, dev), _ptr(prod_idx, dev),
-        _ptr(prod_val, dev), _ptr(s_out, dev), _ptr(workspace, dev), ws_bytes, _stream(stream, dev)),
-        "pdssm_forward")
+        _ptr(prod_val, dev), _ptr(s_out, dev), _ptr(workspace, dev), ws_bytes), "pdssm_forward")
 
 
 def pdssm_forward_noalloc(pb: Problem, logits, idx, d, B, C, x, h0, y, h_final, prod_idx, prod_val,
                           s_out, stream=None) -> None:
     """pdssm_forward with the library's built-in 32 MiB device workspace (no caller workspace)."""
     dev = idx.device
-    _check(_lib.pdssm_forward_noalloc(
+    _check(_launch(
+        _lib.pdssm_forward_noalloc, dev.index, stream,
         ctypes.byref(pb), _ptr(logits, dev), _ptr(idx, dev), _ptr(d, dev), _ptr(B, dev), _ptr(C, dev),
         _ptr(x, dev), _ptr(h0, dev), _ptr(y, dev), _ptr(h_final, dev), _ptr(prod_idx, dev),
-        _ptr(prod_val, dev), _ptr(s_out, dev), _stream(stream, dev)), "pdssm_forward_noalloc")
+        _ptr(prod_val, dev), _ptr(s_out, dev)), "pdssm_forward_noalloc")
 
 
 def pdssm_bwd_workspace_size(pb: Problem) -> int:
@@ -278,25 +292,27 @@ def pdssm_scan_bwd(pb: Problem, logits, s, idx, d, B, C, x, h0, dy, dh_final, ta
                    dx, dh0, workspace, stream=None) -> None:
     dev = idx.device
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(_lib.pdssm_scan_bwd(
+    _check(_launch(
+        _lib.pdssm_scan_bwd, dev.index, stream,
         ctypes.byref(pb), _ptr(logits, dev), _ptr(s, dev), _ptr(idx, dev), _ptr(d, dev), _ptr(B, dev),
         _ptr(C, dev), _ptr(x, dev), _ptr(h0, dev), _ptr(dy, dev), _ptr(dh_final, dev), float(tau),
         _ptr(dlogits, dev), _ptr(dd, dev), _ptr(dB, dev), _ptr(dC, dev), _ptr(dx, dev), _ptr(dh0, dev),
-        _ptr(workspace, dev), ws_bytes, _stream(stream, dev)), "pdssm_scan_bwd")
+        _ptr(workspace, dev), ws_bytes), "pdssm_scan_bwd")
 
 
 def pdssm_dict_hardmax(K: int, N: int, M: torch.Tensor, idx: torch.Tensor, stream=None) -> None:
     dev = M.device
-    _check(_lib.pdssm_dict_hardmax(int(K), int(N), _ptr(M, dev), _ptr(idx, dev), _stream(stream, dev)),
+    _check(_launch(_lib.pdssm_dict_hardmax, dev.index, stream, int(K), int(N), _ptr(M, dev), _ptr(idx, dev)),
            "pdssm_dict_hardmax")
 
 
 def pdssm_select_proj(pb: Problem, D: int, u, W, s, logits, workspace, stream=None) -> None:
     dev = u.device
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(_lib.pdssm_select_proj(ctypes.byref(pb), int(D), _ptr(u, dev), _ptr(W, dev), _ptr(s, dev),
-                                  _ptr(logits, dev), _ptr(workspace, dev), ws_bytes, _stream(stream, dev)),
-           "pdssm_select_proj")
+    _check(_launch(
+        _lib.pdssm_select_proj, dev.index, stream,
+        ctypes.byref(pb), int(D), _ptr(u, dev), _ptr(W, dev), _ptr(s, dev),
+        _ptr(logits, dev), _ptr(workspace, dev), ws_bytes), "pdssm_select_proj")
 
 
 def dict_hardmax(M: torch.Tensor, stream=None) -> torch.Tensor:
@@ -333,18 +349,21 @@ def pdssm_soft_select_workspace_size(pb: Problem) -> int:
 def pdssm_soft_select(pb: Problem, logits, M, tau: float, idx_steps, workspace, stream=None) -> None:
     dev = logits.device
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(_lib.pdssm_soft_select(ctypes.byref(pb), _ptr(logits, dev), _ptr(M, dev), float(tau), _ptr(idx_steps, dev),
-                                  _ptr(workspace, dev), ws_bytes, _stream(stream, dev)), "pdssm_soft_select")
+    _check(_launch(
+        _lib.pdssm_soft_select, dev.index, stream,
+        ctypes.byref(pb), _ptr(logits, dev), _ptr(M, dev), float(tau), _ptr(idx_steps, dev),
+        _ptr(workspace, dev), ws_bytes), "pdssm_soft_select")
 
 
 def pdssm_scan_fwd_steps(pb: Problem, idx_steps, d, B, C, x, h0, y, h_final, prod_idx, prod_val, workspace,
                          stream=None) -> None:
     dev = d.device
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(_lib.pdssm_scan_fwd_steps(
+    _check(_launch(
+        _lib.pdssm_scan_fwd_steps, dev.index, stream,
         ctypes.byref(pb), _ptr(idx_steps, dev), _ptr(d, dev), _ptr(B, dev), _ptr(C, dev), _ptr(x, dev),
         _ptr(h0, dev), _ptr(y, dev), _ptr(h_final, dev), _ptr(prod_idx, dev), _ptr(prod_val, dev),
-        _ptr(workspace, dev), ws_bytes, _stream(stream, dev)), "pdssm_scan_fwd_steps")
+        _ptr(workspace, dev), ws_bytes), "pdssm_scan_fwd_steps")
 
 
 def soft_select(logits: torch.Tensor, M: torch.Tensor, tau: float = 1.0, N: Optional[int] = None,
@@ -386,7 +405,7 @@ def forward_steps(idx_steps: torch.Tensor, d: torch.Tensor, B: torch.Tensor, C: 
 
 def pdssm_read_device_check(workspace: torch.Tensor, stream=None) -> int:
     """Status left in the workspace's error word by the last scan (synchronises)."""
-    return int(_lib.pdssm_read_device_check(_ptr(workspace), _stream(stream, workspace.device)))
+    return int(_launch(_lib.pdssm_read_device_check, workspace.device.index, stream, _ptr(workspace)))
 
 
 class KernelTrace:
@@ -514,12 +533,6 @@ def _addr(tensors, index: int):
     return out
 
 
-def _handle(stream, index: int) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
 def _used_on(stream, index: int, tensors) -> None:
     """Tensors allocated here for a call on ``stream``: the allocator must not reuse them before it is done."""
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_handle(stream, index), index)
@@ -549,7 +562,7 @@ def _nbytes(workspace: Optional[torch.Tensor]) -> int:
 
 def pdssm_qk_norm(pb: NormProblem, q, k, wq, wk, inv_freq, positions, q_out, k_out, stream=None) -> None:
     i = _index(q)
-    st = _lib.pdssm_qk_norm(pb, *_addr((q, k, wq, wk, inv_freq, positions, q_out, k_out), i), _handle(stream, i))
+    st = _launch(_lib.pdssm_qk_norm, i, stream, pb, *_addr((q, k, wq, wk, inv_freq, positions, q_out, k_out), i))
     if st:
         raise PdssmError(st, "pdssm_qk_norm")
 
@@ -561,8 +574,8 @@ def pdssm_qk_norm_bwd_workspace_size(pb: NormProblem) -> int:
 def pdssm_qk_norm_bwd(pb: NormProblem, q, k, wq, wk, inv_freq, positions, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
                       stream=None) -> None:
     i = _index(q)
-    st = _lib.pdssm_qk_norm_bwd(pb, *_addr((q, k, wq, wk, inv_freq, positions, dq_out, dk_out, dq, dk, dwq, dwk, workspace), i),
-                                _nbytes(workspace), _handle(stream, i))
+    st = _launch(_lib.pdssm_qk_norm_bwd, i, stream, pb,
+                 *_addr((q, k, wq, wk, inv_freq, positions, dq_out, dk_out, dq, dk, dwq, dwk, workspace), i), _nbytes(workspace))
     if st:
         raise PdssmError(st, "pdssm_qk_norm_bwd")
 
@@ -573,8 +586,8 @@ def pdssm_delta_workspace_size(pb: DeltaProblem) -> int:
 
 def pdssm_delta_fwd(pb: DeltaProblem, q, k, v, g, beta, lengths, h0, y, h_final, workspace, stream=None) -> None:
     i = _index(q)
-    st = _lib.pdssm_delta_fwd(pb, *_addr((q, k, v, g, beta, lengths, h0, y, h_final, workspace), i), _nbytes(workspace),
-                              _handle(stream, i))
+    st = _launch(_lib.pdssm_delta_fwd, i, stream, pb, *_addr((q, k, v, g, beta, lengths, h0, y, h_final, workspace), i),
+                 _nbytes(workspace))
     if st:
         raise PdssmError(st, "pdssm_delta_fwd")
 
@@ -586,8 +599,8 @@ def pdssm_delta_bwd_workspace_size(pb: DeltaProblem) -> int:
 def pdssm_delta_bwd(pb: DeltaProblem, q, k, v, g, beta, lengths, h0, dy, dh_final, dq, dk, dv, dg, dbeta, dh0, workspace,
                     stream=None) -> None:
     i = _index(q)
-    st = _lib.pdssm_delta_bwd(pb, *_addr((q, k, v, g, beta, lengths, h0, dy, dh_final, dq, dk, dv, dg, dbeta, dh0, workspace), i),
-                              _nbytes(workspace), _handle(stream, i))
+    st = _launch(_lib.pdssm_delta_bwd, i, stream, pb,
+                 *_addr((q, k, v, g, beta, lengths, h0, dy, dh_final, dq, dk, dv, dg, dbeta, dh0, workspace), i), _nbytes(workspace))
     if st:
         raise PdssmError(st, "pdssm_delta_bwd")
 
