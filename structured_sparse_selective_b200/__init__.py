@@ -222,6 +222,24 @@ def _launch(fn, index: int, stream, *args) -> int:
         return fn(*args, handle)
 
 
+def _results_on(stream, t: torch.Tensor, call):
+    """call() with ``stream`` current. What it allocates is then the stream's: memory that work still queued on the
+    caller's own stream uses is not among it. The results are used on the caller's stream, and are not given out again
+    before that is done with them."""
+    index = _index(t)
+    handle = _handle(stream, index)
+    here = torch.cuda.current_stream(index)
+    if handle == here.cuda_stream:
+        return call()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, index) if handle else torch.cuda.default_stream(index)
+    with torch.cuda.stream(stream):
+        out = call()
+    for r in out.values() if isinstance(out, dict) else (out,):
+        r.record_stream(here)
+    return out
+
+
 def make_problem(logits: torch.Tensor, d: torch.Tensor, B: torch.Tensor, x: torch.Tensor,
                  out_dtype: Optional[torch.dtype] = None, chunk: int = 0, flags: int = 0,
                  K: Optional[int] = None) -> Problem:
@@ -317,16 +335,20 @@ def pdssm_select_proj(pb: Problem, D: int, u, W, s, logits, workspace, stream=No
 
 def dict_hardmax(M: torch.Tensor, stream=None) -> torch.Tensor:
     """Column-wise hardmax of dense matrices M [..., N, N] (float32): idx [..., N] int32."""
+    if stream is not None:
+        return _results_on(stream, M, lambda: dict_hardmax(M))
     N = M.shape[-1]
     K = M.numel() // (N * N)
     idx = torch.empty(M.shape[:-2] + (N,), dtype=torch.int32, device=M.device)
-    pdssm_dict_hardmax(K, N, M.contiguous(), idx, stream)
+    pdssm_dict_hardmax(K, N, M.contiguous(), idx)
     return idx
 
 
 def select_proj(u: torch.Tensor, W: torch.Tensor, heads: int, K: int, want_logits: bool = False,
                 stream=None) -> Dict[str, torch.Tensor]:
     """u [Bt, L, D] bf16, W [D, heads * K] bf16 -> s [Bt, L, heads] int32 (and logits [Bt, L, heads, K])."""
+    if stream is not None:
+        return _results_on(stream, u, lambda: select_proj(u, W, heads, K, want_logits))
     Bt, L, D = u.shape
     pb = Problem(batch=Bt, seqlen=L, heads=heads, N=1, P=1, K=K, chunk=0, logits_t=BF16, in_t=BF16, d_t=BF16,
                  state_t=F32, out_t=BF16, flags=0)
@@ -334,7 +356,7 @@ def select_proj(u: torch.Tensor, W: torch.Tensor, heads: int, K: int, want_logit
     if want_logits:
         out["logits"] = torch.empty(Bt, L, heads, K, dtype=torch.float32, device=u.device)
     ws = torch.zeros(256, dtype=torch.uint8, device=u.device)
-    pdssm_select_proj(pb, D, u.contiguous(), W.contiguous(), out["s"], out.get("logits"), ws, stream)
+    pdssm_select_proj(pb, D, u.contiguous(), W.contiguous(), out["s"], out.get("logits"), ws)
     out["workspace"] = ws
     return out
 
@@ -370,6 +392,8 @@ def soft_select(logits: torch.Tensor, M: torch.Tensor, tau: float = 1.0, N: Opti
                 stream=None) -> Dict[str, torch.Tensor]:
     """The original PD-SSM's per-step transitions: idx_steps [Bt, L, H, N] uint8 from logits
     [Bt, L, H, K] and dense dictionary matrices M [K, N, N] (or per head [H, K, N, N])."""
+    if stream is not None:
+        return _results_on(stream, logits, lambda: soft_select(logits, M, tau, N))
     Bt, L, H, K = logits.shape
     N = M.shape[-1]
     flags = FLAG_HEAD_DICTS if M.dim() == 4 else 0
@@ -377,7 +401,7 @@ def soft_select(logits: torch.Tensor, M: torch.Tensor, tau: float = 1.0, N: Opti
                  d_t=F32, state_t=F32, out_t=F32, flags=flags)
     ws = torch.empty(pdssm_soft_select_workspace_size(pb), dtype=torch.uint8, device=logits.device)
     steps = torch.empty(Bt, L, H, N, dtype=torch.uint8, device=logits.device)
-    pdssm_soft_select(pb, logits.contiguous(), M.contiguous(), tau, steps, ws, stream)
+    pdssm_soft_select(pb, logits.contiguous(), M.contiguous(), tau, steps, ws)
     return {"idx_steps": steps, "workspace": ws}
 
 
@@ -385,6 +409,8 @@ def forward_steps(idx_steps: torch.Tensor, d: torch.Tensor, B: torch.Tensor, C: 
                   h0: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None, flags: int = 0,
                   stream=None) -> Dict[str, torch.Tensor]:
     """The scan with a transition per step (idx_steps [Bt, L, H, N] uint8), e.g. from soft_select."""
+    if stream is not None:
+        return _results_on(stream, B, lambda: forward_steps(idx_steps, d, B, C, x, h0, out_dtype, flags))
     Bt, L, H, N = B.shape
     P = x.shape[-1]
     if out_dtype is None:
@@ -398,7 +424,7 @@ def forward_steps(idx_steps: torch.Tensor, d: torch.Tensor, B: torch.Tensor, C: 
            "prod_val": torch.empty(Bt, H, N, dtype=torch.float32, device=dev)}
     ws = alloc_workspace(pb, dev)
     pdssm_scan_fwd_steps(pb, idx_steps, d, B, C, x, h0, out["y"], out["h_final"], out["prod_idx"], out["prod_val"],
-                         ws, stream)
+                         ws)
     out["workspace"] = ws
     return out
 
@@ -458,6 +484,9 @@ def forward(logits: torch.Tensor, idx: torch.Tensor, d: torch.Tensor, B: torch.T
             stream=None) -> Dict[str, torch.Tensor]:
     """Allocates the outputs (torch) and runs ``pdssm_forward`` on the inputs' device.
     A 3-D ``idx`` [heads, K, N] is a per-head dictionary (PDSSM_FLAG_HEAD_DICTS)."""
+    if stream is not None:
+        return _results_on(stream, B, lambda: forward(logits, idx, d, B, C, x, h0, out_dtype, chunk, flags, want_prod, want_s,
+                                                      workspace))
     flags |= _dict_flags(idx, B.shape[2], logits.shape[-1], B.shape[-1])
     pb = make_problem(logits, d, B, x, out_dtype=out_dtype, chunk=chunk, flags=flags)
     dev = B.device
@@ -476,7 +505,7 @@ def forward(logits: torch.Tensor, idx: torch.Tensor, d: torch.Tensor, B: torch.T
         out["s"] = torch.empty(Bt, L, H, dtype=torch.int32, device=dev)
     ws = workspace if workspace is not None else alloc_workspace(pb, dev)
     pdssm_forward(pb, logits, idx, d, B, C, x, h0, out["y"], out["h_final"], out.get("prod_idx"),
-                  out.get("prod_val"), out.get("s"), ws, stream)
+                  out.get("prod_val"), out.get("s"), ws)
     return out
 
 
@@ -487,6 +516,8 @@ def backward(logits: Optional[torch.Tensor], s: torch.Tensor, idx: torch.Tensor,
     """Allocates the gradients and runs ``pdssm_scan_bwd``; ``s`` are the forward's selections,
     ``dy`` has the forward output's dtype. dd and dh0 have the state's dtype (float32, or
     complex64 for a complex ``d``), the others are float32. No logits -> no ``dlogits``."""
+    if stream is not None:
+        return _results_on(stream, B, lambda: backward(logits, s, idx, d, B, C, x, dy, h0, dh_final, tau, want_dh0, workspace))
     K = logits.shape[-1] if logits is not None else int(idx.shape[-2])
     pb = make_problem(logits, d, B, x, out_dtype=dy.dtype, K=K,
                       flags=_dict_flags(idx, B.shape[2], K, B.shape[-1]))
@@ -504,7 +535,7 @@ def backward(logits: Optional[torch.Tensor], s: torch.Tensor, idx: torch.Tensor,
     ws = workspace if workspace is not None else torch.empty(max(1, pdssm_bwd_workspace_size(pb)),
                                                               dtype=torch.uint8, device=dev)
     pdssm_scan_bwd(pb, logits, s, idx, d, B, C, x, h0, dy, dh_final, tau, out.get("dlogits"), out["dd"], out["dB"],
-                   out["dC"], out["dx"], out.get("dh0"), ws, stream)
+                   out["dC"], out["dx"], out.get("dh0"), ws)
     return out
 
 
@@ -531,14 +562,6 @@ def _addr(tensors, index: int):
         else:
             _ptr(t, torch.device("cuda", index))  # says what is wrong with it
     return out
-
-
-def _used_on(stream, index: int, tensors) -> None:
-    """Tensors allocated here for a call on ``stream``: the allocator must not reuse them before it is done."""
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_handle(stream, index), index)
-    for t in tensors:
-        if t is not None:
-            t.record_stream(s)
 
 
 def _size(fn, pb, where: str) -> int:
@@ -636,21 +659,18 @@ def qk_norm(q: torch.Tensor, k: torch.Tensor, wq: Optional[torch.Tensor] = None,
     2 * len(inv_freq) values by position (``positions`` int32 [Bt, L]; None: the token's place in its
     sequence). ``mode``: "rms" or "l2". Results: "q", "k", written to ``q_out`` / ``k_out`` where given
     (which may be q and k themselves)."""
+    if stream is not None:
+        return _results_on(stream, q, lambda: qk_norm(q, k, wq, wk, inv_freq, positions, eps, mode, interleaved, q_out, k_out))
     pb = _norm_problem(q, k, wq, wk, inv_freq, positions, eps, mode, interleaved)
-    new = []
     if q_out is None:
         q_out = torch.empty_like(q)
-        new.append(q_out)
     else:
         _expect("q_out", q_out, q.shape, q.dtype)
     if k_out is None:
         k_out = torch.empty_like(k)
-        new.append(k_out)
     else:
         _expect("k_out", k_out, k.shape, q.dtype)
-    pdssm_qk_norm(pb, q, k, wq, wk, inv_freq, positions, q_out, k_out, stream)
-    if stream is not None:
-        _used_on(stream, q.get_device(), new)
+    pdssm_qk_norm(pb, q, k, wq, wk, inv_freq, positions, q_out, k_out)
     return {"q": q_out, "k": k_out}
 
 
@@ -661,6 +681,9 @@ def qk_norm_backward(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_
                      stream=None) -> Dict[str, torch.Tensor]:
     """Gradients of ``qk_norm`` from its inputs and its outputs' gradients: "dq", "dk" and, for each weight
     given, "dwq", "dwk" (float32)."""
+    if stream is not None:
+        return _results_on(stream, q, lambda: qk_norm_backward(q, k, dq_out, dk_out, wq, wk, inv_freq, positions, eps, mode,
+                                                               interleaved))
     pb = _norm_problem(q, k, wq, wk, inv_freq, positions, eps, mode, interleaved)
     _expect("dq_out", dq_out, q.shape, q.dtype)
     _expect("dk_out", dk_out, k.shape, q.dtype)
@@ -673,9 +696,7 @@ def qk_norm_backward(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_
     if len(out) > 2:
         ws = torch.empty(pdssm_qk_norm_bwd_workspace_size(pb), dtype=torch.uint8, device=q.device)
     pdssm_qk_norm_bwd(pb, q, k, wq, wk, inv_freq, positions, dq_out, dk_out, out["dq"], out["dk"], out.get("dwq"),
-                      out.get("dwk"), ws, stream)
-    if stream is not None:
-        _used_on(stream, q.get_device(), [ws, *out.values()])
+                      out.get("dwk"), ws)
     return out
 
 
@@ -729,22 +750,20 @@ def delta_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     ``pdssm_delta_workspace_size`` bytes, one for each call that may run at the same time (allocated when None;
     a size of 0 needs none); ``pdssm_read_device_check`` reads its error word. What a call whose bounded waits
     ran out could not finish is NaN."""
+    if stream is not None:
+        return _results_on(stream, q, lambda: delta_forward(q, k, v, g, beta, h0, scale, lengths, h_final, want_h_final, flags,
+                                                            workspace))
     pb, key = _delta_problem(q, k, v, g, beta, h0, scale, lengths, flags)
     y = torch.empty_like(v)
-    new = [y]
     if h_final is not None:
         _expect("h_final", h_final, (key[0], key[2], key[4], key[5]), torch.float32)
     elif want_h_final:
         h_final = torch.empty_like(h0) if h0 is not None else v.new_empty((key[0], key[2], key[4], key[5]), dtype=torch.float32)
-        new.append(h_final)
     if workspace is None:
         n = _workspace_bytes(pdssm_delta_workspace_size, pb, key)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-            new.append(workspace)
-    pdssm_delta_fwd(pb, q, k, v, g, beta, lengths, h0, y, h_final, workspace, stream)
-    if stream is not None:
-        _used_on(stream, q.get_device(), new)
+    pdssm_delta_fwd(pb, q, k, v, g, beta, lengths, h0, y, h_final, workspace)
     return {"y": y} if h_final is None else {"y": y, "h_final": h_final}
 
 
@@ -756,6 +775,9 @@ def delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     """Gradients of ``delta_forward`` for dy (like v) and dh_final (float32 [Bt, H, N, P] or None: zeros):
     "dq", "dk" (summed over the value heads that share a key head), "dv", "dg", "dbeta", each in the type of what
     it belongs to, and "dh0" (by default where an h0 is given)."""
+    if stream is not None:
+        return _results_on(stream, q, lambda: delta_backward(q, k, v, g, beta, dy, h0, dh_final, scale, lengths, want_dh0, flags,
+                                                             workspace))
     pb, key = _delta_problem(q, k, v, g, beta, h0, scale, lengths, flags)
     state = (key[0], key[2], key[4], key[5])
     _expect("dy", dy, v.shape, v.dtype)
@@ -765,13 +787,9 @@ def delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     dh0 = None
     if want_dh0 or (want_dh0 is None and h0 is not None):
         dh0 = v.new_empty(state, dtype=torch.float32)
-    new = [dq, dk, dv, dg, db, dh0]
     if workspace is None:
         workspace = torch.empty(_workspace_bytes(pdssm_delta_bwd_workspace_size, pb, key), dtype=torch.uint8, device=q.device)
-        new.append(workspace)
-    pdssm_delta_bwd(pb, q, k, v, g, beta, lengths, h0, dy, dh_final, dq, dk, dv, dg, db, dh0, workspace, stream)
-    if stream is not None:
-        _used_on(stream, q.get_device(), new)
+    pdssm_delta_bwd(pb, q, k, v, g, beta, lengths, h0, dy, dh_final, dq, dk, dv, dg, db, dh0, workspace)
     out = {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dbeta": db}
     if dh0 is not None:
         out["dh0"] = dh0
