@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaArgs a, int l
 template <int J>
 cudaError_t launch_j(const DeltaArgs &a, cudaStream_t st) {
   const Shape s = shape_of(J, a.N, a.Pp);
-  cudaError_t e = cudaFuncSetAttribute(delta_grad_kernel<J>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.bytes);
+  cudaError_t e = allow_shared(delta_grad_kernel<J>);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((a.L + kC - 1) / kC), (unsigned)a.Hk, (unsigned)a.Bt);
   delta_grad_kernel<J><<<grid, kThreads, s.bytes, st>>>(a, s.ldn, s.ldp);

@@ -542,7 +542,7 @@ cudaError_t launch_jc(const DeltaArgs &a, bool bwd, const char *name, cudaStream
   const bool own = warps < kMaxWarps;
   auto kern = bwd ? (own ? delta_rows_both_kernel<J, CW, true> : delta_rows_both_kernel<J, CW, false>)
                   : (own ? delta_rows_kernel<J, CW, true> : delta_rows_kernel<J, CW, false>);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_shared(kern);
   if (e != cudaSuccess || (e = trace_before(st, name)) != cudaSuccess) return e;
   uintptr_t all16 = reinterpret_cast<uintptr_t>(a.v) | reinterpret_cast<uintptr_t>(bwd ? a.dy : a.y);
   all16 |= reinterpret_cast<uintptr_t>(a.h0) | reinterpret_cast<uintptr_t>(a.h_final) | reinterpret_cast<uintptr_t>(a.dv) |

@@ -32,6 +32,14 @@ struct ScanArgs {
 cudaError_t trace_before(cudaStream_t st, const char *kernel_name);
 cudaError_t trace_after(cudaStream_t st);
 
+// Lets a kernel without shared memory of a fixed size be launched with all that a block can have. The limit belongs
+// to the kernel, not to a launch: with what one call needs, a call of another host thread that needs more would be
+// refused between setting its own limit and its launch.
+template <typename Kern>
+cudaError_t allow_shared(Kern kern) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+}
+
 cudaError_t launch_select(int logits_t, const void *logits, int64_t rows, int K, int32_t *s,
                           cudaStream_t st);
 cudaError_t launch_prep_dict(const int32_t *idx, int K, int N, const Workspace &ws,

@@ -506,7 +506,7 @@ cudaError_t launch_scan_bwd(const ScanBwdArgs &s, cudaStream_t st) {
     PDSSM_BWD_KERNEL(kBTWhole)
   }
 #undef PDSSM_BWD_KERNEL
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(kern);
   if (e != cudaSuccess) return e;
   if ((e = trace_before(st, "scan_bwd")) != cudaSuccess) return e;
   kern<<<(unsigned)(s.Bt * s.H * s.nPB), split ? kBTSplit : kBTWhole, smem, st>>>(a);

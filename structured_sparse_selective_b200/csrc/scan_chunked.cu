@@ -514,7 +514,7 @@ cudaError_t launch_dyn(Kern kern, const char *name, dim3 grid, int threads, size
                        const KParams &k) {
   cudaError_t e;
   if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = allow_shared(kern);
     if (e != cudaSuccess) return e;
   }
   if ((e = trace_before(st, name)) != cudaSuccess) return e;

@@ -1172,7 +1172,7 @@ cudaError_t launch_fused_scan(const ScanArgs &s, cudaStream_t st) {
                              : fused_scan_kernel<__nv_bfloat16, __nv_bfloat16, false>)
                   : (precise ? fused_scan_kernel<float, float, true>
                              : fused_scan_kernel<float, __nv_bfloat16, false>);
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, off);
+  e = allow_shared(kern);
   if (e != cudaSuccess) return e;
   if ((e = trace_before(st, "fused_scan")) != cudaSuccess) return e;
   kern<<<(unsigned)(s.Bt * s.H), kThreads, off, st>>>(a);

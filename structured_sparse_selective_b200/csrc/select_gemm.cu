@@ -430,7 +430,7 @@ cudaError_t launch_soft_select(int64_t rows, int64_t H, int64_t N, int64_t K, in
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = trace_after(st)) != cudaSuccess) return e;
   const size_t smem = (size_t)2 * kSM * a.K16 * 2 + (size_t)4 * a.K16 * 256 * 2 + 64;
-  e = cudaFuncSetAttribute(soft_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = allow_shared(soft_select_kernel);
   if (e != cudaSuccess) return e;
   if ((e = trace_before(st, "soft_select")) != cudaSuccess) return e;
   soft_select_kernel<<<dim3((unsigned)((rows + kSM - 1) / kSM), (unsigned)H), kPThreads, smem, st>>>(a);
@@ -463,7 +463,7 @@ cudaError_t launch_proj_select(int64_t rows, int64_t D, int64_t H, int64_t K, co
   a.logits = logits;
   a.err = err;
   const size_t smem = proj_select_smem_bytes(H, K);
-  cudaError_t e = cudaFuncSetAttribute(proj_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(proj_select_kernel);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((rows + kPM - 1) / kPM), (unsigned)(a.HK / a.ntile));
   if ((e = trace_before(st, "proj_select")) != cudaSuccess) return e;
