@@ -203,38 +203,41 @@ def _ptr(t: Optional[torch.Tensor], device: Optional[torch.device] = None):
     return ctypes.c_void_p(t.data_ptr()) if t.numel() > 0 else ctypes.c_void_p(t.data_ptr() or 0)
 
 
+_get_device, _current_handle = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _handle(stream, index: int) -> int:
     """The stream's handle; None: the current stream of CUDA device ``index``."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
+        return _current_handle(index)
     if getattr(stream, "device_index", index) != index:
         raise ValueError(f"stream of cuda:{stream.device_index}, tensors on cuda:{index}")
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _launch(fn, index: int, stream, *args) -> int:
+def _launch(fn, index: int, stream, args) -> int:
     """fn(*args, stream handle) with CUDA device ``index`` current: the handle of a default stream is 0 on every
     device, and the library takes it for the current device's."""
+    if stream is None and _get_device() == index:
+        return fn(*args, _current_handle(index))
     handle = _handle(stream, index)
-    if index == torch._C._cuda_getDevice():
-        return fn(*args, handle)
     with torch.cuda.device(index):
         return fn(*args, handle)
 
 
-def _results_on(stream, t: torch.Tensor, call):
-    """call() with ``stream`` current. What it allocates is then the stream's: memory that work still queued on the
+def _results_on(stream, t: torch.Tensor, call, *args):
+    """call(*args) with ``stream`` current. What it allocates is then the stream's: memory that work still queued on the
     caller's own stream uses is not among it. The results are used on the caller's stream, and are not given out again
     before that is done with them."""
     index = _index(t)
     handle = _handle(stream, index)
     here = torch.cuda.current_stream(index)
     if handle == here.cuda_stream:
-        return call()
+        return call(*args)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(handle, index) if handle else torch.cuda.default_stream(index)
     with torch.cuda.stream(stream):
-        out = call()
+        out = call(*args)
     for r in out.values() if isinstance(out, dict) else (out,):
         r.record_stream(here)
     return out
@@ -263,7 +266,7 @@ def pdssm_workspace_size(pb: Problem) -> int:
 
 def pdssm_select(pb: Problem, logits: torch.Tensor, s: torch.Tensor, stream=None) -> None:
     dev = logits.device
-    _check(_launch(_lib.pdssm_select, dev.index, stream, ctypes.byref(pb), _ptr(logits, dev), _ptr(s, dev)),
+    _check(_launch(_lib.pdssm_select, dev.index, stream, (ctypes.byref(pb), _ptr(logits, dev), _ptr(s, dev))),
            "pdssm_select")
 
 
@@ -273,9 +276,9 @@ def pdssm_scan_fwd(pb: Problem, s, idx, d, B, C, x, h0, y, h_final, prod_idx, pr
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(_launch(
         _lib.pdssm_scan_fwd, dev.index, stream,
-        ctypes.byref(pb), _ptr(s, dev), _ptr(idx, dev), _ptr(d, dev), _ptr(B, dev), _ptr(C, dev),
-        _ptr(x, dev), _ptr(h0, dev), _ptr(y, dev), _ptr(h_final, dev), _ptr(prod_idx, dev),
-        _ptr(prod_val, dev), _ptr(workspace, dev), ws_bytes), "pdssm_scan_fwd")
+        (ctypes.byref(pb), _ptr(s, dev), _ptr(idx, dev), _ptr(d, dev), _ptr(B, dev), _ptr(C, dev),
+         _ptr(x, dev), _ptr(h0, dev), _ptr(y, dev), _ptr(h_final, dev), _ptr(prod_idx, dev),
+         _ptr(prod_val, dev), _ptr(workspace, dev), ws_bytes)), "pdssm_scan_fwd")
 
 
 def pdssm_forward(pb: Problem, logits, idx, d, B, C, x, h0, y, h_final, prod_idx, prod_val, s_out,
@@ -284,9 +287,9 @@ def pdssm_forward(pb: Problem, logits, idx, d, B, C, x, h0, y, h_final, prod_idx
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(_launch(
         _lib.pdssm_forward, dev.index, stream,
-        ctypes.byref(pb), _ptr(logits, dev), _ptr(idx, dev), _ptr(d, dev), _ptr(B, dev), _ptr(C, dev),
-        _ptr(x, dev), _ptr(h0, dev), _ptr(y, dev), _ptr(h_final, dev), _ptr(prod_idx, dev),
-        _ptr(prod_val, dev), _ptr(s_out, dev), _ptr(workspace, dev), ws_bytes), "pdssm_forward")
+        (ctypes.byref(pb), _ptr(logits, dev), _ptr(idx, dev), _ptr(d, dev), _ptr(B, dev), _ptr(C, dev),
+         _ptr(x, dev), _ptr(h0, dev), _ptr(y, dev), _ptr(h_final, dev), _ptr(prod_idx, dev),
+         _ptr(prod_val, dev), _ptr(s_out, dev), _ptr(workspace, dev), ws_bytes)), "pdssm_forward")
 
 
 def pdssm_forward_noalloc(pb: Problem, logits, idx, d, B, C, x, h0, y, h_final, prod_idx, prod_val,
@@ -295,9 +298,9 @@ def pdssm_forward_noalloc(pb: Problem, logits, idx, d, B, C, x, h0, y, h_final, 
     dev = idx.device
     _check(_launch(
         _lib.pdssm_forward_noalloc, dev.index, stream,
-        ctypes.byref(pb), _ptr(logits, dev), _ptr(idx, dev), _ptr(d, dev), _ptr(B, dev), _ptr(C, dev),
-        _ptr(x, dev), _ptr(h0, dev), _ptr(y, dev), _ptr(h_final, dev), _ptr(prod_idx, dev),
-        _ptr(prod_val, dev), _ptr(s_out, dev)), "pdssm_forward_noalloc")
+        (ctypes.byref(pb), _ptr(logits, dev), _ptr(idx, dev), _ptr(d, dev), _ptr(B, dev), _ptr(C, dev),
+         _ptr(x, dev), _ptr(h0, dev), _ptr(y, dev), _ptr(h_final, dev), _ptr(prod_idx, dev),
+         _ptr(prod_val, dev), _ptr(s_out, dev))), "pdssm_forward_noalloc")
 
 
 def pdssm_bwd_workspace_size(pb: Problem) -> int:
@@ -312,15 +315,15 @@ def pdssm_scan_bwd(pb: Problem, logits, s, idx, d, B, C, x, h0, dy, dh_final, ta
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(_launch(
         _lib.pdssm_scan_bwd, dev.index, stream,
-        ctypes.byref(pb), _ptr(logits, dev), _ptr(s, dev), _ptr(idx, dev), _ptr(d, dev), _ptr(B, dev),
-        _ptr(C, dev), _ptr(x, dev), _ptr(h0, dev), _ptr(dy, dev), _ptr(dh_final, dev), float(tau),
-        _ptr(dlogits, dev), _ptr(dd, dev), _ptr(dB, dev), _ptr(dC, dev), _ptr(dx, dev), _ptr(dh0, dev),
-        _ptr(workspace, dev), ws_bytes), "pdssm_scan_bwd")
+        (ctypes.byref(pb), _ptr(logits, dev), _ptr(s, dev), _ptr(idx, dev), _ptr(d, dev), _ptr(B, dev),
+         _ptr(C, dev), _ptr(x, dev), _ptr(h0, dev), _ptr(dy, dev), _ptr(dh_final, dev), float(tau),
+         _ptr(dlogits, dev), _ptr(dd, dev), _ptr(dB, dev), _ptr(dC, dev), _ptr(dx, dev), _ptr(dh0, dev),
+         _ptr(workspace, dev), ws_bytes)), "pdssm_scan_bwd")
 
 
 def pdssm_dict_hardmax(K: int, N: int, M: torch.Tensor, idx: torch.Tensor, stream=None) -> None:
     dev = M.device
-    _check(_launch(_lib.pdssm_dict_hardmax, dev.index, stream, int(K), int(N), _ptr(M, dev), _ptr(idx, dev)),
+    _check(_launch(_lib.pdssm_dict_hardmax, dev.index, stream, (int(K), int(N), _ptr(M, dev), _ptr(idx, dev))),
            "pdssm_dict_hardmax")
 
 
@@ -329,14 +332,14 @@ def pdssm_select_proj(pb: Problem, D: int, u, W, s, logits, workspace, stream=No
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(_launch(
         _lib.pdssm_select_proj, dev.index, stream,
-        ctypes.byref(pb), int(D), _ptr(u, dev), _ptr(W, dev), _ptr(s, dev),
-        _ptr(logits, dev), _ptr(workspace, dev), ws_bytes), "pdssm_select_proj")
+        (ctypes.byref(pb), int(D), _ptr(u, dev), _ptr(W, dev), _ptr(s, dev),
+         _ptr(logits, dev), _ptr(workspace, dev), ws_bytes)), "pdssm_select_proj")
 
 
 def dict_hardmax(M: torch.Tensor, stream=None) -> torch.Tensor:
     """Column-wise hardmax of dense matrices M [..., N, N] (float32): idx [..., N] int32."""
     if stream is not None:
-        return _results_on(stream, M, lambda: dict_hardmax(M))
+        return _results_on(stream, M, dict_hardmax, M)
     N = M.shape[-1]
     K = M.numel() // (N * N)
     idx = torch.empty(M.shape[:-2] + (N,), dtype=torch.int32, device=M.device)
@@ -348,7 +351,7 @@ def select_proj(u: torch.Tensor, W: torch.Tensor, heads: int, K: int, want_logit
                 stream=None) -> Dict[str, torch.Tensor]:
     """u [Bt, L, D] bf16, W [D, heads * K] bf16 -> s [Bt, L, heads] int32 (and logits [Bt, L, heads, K])."""
     if stream is not None:
-        return _results_on(stream, u, lambda: select_proj(u, W, heads, K, want_logits))
+        return _results_on(stream, u, select_proj, u, W, heads, K, want_logits)
     Bt, L, D = u.shape
     pb = Problem(batch=Bt, seqlen=L, heads=heads, N=1, P=1, K=K, chunk=0, logits_t=BF16, in_t=BF16, d_t=BF16,
                  state_t=F32, out_t=BF16, flags=0)
@@ -373,8 +376,8 @@ def pdssm_soft_select(pb: Problem, logits, M, tau: float, idx_steps, workspace, 
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(_launch(
         _lib.pdssm_soft_select, dev.index, stream,
-        ctypes.byref(pb), _ptr(logits, dev), _ptr(M, dev), float(tau), _ptr(idx_steps, dev),
-        _ptr(workspace, dev), ws_bytes), "pdssm_soft_select")
+        (ctypes.byref(pb), _ptr(logits, dev), _ptr(M, dev), float(tau), _ptr(idx_steps, dev),
+         _ptr(workspace, dev), ws_bytes)), "pdssm_soft_select")
 
 
 def pdssm_scan_fwd_steps(pb: Problem, idx_steps, d, B, C, x, h0, y, h_final, prod_idx, prod_val, workspace,
@@ -383,9 +386,9 @@ def pdssm_scan_fwd_steps(pb: Problem, idx_steps, d, B, C, x, h0, y, h_final, pro
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(_launch(
         _lib.pdssm_scan_fwd_steps, dev.index, stream,
-        ctypes.byref(pb), _ptr(idx_steps, dev), _ptr(d, dev), _ptr(B, dev), _ptr(C, dev), _ptr(x, dev),
-        _ptr(h0, dev), _ptr(y, dev), _ptr(h_final, dev), _ptr(prod_idx, dev), _ptr(prod_val, dev),
-        _ptr(workspace, dev), ws_bytes), "pdssm_scan_fwd_steps")
+        (ctypes.byref(pb), _ptr(idx_steps, dev), _ptr(d, dev), _ptr(B, dev), _ptr(C, dev), _ptr(x, dev),
+         _ptr(h0, dev), _ptr(y, dev), _ptr(h_final, dev), _ptr(prod_idx, dev), _ptr(prod_val, dev),
+         _ptr(workspace, dev), ws_bytes)), "pdssm_scan_fwd_steps")
 
 
 def soft_select(logits: torch.Tensor, M: torch.Tensor, tau: float = 1.0, N: Optional[int] = None,
@@ -393,7 +396,7 @@ def soft_select(logits: torch.Tensor, M: torch.Tensor, tau: float = 1.0, N: Opti
     """The original PD-SSM's per-step transitions: idx_steps [Bt, L, H, N] uint8 from logits
     [Bt, L, H, K] and dense dictionary matrices M [K, N, N] (or per head [H, K, N, N])."""
     if stream is not None:
-        return _results_on(stream, logits, lambda: soft_select(logits, M, tau, N))
+        return _results_on(stream, logits, soft_select, logits, M, tau, N)
     Bt, L, H, K = logits.shape
     N = M.shape[-1]
     flags = FLAG_HEAD_DICTS if M.dim() == 4 else 0
@@ -410,7 +413,7 @@ def forward_steps(idx_steps: torch.Tensor, d: torch.Tensor, B: torch.Tensor, C: 
                   stream=None) -> Dict[str, torch.Tensor]:
     """The scan with a transition per step (idx_steps [Bt, L, H, N] uint8), e.g. from soft_select."""
     if stream is not None:
-        return _results_on(stream, B, lambda: forward_steps(idx_steps, d, B, C, x, h0, out_dtype, flags))
+        return _results_on(stream, B, forward_steps, idx_steps, d, B, C, x, h0, out_dtype, flags)
     Bt, L, H, N = B.shape
     P = x.shape[-1]
     if out_dtype is None:
@@ -431,7 +434,7 @@ def forward_steps(idx_steps: torch.Tensor, d: torch.Tensor, B: torch.Tensor, C: 
 
 def pdssm_read_device_check(workspace: torch.Tensor, stream=None) -> int:
     """Status left in the workspace's error word by the last scan (synchronises)."""
-    return int(_launch(_lib.pdssm_read_device_check, workspace.device.index, stream, _ptr(workspace)))
+    return int(_launch(_lib.pdssm_read_device_check, workspace.device.index, stream, (_ptr(workspace),)))
 
 
 class KernelTrace:
@@ -485,8 +488,8 @@ def forward(logits: torch.Tensor, idx: torch.Tensor, d: torch.Tensor, B: torch.T
     """Allocates the outputs (torch) and runs ``pdssm_forward`` on the inputs' device.
     A 3-D ``idx`` [heads, K, N] is a per-head dictionary (PDSSM_FLAG_HEAD_DICTS)."""
     if stream is not None:
-        return _results_on(stream, B, lambda: forward(logits, idx, d, B, C, x, h0, out_dtype, chunk, flags, want_prod, want_s,
-                                                      workspace))
+        return _results_on(stream, B, forward, logits, idx, d, B, C, x, h0, out_dtype, chunk, flags, want_prod, want_s,
+                           workspace)
     flags |= _dict_flags(idx, B.shape[2], logits.shape[-1], B.shape[-1])
     pb = make_problem(logits, d, B, x, out_dtype=out_dtype, chunk=chunk, flags=flags)
     dev = B.device
@@ -517,7 +520,7 @@ def backward(logits: Optional[torch.Tensor], s: torch.Tensor, idx: torch.Tensor,
     ``dy`` has the forward output's dtype. dd and dh0 have the state's dtype (float32, or
     complex64 for a complex ``d``), the others are float32. No logits -> no ``dlogits``."""
     if stream is not None:
-        return _results_on(stream, B, lambda: backward(logits, s, idx, d, B, C, x, dy, h0, dh_final, tau, want_dh0, workspace))
+        return _results_on(stream, B, backward, logits, s, idx, d, B, C, x, dy, h0, dh_final, tau, want_dh0, workspace)
     K = logits.shape[-1] if logits is not None else int(idx.shape[-2])
     pb = make_problem(logits, d, B, x, out_dtype=dy.dtype, K=K,
                       flags=_dict_flags(idx, B.shape[2], K, B.shape[-1]))
@@ -543,7 +546,9 @@ def backward(logits: Optional[torch.Tensor], s: torch.Tensor, idx: torch.Tensor,
 
 _NORM_MODES = {"rms": 0, "l2": 1}
 _REAL = {torch.float32: F32, torch.bfloat16: BF16}
-_workspaces: Dict[tuple, int] = {}  # workspace bytes by problem (sizes, types and flags), so a call need not ask again
+# workspace bytes by problem (sizes, types and flags), forwards and backwards, so a call need not ask again
+_fwd_bytes: Dict[tuple, int] = {}
+_bwd_bytes: Dict[tuple, int] = {}
 
 
 def _expect(name: str, t: Optional[torch.Tensor], shape, dtype) -> None:
@@ -551,17 +556,19 @@ def _expect(name: str, t: Optional[torch.Tensor], shape, dtype) -> None:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
-def _addr(tensors, index: int):
-    """Device addresses of contiguous tensors on CUDA device ``index`` (None -> NULL)."""
-    out = []
+def _addr(args: list, tensors, index: int, size: Optional[int] = None) -> list:
+    """``args`` and behind them the device addresses of contiguous tensors on CUDA device ``index`` (None -> NULL) and
+    the size of a workspace that is the last of them."""
     for t in tensors:
         if t is None:
-            out.append(None)
+            args.append(None)
         elif t.get_device() == index and t.is_contiguous():
-            out.append(t.data_ptr())
+            args.append(t.data_ptr())
         else:
             _ptr(t, torch.device("cuda", index))  # says what is wrong with it
-    return out
+    if size is not None:
+        args.append(size)
+    return args
 
 
 def _size(fn, pb, where: str) -> int:
@@ -585,7 +592,7 @@ def _nbytes(workspace: Optional[torch.Tensor]) -> int:
 
 def pdssm_qk_norm(pb: NormProblem, q, k, wq, wk, inv_freq, positions, q_out, k_out, stream=None) -> None:
     i = _index(q)
-    st = _launch(_lib.pdssm_qk_norm, i, stream, pb, *_addr((q, k, wq, wk, inv_freq, positions, q_out, k_out), i))
+    st = _launch(_lib.pdssm_qk_norm, i, stream, _addr([pb], (q, k, wq, wk, inv_freq, positions, q_out, k_out), i))
     if st:
         raise PdssmError(st, "pdssm_qk_norm")
 
@@ -597,8 +604,8 @@ def pdssm_qk_norm_bwd_workspace_size(pb: NormProblem) -> int:
 def pdssm_qk_norm_bwd(pb: NormProblem, q, k, wq, wk, inv_freq, positions, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
                       stream=None) -> None:
     i = _index(q)
-    st = _launch(_lib.pdssm_qk_norm_bwd, i, stream, pb,
-                 *_addr((q, k, wq, wk, inv_freq, positions, dq_out, dk_out, dq, dk, dwq, dwk, workspace), i), _nbytes(workspace))
+    st = _launch(_lib.pdssm_qk_norm_bwd, i, stream, _addr(
+        [pb], (q, k, wq, wk, inv_freq, positions, dq_out, dk_out, dq, dk, dwq, dwk, workspace), i, _nbytes(workspace)))
     if st:
         raise PdssmError(st, "pdssm_qk_norm_bwd")
 
@@ -609,8 +616,8 @@ def pdssm_delta_workspace_size(pb: DeltaProblem) -> int:
 
 def pdssm_delta_fwd(pb: DeltaProblem, q, k, v, g, beta, lengths, h0, y, h_final, workspace, stream=None) -> None:
     i = _index(q)
-    st = _launch(_lib.pdssm_delta_fwd, i, stream, pb, *_addr((q, k, v, g, beta, lengths, h0, y, h_final, workspace), i),
-                 _nbytes(workspace))
+    st = _launch(_lib.pdssm_delta_fwd, i, stream, _addr(
+        [pb], (q, k, v, g, beta, lengths, h0, y, h_final, workspace), i, _nbytes(workspace)))
     if st:
         raise PdssmError(st, "pdssm_delta_fwd")
 
@@ -622,8 +629,8 @@ def pdssm_delta_bwd_workspace_size(pb: DeltaProblem) -> int:
 def pdssm_delta_bwd(pb: DeltaProblem, q, k, v, g, beta, lengths, h0, dy, dh_final, dq, dk, dv, dg, dbeta, dh0, workspace,
                     stream=None) -> None:
     i = _index(q)
-    st = _launch(_lib.pdssm_delta_bwd, i, stream, pb,
-                 *_addr((q, k, v, g, beta, lengths, h0, dy, dh_final, dq, dk, dv, dg, dbeta, dh0, workspace), i), _nbytes(workspace))
+    st = _launch(_lib.pdssm_delta_bwd, i, stream, _addr(
+        [pb], (q, k, v, g, beta, lengths, h0, dy, dh_final, dq, dk, dv, dg, dbeta, dh0, workspace), i, _nbytes(workspace)))
     if st:
         raise PdssmError(st, "pdssm_delta_bwd")
 
@@ -638,16 +645,17 @@ def _norm_problem(q, k, wq, wk, inv_freq, positions, eps, mode, interleaved) -> 
     kb, kl, Hk, kn = k.shape
     if kb != Bt or kl != L or kn != N or k.dtype is not dt:
         _expect("k", k, (Bt, L, Hk, N), dt)
-    if wq is not None:
-        _expect("wq", wq, (N,), torch.float32)
-    if wk is not None:
-        _expect("wk", wk, (N,), torch.float32)
-    if positions is not None:
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None and (w.shape != (N,) or w.dtype is not torch.float32):
+            _expect(name, w, (N,), torch.float32)
+    if positions is not None and (positions.shape != (Bt, L) or positions.dtype is not torch.int32):
         _expect("positions", positions, (Bt, L), torch.int32)
     rot = 0
     if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        _expect("inv_freq", inv_freq, (rot // 2,), torch.float32)
+        half = inv_freq.numel()
+        rot = 2 * half
+        if inv_freq.shape != (half,) or inv_freq.dtype is not torch.float32:
+            _expect("inv_freq", inv_freq, (half,), torch.float32)
     return NormProblem(Bt, L, Hq, Hk, N, _REAL[dt], _NORM_MODES[mode], rot, int(interleaved), eps, 0)
 
 
@@ -660,7 +668,7 @@ def qk_norm(q: torch.Tensor, k: torch.Tensor, wq: Optional[torch.Tensor] = None,
     sequence). ``mode``: "rms" or "l2". Results: "q", "k", written to ``q_out`` / ``k_out`` where given
     (which may be q and k themselves)."""
     if stream is not None:
-        return _results_on(stream, q, lambda: qk_norm(q, k, wq, wk, inv_freq, positions, eps, mode, interleaved, q_out, k_out))
+        return _results_on(stream, q, qk_norm, q, k, wq, wk, inv_freq, positions, eps, mode, interleaved, q_out, k_out)
     pb = _norm_problem(q, k, wq, wk, inv_freq, positions, eps, mode, interleaved)
     if q_out is None:
         q_out = torch.empty_like(q)
@@ -682,8 +690,8 @@ def qk_norm_backward(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_
     """Gradients of ``qk_norm`` from its inputs and its outputs' gradients: "dq", "dk" and, for each weight
     given, "dwq", "dwk" (float32)."""
     if stream is not None:
-        return _results_on(stream, q, lambda: qk_norm_backward(q, k, dq_out, dk_out, wq, wk, inv_freq, positions, eps, mode,
-                                                               interleaved))
+        return _results_on(stream, q, qk_norm_backward, q, k, dq_out, dk_out, wq, wk, inv_freq, positions, eps, mode,
+                           interleaved)
     pb = _norm_problem(q, k, wq, wk, inv_freq, positions, eps, mode, interleaved)
     _expect("dq_out", dq_out, q.shape, q.dtype)
     _expect("dk_out", dk_out, k.shape, q.dtype)
@@ -727,12 +735,12 @@ def _delta_problem(q, k, v, g, beta, h0, scale, lengths, flags):
     return DeltaProblem(Bt, L, H, Hk, N, P, key[6], key[7], N ** -0.5 if scale is None else scale, flags), key
 
 
-def _workspace_bytes(fn, pb: DeltaProblem, key: tuple) -> int:
-    n = _workspaces.get((fn.__name__,) + key)
+def _workspace_bytes(known: Dict[tuple, int], fn, pb: DeltaProblem, key: tuple) -> int:
+    n = known.get(key)
     if n is None:
-        if len(_workspaces) >= 4096:
-            _workspaces.clear()
-        n = _workspaces[(fn.__name__,) + key] = fn(pb)
+        if len(known) >= 4096:
+            known.clear()
+        n = known[key] = fn(pb)
     return n
 
 
@@ -751,8 +759,8 @@ def delta_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     a size of 0 needs none); ``pdssm_read_device_check`` reads its error word. What a call whose bounded waits
     ran out could not finish is NaN."""
     if stream is not None:
-        return _results_on(stream, q, lambda: delta_forward(q, k, v, g, beta, h0, scale, lengths, h_final, want_h_final, flags,
-                                                            workspace))
+        return _results_on(stream, q, delta_forward, q, k, v, g, beta, h0, scale, lengths, h_final, want_h_final, flags,
+                           workspace)
     pb, key = _delta_problem(q, k, v, g, beta, h0, scale, lengths, flags)
     y = torch.empty_like(v)
     if h_final is not None:
@@ -760,7 +768,7 @@ def delta_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     elif want_h_final:
         h_final = torch.empty_like(h0) if h0 is not None else v.new_empty((key[0], key[2], key[4], key[5]), dtype=torch.float32)
     if workspace is None:
-        n = _workspace_bytes(pdssm_delta_workspace_size, pb, key)
+        n = _workspace_bytes(_fwd_bytes, pdssm_delta_workspace_size, pb, key)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     pdssm_delta_fwd(pb, q, k, v, g, beta, lengths, h0, y, h_final, workspace)
@@ -776,8 +784,8 @@ def delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     "dq", "dk" (summed over the value heads that share a key head), "dv", "dg", "dbeta", each in the type of what
     it belongs to, and "dh0" (by default where an h0 is given)."""
     if stream is not None:
-        return _results_on(stream, q, lambda: delta_backward(q, k, v, g, beta, dy, h0, dh_final, scale, lengths, want_dh0, flags,
-                                                             workspace))
+        return _results_on(stream, q, delta_backward, q, k, v, g, beta, dy, h0, dh_final, scale, lengths, want_dh0, flags,
+                           workspace)
     pb, key = _delta_problem(q, k, v, g, beta, h0, scale, lengths, flags)
     state = (key[0], key[2], key[4], key[5])
     _expect("dy", dy, v.shape, v.dtype)
@@ -788,7 +796,8 @@ def delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     if want_dh0 or (want_dh0 is None and h0 is not None):
         dh0 = v.new_empty(state, dtype=torch.float32)
     if workspace is None:
-        workspace = torch.empty(_workspace_bytes(pdssm_delta_bwd_workspace_size, pb, key), dtype=torch.uint8, device=q.device)
+        n = _workspace_bytes(_bwd_bytes, pdssm_delta_bwd_workspace_size, pb, key)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     pdssm_delta_bwd(pb, q, k, v, g, beta, lengths, h0, dy, dh_final, dq, dk, dv, dg, db, dh0, workspace)
     out = {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dbeta": db}
     if dh0 is not None:

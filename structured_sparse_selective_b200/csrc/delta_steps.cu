@@ -402,7 +402,6 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + kLoaders)) delta_steps_both_
 // their own; k^T H and q^T H are finished by three shuffles.
 template <int J, typename T, typename G>
 __global__ void __launch_bounds__(128) delta_token_kernel(DeltaArgs a) {
-  clear_error(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane >> 2;
   const int col = (blockIdx.x * (blockDim.x >> 5) + warp) * 16 + 4 * (lane & 3);
   const int64_t h = blockIdx.y, b = blockIdx.z, bh = b * a.H + h, hk = h / (a.H / a.Hk);
@@ -472,6 +471,7 @@ __global__ void __launch_bounds__(128) delta_token_kernel(DeltaArgs a) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) y[c] += __shfl_xor_sync(0xffffffffu, y[c], o);
   }
+  clear_error(a);  // here, where nothing waits for it any more
   if (rg == 0) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)

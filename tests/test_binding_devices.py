@@ -52,8 +52,8 @@ def calls(monkeypatch):
     for name in ENTRIES:
         replace(name)
     monkeypatch.setattr(torch.cuda, "device", device)
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: state["device"])
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0)  # the default stream, on any device
+    monkeypatch.setattr(pd, "_get_device", lambda: state["device"])
+    monkeypatch.setattr(pd, "_current_handle", lambda index: 0)  # the default stream, on any device
     yield seen
     assert state["device"] == 0
 
