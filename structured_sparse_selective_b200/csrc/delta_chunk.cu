@@ -391,7 +391,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
       if (i + 1 < chunks && !fetch_v(next, turn)) goto state_done;
       if (!wait(kDoneD, ph)) goto state_done;
       tc_fence_after();
-      const float last = scal[3 * kChunk];
+      const float last = scal[3 * kChunk], rest = scal[3 * kChunk + 1];
       {
         float d[WN];
         if constexpr (WN == 64) {
@@ -401,7 +401,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
           load_cols<PM, WN>(tD, d);
         }
 #pragma unroll
-        for (int n = 0; n < WN; ++n) st[n] = fmaf(last, st[n], d[n]);
+        for (int n = 0; n < WN; ++n) st[n] = fmaf(last, st[n], fmaf(rest, st[n], d[n]));
       }
       // where u's parts lie among those of the state, the product with A has to be done too
       if (Lay::kUy < Lay::kD) {

@@ -12,7 +12,7 @@ constexpr int kChunk = 64;
 // Read K-major it is [rows c][k = j], read MN-major [k = c][columns j].
 constexpr int kSquare = kChunk * kChunk * 2;
 constexpr int kChunkGroup = kChunk * 16 + 16;  // bytes of eight columns of K or Q; 16 more spread the banks
-// exp(G), exp(G_64 - G), beta, exp(G_64), and G to the base 2 as two floats, 64 values each
+// exp(G), exp(G_64 - G), beta, exp(G_64) in two parts (in turn), and G to the base 2 as two floats, 64 values each
 constexpr int kScalars = 6 * kChunk * 4;
 // Record of a chunk: Te (3 parts), backward also Tb (3 parts), A (2 parts, backward 3), scalars.
 constexpr int delta_a_parts(bool bwd) { return bwd ? 3 : 2; }

@@ -280,7 +280,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
             if (c < n) *tv = __float2bfloat16_rn(w[c]);
         }
       }
-      const float last = scal[3 * kChunk];
+      const float last = scal[3 * kChunk], rest = scal[3 * kChunk + 1];
       if (!wait(kDoneD, ph)) goto state_done;
       tc_fence_after();
       {
@@ -292,7 +292,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, bool wide, bool wide_v, 
           load_cols<PM, WN>(tD, d);
         }
 #pragma unroll
-        for (int n = 0; n < WN; ++n) st[n] = fmaf(last, st[n], d[n]);
+        for (int n = 0; n < WN; ++n) st[n] = fmaf(last, st[n], fmaf(rest, st[n], d[n]));
       }
       tc_fence_before();
       __syncwarp();

@@ -198,7 +198,9 @@ __global__ void __launch_bounds__(kThreads, NP == 64 ? 6 : 4) delta_prep_kernel(
         if (lane >= o) sum += up;
       }
       const double last = __shfl_sync(0xffffffffu, sum, 31), G[2] = {sum - g1, sum};
-      const float all = decay2((float)last);
+      // the state's decay over the chunk, as a float and what that lacks: hundreds of them are multiplied
+      const double all = exp2(last);
+      const float2 two = make_float2((float)all, (float)(all - (double)(float)all));
       float grow[2], fade[2], bt[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, NP == 64 ? 6 : 4) delta_prep_kernel(
       out[lane] = make_float2(grow[0], grow[1]);
       out[32 + lane] = make_float2(fade[0], fade[1]);
       out[64 + lane] = make_float2(bt[0], bt[1]);
-      out[96 + lane] = make_float2(all, all);
+      out[96 + lane] = two;
       out[128 + lane] = make_float2((float)G[0], (float)G[1]);
       out[160 + lane] = make_float2((float)(G[0] - (double)(float)G[0]), (float)(G[1] - (double)(float)G[1]));
       if (hh + 1 < r_heads) fetch_gates(h + 1);

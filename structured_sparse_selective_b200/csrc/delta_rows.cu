@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kC = 32;        // steps a chunk
 constexpr int kTri = kC * kC;  // values of a triangle
-constexpr int kScal = 4 * kC;  // exp G, exp(G_32 - G), beta, exp(G_32)
+constexpr int kScal = 4 * kC;  // exp G, exp(G_32 - G), beta, exp(G_32) in two parts
 
 // Values of a record. A key head's: K [n / 4][step][4], K^T [step / 4][n][4], then Q as K, or
 // (backward) Q^T as K^T. A value head's: Te [j / 4][step][4], the scalars, then A as Te, or
@@ -126,7 +126,9 @@ __global__ void __launch_bounds__(32 * kPrepWarps, BWD ? 2 : 4) delta_rows_prep_
     rec[kTri + lane] = decay2(hi);
     rec[kTri + kC + lane] = decay2((float)(last - sum));
     rec[kTri + 2 * kC + lane] = beta;
-    rec[kTri + 3 * kC + lane] = decay2((float)last);
+    // the state's decay over the chunk, as a float and what that lacks: hundreds of them are multiplied
+    const double all = exp2(last);
+    rec[kTri + 3 * kC + lane] = lane & 1 ? (float)(all - (double)(float)all) : (float)all;
     __syncwarp();  // nt and tt: the head before has been read, or K and Q
     float row[kC];
 #pragma unroll
@@ -397,7 +399,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, int group, int warps, in
     }
     __syncwarp();
     if (!__all_sync(0xffffffffu, wait_bar(&bars[s], turn & 1, a.err, a.wait_ns))) break;
-    const float grow = scal[lane], fade = scal[kC + lane], beta = scal[2 * kC + lane], last = scal[3 * kC];
+    const float grow = scal[lane], fade = scal[kC + lane], beta = scal[2 * kC + lane], last = scal[3 * kC], rest = scal[3 * kC + 1];
     if constexpr (WHAT != kBack) {
       float y[CW];
       {
@@ -433,7 +435,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, int group, int warps, in
         pair2 acc[CW] = {};
         mul<CW, kC / 4>(KT + 32 * j, NP, b1, acc);
 #pragma unroll
-        for (int c = 0; c < CW; ++c) st[j][c] = fmaf(last, st[j][c], both(acc[c]));
+        for (int c = 0; c < CW; ++c) st[j][c] = fmaf(last, st[j][c], fmaf(rest, st[j][c], both(acc[c])));
       }
       if constexpr (WHAT == kForward) {
         pair2 acc[CW] = {};
@@ -484,7 +486,7 @@ __device__ __forceinline__ void run(const DeltaArgs &a, int group, int warps, in
         mul<CW, kC / 4>(third + 32 * j, NP, b1, acc);
         mul<CW, kC / 4>(KT + 32 * j, NP, b3, acc);
 #pragma unroll
-        for (int c = 0; c < CW; ++c) st[j][c] = fmaf(last, st[j][c], both(acc[c]));
+        for (int c = 0; c < CW; ++c) st[j][c] = fmaf(last, st[j][c], fmaf(rest, st[j][c], both(acc[c])));
       }
     }
     __syncwarp();

@@ -27,21 +27,23 @@ constexpr int kMaxCols = 64;     // their columns
 constexpr int kLoaders = 4;      // loader w has the tiles w, w + 4, ...
 
 // One tile in shared memory: rows of k and q (padded with zeros to 32 J), of the
-// block's columns of v (or dy), and (a, beta).
+// block's columns of v (or dy), (a, beta), and what the tile's decays lack together,
+// relative to them: the state is multiplied by 1 + that once a tile.
 template <int J>
 struct Tile {
   static constexpr int kRow = 32 * J;
-  float *k, *q, *c;
+  float *k, *q, *c, *rest;
   float2 *ab;
   __device__ Tile(float *base, int cols, int buf) {
-    const int one = kTS * (2 * kRow + cols + 2);
+    const int one = kTS * (2 * kRow + cols + 2) + 4;
     base += buf * one;
     k = base;
     q = base + kTS * kRow;
     c = base + 2 * kTS * kRow;
     ab = reinterpret_cast<float2 *>(c + kTS * cols);
+    rest = reinterpret_cast<float *>(ab + kTS);
   }
-  static size_t bytes(int cols) { return (size_t)2 * kTS * (2 * kRow + cols + 2) * 4; }
+  static size_t bytes(int cols) { return (size_t)2 * (kTS * (2 * kRow + cols + 2) + 4) * 4; }
 };
 
 // A loader warp, with every fourth tile. A tile's values wait in registers: fetch() starts
@@ -108,7 +110,12 @@ struct Loader {
         if (i < cols) tile.c[s * cols + i] = p0 + i < a.P ? to_f32(cv[s][j]) : 0.f;
       }
     }
-    if (lane < kTS) tile.ab[lane] = make_float2(expf(clamp_gate(to_f32(gv))), to_f32(bv));
+    const Decay d = decay_of(to_f32(gv));
+    if (lane < kTS) tile.ab[lane] = make_float2(d.a, to_f32(bv));
+    float rest = lane < n && d.rest != 0.f ? d.rest / d.a : 0.f;
+#pragma unroll
+    for (int o = kTS / 2; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+    if (lane == 0) *tile.rest = rest;
   }
 };
 
@@ -221,6 +228,11 @@ __device__ __forceinline__ void forward(const DeltaArgs &a, int group) {
     const Tile<J> tile(smem, cols, buf), after(smem, cols, buf ^ 1);
     if (SAVE && room && (t0 & (a.C - 1)) == 0)  // a.C is a multiple of kTS
       store_column<J>(st, a.carry + (bh * a.nC + t0 / a.C) * a.N * a.Pp + col, l, N, a.Pp);
+    const pair2 rest = pack2(*tile.rest, *tile.rest);
+#pragma unroll
+    for (int r = 0; r < R; ++r) st[r] = fma2(rest, st[r], st[r]);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) d[r] = fma2(rest, d[r], d[r]);
     const float *kl = tile.k + 4 * l, *ql = tile.q + 4 * l, *cl = tile.c + c;
     // everything a step reads comes ahead of the shuffles that it waits for
     const auto one = [&](int s, bool last, bool has_y) {
@@ -323,6 +335,9 @@ __device__ __forceinline__ void backward(const DeltaArgs &a, int group) {
     const Tile<J> tile(smem, cols, buf), before(smem, cols, buf ^ 1);
     if (room && (i == 0 || ((t0 + kTS) & (a.C - 1)) == 0))  // a.C is a multiple of kTS
       store_column<J>(x, a.xcarry + (bh * a.nC + t0 / a.C) * a.N * a.Pp + col, l, N, a.Pp);
+    const pair2 rest = pack2(*tile.rest, *tile.rest);
+#pragma unroll
+    for (int r = 0; r < R; ++r) x[r] = fma2(rest, x[r], x[r]);
     const float *kl = tile.k + 4 * l, *ql = tile.q + 4 * l, *cl = tile.c + c;
     const auto one = [&](int s) {
       const float2 ab = tile.ab[s];
@@ -431,7 +446,7 @@ __global__ void __launch_bounds__(128) delta_token_kernel(DeltaArgs a) {
       for (int c = 0; c < 4; ++c) st[i][c] = 0.f;
   }
   float k[4 * J], q[4 * J], v[4] = {}, y[4] = {};
-  float decay = 1.f, beta = 0.f;
+  float beta = 0.f;
   if (on) {
     const T *kp = static_cast<const T *>(a.k) + (b * a.Hk + hk) * N, *qp = static_cast<const T *>(a.q) + (b * a.Hk + hk) * N;
 #pragma unroll
@@ -441,7 +456,7 @@ __global__ void __launch_bounds__(128) delta_token_kernel(DeltaArgs a) {
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) v[c] = ldf(static_cast<const T *>(a.v) + bh * P + min(col + c, P - 1));
-    decay = expf(clamp_gate(ldf(static_cast<const G *>(a.g) + bh)));
+    const Decay decay = decay_of(ldf(static_cast<const G *>(a.g) + bh));
     beta = ldf(static_cast<const G *>(a.beta) + bh);
 #pragma unroll
     for (int i = 0; i < 4 * J; ++i) {
@@ -459,10 +474,10 @@ __global__ void __launch_bounds__(128) delta_token_kernel(DeltaArgs a) {
       for (int c = 0; c < 4; ++c) d[c] += __shfl_xor_sync(0xffffffffu, d[c], o);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const float u = beta * fmaf(-decay, d[c], v[c]);
+      const float u = beta * fmaf(-decay.a, d[c], v[c]);
 #pragma unroll
       for (int i = 0; i < 4 * J; ++i) {
-        st[i][c] = fmaf(k[i], u, decay * st[i][c]);
+        st[i][c] = fmaf(k[i], u, fmaf(decay.a, st[i][c], decay.rest * st[i][c]));
         y[c] = fmaf(q[i], st[i][c], y[c]);
       }
     }

@@ -1,0 +1,94 @@
+"""The delta rule's fp32 results on the GPU at the precision that they are promised with.
+
+Errors are norms over a (sequence, head)'s slice, relative, in units of 2^-24 (half a step of fp32, the largest relative error of one
+rounding; of a norm over many values a rounding makes about 1 / sqrt(3) of it).
+"""
+import pytest
+import torch
+
+import structured_sparse_selective_b200 as pd
+
+pytestmark = pytest.mark.gpu
+
+UNIT = 2.0 ** -24
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def off(got, want):
+    """The largest slice's error in units; slices are the leading two dimensions."""
+    d, w = (got.double() - want).flatten(2), want.flatten(2)
+    return float((d.norm(dim=-1) / w.norm(dim=-1)).max()) / UNIT
+
+
+# --------------------------------------------------------------- slow decays over long sequences
+
+LONG = 8192
+
+
+def slow_case(dt, g, N, P, seed=3, L=LONG, H=2):
+    """Decays so slow that the state remembers hundreds of chunks: exp(g) is a little off as a float, and is multiplied that often."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=gen)  # noqa: E731
+    unit = lambda x: x / x.norm(dim=-1, keepdim=True)  # noqa: E731
+    g = torch.full((1, L, H), g, device="cuda") if g is not None else -1e-4 * rand(1, L, H).abs()
+    a = dict(q=unit(rand(1, L, H, N)).to(dt), k=unit(rand(1, L, H, N)).to(dt), v=rand(1, L, H, P).to(dt), g=g,
+             beta=torch.full((1, L, H), 0.002, device="cuda"))
+    return a, rand(1, H, N, P), rand(1, L, H, P).to(dt), rand(1, H, N, P)
+
+
+def last_state(a, h):
+    k, v, f, b = a["k"].double(), a["v"].double(), a["g"].double().exp(), a["beta"].double()
+    h = h.double()
+    for t in range(v.shape[1]):
+        h = f[:, t, :, None, None] * h
+        e = v[:, t] - torch.matmul(k[:, t, :, None, :], h).squeeze(-2)
+        h = h + k[:, t, :, :, None] * (b[:, t, :, None] * e)[:, :, None, :]
+    return h
+
+
+def first_adjoint(a, dy, x):
+    q, k, f, b = a["q"].double() * a["q"].shape[-1] ** -0.5, a["k"].double(), a["g"].double().exp(), a["beta"].double()
+    dy, x = dy.double(), x.double()
+    for t in range(dy.shape[1] - 1, -1, -1):
+        x = x + q[:, t, :, :, None] * dy[:, t, :, None, :]
+        dv = b[:, t, :, None] * torch.matmul(k[:, t, :, None, :], x).squeeze(-2)
+        x = f[:, t, :, None, None] * (x - k[:, t, :, :, None] * dv[:, :, None, :])
+    return x
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("N,P", [(32, 32), (96, 80)])
+@pytest.mark.parametrize("g", [-1e-4, -3e-4, None])
+def test_slow_decays_by_chunks(dt, N, P, g):
+    """A chunk multiplies the state once: with a factor that is off by a float's half step, 128 chunks would be off by up to 128 units.
+    With an exact one there are two roundings a chunk, 0.6 sqrt(2 x 128) = 9 units, and those of one chunk's products, 5; three times
+    that. (16 chunks or more are in memory.)"""
+    a, h0, dy, dh = slow_case(dt, g, N, P)
+    with pd.KernelTrace() as tr:
+        got, back = pd.delta_forward(**a, h0=h0), pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh)
+    assert not any("steps" in n for n in tr.names)
+    assert off(got["h_final"], last_state(a, h0)) <= 32
+    assert off(back["dh0"], first_adjoint(a, dy, dh)) <= 32
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("N,P", [(32, 32), (96, 80)])
+@pytest.mark.parametrize("g", [-1e-4, -3e-4, None])
+def test_slow_decays_by_steps(dt, N, P, g):
+    """A factor that is off by a float's half step would be off by up to 8,192 units. Two roundings a step are 0.6 sqrt(2 x 8,192) = 74
+    units where they are independent; those of neighbouring steps are not, since the state changes little: eight times that."""
+    a, h0, dy, dh = slow_case(dt, g, N, P)
+    got = pd.delta_forward(**a, h0=h0, flags=pd.FLAG_REFERENCE_PATH)
+    back = pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh, flags=pd.FLAG_REFERENCE_PATH)
+    assert off(got["h_final"], last_state(a, h0)) <= 592
+    assert off(back["dh0"], first_adjoint(a, dy, dh)) <= 592
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_slow_decays_token_by_token(dt):
+    """As by steps, 2,000 of them: eight times 0.6 sqrt(2 x 2,000)."""
+    a, h0, _, _ = slow_case(dt, -1e-4, 64, 64, L=2000)
+    state, tokens = h0.clone(), [{n: x[:, t:t + 1].contiguous() for n, x in a.items()} for t in range(2000)]
+    for tok in tokens:
+        pd.delta_forward(**tok, h0=state, h_final=state)
+    assert off(state, last_state(a, h0)) <= 300
