@@ -459,6 +459,9 @@ pdssm_status pdssm_delta_fwd(const pdssm_delta_problem *pb, const void *q, const
  *   dq, dk   in_t [batch][seqlen][qk_heads][N]: sums over the value heads that share a key head
  *   dv       in_t [batch][seqlen][heads][P];  dg, dbeta  gate_t [batch][seqlen][heads]
  *   dh0      float [batch][heads][N][P] or NULL
+ * dg is 0 where exp(g) is 0 in fp32. By chunks of bf16 inputs it is a sum over the rest of the chunk whose
+ * terms cancel where the decay is strong: off by fp32's rounding of the terms (the sizes of <dy, y> and
+ * <dv, v>), not of dg; on the other paths by that of dg itself.
  * Each gradient has the type of what it belongs to and is rounded once. Rows behind a
  * sequence's length get zeros. No atomics: the same call gives the same bits.
  *   workspace pdssm_delta_bwd_workspace_size bytes, 16-byte aligned: an error word as above (on

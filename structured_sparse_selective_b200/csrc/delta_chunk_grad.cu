@@ -11,7 +11,10 @@
 // (X and H' at the chunk's end). The last line is the scaling identity of the recurrence:
 // making every state from step i on larger by a factor scales the outputs, and what the
 // values contribute does not take part. It needs no product but three dot products a row,
-// which stay in fp32, so the gates' gradients have fp32's precision.
+// which stay in fp32, so dg is exact to fp32's rounding of the sum's terms: off by some 2^-24 of
+// |<X, H'>| + sum over j >= i of (|<dy_j, y_j>| + beta_j |<du_j, v_j>|). Its value has the factor
+// exp(g_i), which no single term has: where the decay is strong, that is rounding of terms that cancel,
+// not of dg (csrc/delta_grad.cu sums terms that have the factor). Where exp(g_i) is 0 in fp32 dg_i is 0.
 //
 // The products have 64 rows (steps) and run on the tensor cores, operands in shared memory as two
 // bf16 parts (16 bits; dq and dk are rounded to bf16). Row scalings are applied where an
@@ -323,7 +326,10 @@ __global__ void __launch_bounds__(kThreads, NP == 64 && PP == 64 ? 2 : 1) delta_
         const int c = 2 * lane + k;
         if (c < rows) {
           const int64_t at = (row0 + c) * a.H + h;
-          store_any(a.dg, at, gb, c < live ? (float)(k ? s - (double)sdG[2 * lane] : s) : 0.f);
+          // the gate to the base 2 from its running sum; exp2(-150) is 0
+          const float *hi = scal + 4 * kChunk + c, *lo = scal + 5 * kChunk + c;
+          const float g2 = c ? (hi[0] - hi[-1]) + (lo[0] - lo[-1]) : hi[0] + lo[0];
+          store_any(a.dg, at, gb, c < live && !(g2 <= -150.f) ? (float)(k ? s - (double)sdG[2 * lane] : s) : 0.f);
           store_any(a.dbeta, at, gb, c < live ? sdb[c] : 0.f);
         }
       }

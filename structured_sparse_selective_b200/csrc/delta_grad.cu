@@ -9,9 +9,11 @@
 //   dq_i  = scale (gam_i H dy_i + sum_j F1_ij k_j)
 //   dk_i  = fade_i X u_i - beta_i gam_i H du_i + sum_j F1_ji qs_j + sum_j (F2_ij + F2_ji) k_j
 //   dbeta_i = <du_i, e_i>
-//   dG_i  = <qs_i, gam_i H dy_i> - <k_i, beta_i gam_i H du_i> - <k_i, fade_i X u_i>
-//           + sum_j (F1_ij <qs_i, k_j> + F2_ij <k_i, k_j>) - sum_j (F1_ji <qs_j, k_i> + F2_ji <k_j, k_i>)
-//   dG_C += last <X, H> + sum_i <k_i, fade_i X u_i>;  dg_i = sum of dG_j over j >= i
+//   dG_i  = <qs_i, gam_i H dy_i> - <k_i, beta_i gam_i H du_i>
+//           + sum_j (F1_ij <qs_i, k_j> + F2_ij <k_i, k_j>) - sum_j (F1_ji <qs_j, k_i> + F2_ji <k_j, k_i>)   (j < i, j > i)
+//   dg_i  = sum of dG_j over j >= i + last <X, H> + sum over j < i of <k_j, fade_j X u_j>
+// Every term has a factor exp(g); those of pairs behind step i cancel in dg_i up to their rounding (so where exp(g_i)
+// is 0 in fp32, dg_i is set to 0).
 //
 // A block has one chunk of 32 steps of one key head and goes through the value heads
 // that share it, so their sum for dq and dk stays in registers and needs neither
@@ -145,9 +147,12 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaArgs a, int l
     const int64_t h = hk * r_heads + hh, bh = b * a.H + h;
     const float *carry = a.carry + (bh * a.nC + chunk) * N * Pp, *xcarry = a.xcarry + (bh * a.nC + chunk) * N * Pp;
     __syncthreads();  // the arrays of the head before have been read
+    bool dropped = false;  // warp 0: the state before its step does not matter
     if (ty == 0) {
       const int64_t at = (row0 + tx) * a.H + h;
-      double G = tx < live ? (double)clamp_gate(load_any(a.g, at, gb)) : 0.0;
+      const float g = tx < live ? clamp_gate(load_any(a.g, at, gb)) : 0.f;
+      dropped = expf(g) == 0.f;
+      double G = (double)g;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const double up = __shfl_up_sync(0xffffffffu, G, o);
@@ -280,28 +285,32 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaArgs a, int l
         const float al = warp_sum(alpha[r]);
         if (tx == 0) {
           sx[i] = s;
-          sdG[i] += al - s;
+          sdG[i] += al;
         }
       }
     }
     __syncthreads();
     if (ty == 0) {
-      // the suffix sums of dG; what reaches dG_C reaches every dg of the chunk
-      float d = sdG[tx], xs = warp_sum(sx[tx]), xhs = 0.f;
+      // the suffix sums of dG, the sums of what goes out of the earlier steps (those of all steps less the suffix
+      // would leave the rounding of the last one's, which has no factor), and the state's way through the chunk
+      float d = sdG[tx], xhs = 0.f;
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
         d -= colp[w * kC + tx];
         xhs += swarp[w];
       }
-      double s = (double)d + (tx == 31 ? (double)fmaf(swarp[8], xhs, xs) : 0.0);
+      double s = (double)d, out = __shfl_up_sync(0xffffffffu, sx[tx], 1);
+      if (tx == 0) out = 0.0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const double dn = __shfl_down_sync(0xffffffffu, s, o);
+        const double dn = __shfl_down_sync(0xffffffffu, s, o), up = __shfl_up_sync(0xffffffffu, out, o);
         if (tx + o < 32) s += dn;
+        if (tx >= o) out += up;
       }
+      s += out + (double)(swarp[8] * xhs);
       if (tx < rows) {
         const int64_t at = (row0 + tx) * a.H + h;
-        store_any(a.dg, at, gb, tx < live ? (float)s : 0.f);
+        store_any(a.dg, at, gb, tx < live && !dropped ? (float)s : 0.f);
         store_any(a.dbeta, at, gb, tx < live ? sdb[tx] : 0.f);
       }
     }

@@ -3,10 +3,13 @@
 Errors are norms over a (sequence, head)'s slice, relative, in units of 2^-24 (half a step of fp32, the largest relative error of one
 rounding; of a norm over many values a rounding makes about 1 / sqrt(3) of it).
 """
+import numpy as np
 import pytest
 import torch
 
 import structured_sparse_selective_b200 as pd
+from oracle import layers
+from tests.test_gpu_layers import delta_case, gradients_in, npy
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +95,72 @@ def test_slow_decays_token_by_token(dt):
     for tok in tokens:
         pd.delta_forward(**tok, h0=state, h_final=state)
     assert off(state, last_state(a, h0)) <= 300
+
+
+# --------------------------------------------------------------- gradients of the gates where decays are strong
+
+PATHS = [(BF16, 300, 0), (BF16, 6, 0), (F32, 300, 0), (F32, 40, 0), (BF16, 150, pd.FLAG_REFERENCE_PATH)]
+
+
+@pytest.mark.parametrize("gates", [F32, BF16])
+@pytest.mark.parametrize("dt,L,flags", PATHS)
+def test_a_dropped_states_gate_has_no_gradient(dt, L, flags, gates):
+    a, h0 = delta_case((2, L, 2, 4, 64, 48), dt, gates)
+    dy, dh = gradients_in(a)
+    at = sorted({0, 1, L // 2, L - 1, min(63, L - 1), min(64, L - 1)})
+    a["g"][:, at[::2]] = -float("inf")
+    a["g"][:, at[1::2]] = -150.0
+    got = pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh, flags=flags)
+    assert not got["dg"][:, at].any()
+    assert not got["dh0"].any()  # the first step drops it
+
+
+def backward_oracle(a, h0, dy, dh, lengths=None):
+    x = [npy(a[n]) for n in ("q", "k", "v", "g", "beta")]
+    scale = a["q"].shape[-1] ** -0.5
+    y, h = layers.delta(*x, npy(h0), scale, lengths)
+    return y, h, layers.delta_backward(*x, npy(h0), scale, lengths, npy(dy), npy(dh))
+
+
+def gate_terms(a, y, h, want, dy, dh, chunk):
+    """|<X, H'>| + sum over the chunk's j >= i of |<dy_j, y_j>| + beta_j |<du_j, v_j>|: what dg_i is a sum of. X at a chunk's end with
+    the state there is the next step's dg."""
+    L = y.shape[1]
+    local = np.abs((npy(dy) * y).sum(-1)) + np.abs((want["dv"] * npy(a["v"])).sum(-1))
+    M = np.zeros_like(local)
+    for t0 in range(0, L, chunk):
+        t1 = min(L, t0 + chunk)
+        end = (npy(dh) * h).sum((-1, -2)) if t1 == L else want["dg"][:, t1]
+        M[:, t0:t1] = np.abs(end)[:, None] + local[:, t0:t1][:, ::-1].cumsum(1)[:, ::-1]
+    return M
+
+
+@pytest.mark.parametrize("bias", [0.0, 3.0, 10.0, 30.0])
+def test_gates_gradients_on_the_tensor_cores_against_their_terms(bias):
+    """y and du are off by some 7 units of their norm (three products a chunk, some 60 roundings of 0.6 units and four factors that
+    are off by up to 4): so is a dot product of such a row, of its usual size. The errors of a sum's terms are independent, 7 / sqrt(32)
+    for the usual number of terms; <X, H'> is one term of 7 sqrt(2). 5 units of the terms together."""
+    a, h0 = delta_case((1, 300, 1, 2, 64, 64), BF16, bias=bias)
+    dy, dh = gradients_in(a)
+    y, h, want = backward_oracle(a, h0, dy, dh)
+    got = npy(pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh)["dg"])
+    M = gate_terms(a, y, h, want, dy, dh, 64)
+    for i in range(2):
+        assert np.linalg.norm((got - want["dg"])[0, :, i]) <= 5 * UNIT * np.linalg.norm(M[0, :, i])
+
+
+@pytest.mark.parametrize("bias", [3.0, 10.0, 30.0])
+@pytest.mark.parametrize("dt,L,flags", [p for p in PATHS if p[:2] != (BF16, 300)])
+def test_gates_gradients_where_every_term_decays_are_exact_relatively(dt, L, flags, bias):
+    """The other paths sum terms that have the factor. An exponent of size |g| is off by |g| units and a term with it, its products by
+    some 8; a step's sum has the later steps' of its chunk of 32 too, which cancel up to their rounding. A step's terms are up to three
+    times their sum."""
+    a, h0 = delta_case((1, L, 1, 2, 64, 64), dt, bias=bias)
+    dy, dh = gradients_in(a)
+    want = backward_oracle(a, h0, dy, dh)[2]["dg"]
+    got = npy(pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh, flags=flags)["dg"])
+    size = float(a["g"].abs().max())
+    for i in range(2):
+        w = np.abs(want[0, :, i])
+        M = np.concatenate([w[t:t + 32][::-1].cumsum()[::-1] for t in range(0, L, 32)])
+        assert np.linalg.norm((got - want)[0, :, i]) <= 3 * (8 + size) * UNIT * np.linalg.norm(M)
