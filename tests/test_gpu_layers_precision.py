@@ -8,12 +8,11 @@ import pytest
 import torch
 
 import structured_sparse_selective_b200 as pd
-from oracle import layers
+from tests.layers_precision import BOUNDS, UNIT, backward_oracle, gate_terms, slices_off
 from tests.test_gpu_layers import delta_case, gradients_in, npy
 
 pytestmark = pytest.mark.gpu
 
-UNIT = 2.0 ** -24
 BF16, F32 = torch.bfloat16, torch.float32
 
 
@@ -115,38 +114,15 @@ def test_a_dropped_states_gate_has_no_gradient(dt, L, flags, gates):
     assert not got["dh0"].any()  # the first step drops it
 
 
-def backward_oracle(a, h0, dy, dh, lengths=None):
-    x = [npy(a[n]) for n in ("q", "k", "v", "g", "beta")]
-    scale = a["q"].shape[-1] ** -0.5
-    y, h = layers.delta(*x, npy(h0), scale, lengths)
-    return y, h, layers.delta_backward(*x, npy(h0), scale, lengths, npy(dy), npy(dh))
-
-
-def gate_terms(a, y, h, want, dy, dh, chunk):
-    """|<X, H'>| + sum over the chunk's j >= i of |<dy_j, y_j>| + beta_j |<du_j, v_j>|: what dg_i is a sum of. X at a chunk's end with
-    the state there is the next step's dg."""
-    L = y.shape[1]
-    local = np.abs((npy(dy) * y).sum(-1)) + np.abs((want["dv"] * npy(a["v"])).sum(-1))
-    M = np.zeros_like(local)
-    for t0 in range(0, L, chunk):
-        t1 = min(L, t0 + chunk)
-        end = (npy(dh) * h).sum((-1, -2)) if t1 == L else want["dg"][:, t1]
-        M[:, t0:t1] = np.abs(end)[:, None] + local[:, t0:t1][:, ::-1].cumsum(1)[:, ::-1]
-    return M
-
-
 @pytest.mark.parametrize("bias", [0.0, 3.0, 10.0, 30.0])
 def test_gates_gradients_on_the_tensor_cores_against_their_terms(bias):
-    """y and du are off by some 7 units of their norm (three products a chunk, some 60 roundings of 0.6 units and four factors that
-    are off by up to 4): so is a dot product of such a row, of its usual size. The errors of a sum's terms are independent, 7 / sqrt(32)
-    for the usual number of terms; <X, H'> is one term of 7 sqrt(2). 5 units of the terms together."""
     a, h0 = delta_case((1, 300, 1, 2, 64, 64), BF16, bias=bias)
     dy, dh = gradients_in(a)
     y, h, want = backward_oracle(a, h0, dy, dh)
     got = npy(pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh)["dg"])
-    M = gate_terms(a, y, h, want, dy, dh, 64)
+    M = gate_terms(a, h0, y, want, dy, dh, 64)
     for i in range(2):
-        assert np.linalg.norm((got - want["dg"])[0, :, i]) <= 5 * UNIT * np.linalg.norm(M[0, :, i])
+        assert np.linalg.norm((got - want["dg"])[0, :, i]) <= BOUNDS["dg"] * UNIT * np.linalg.norm(M[0, :, i])
 
 
 @pytest.mark.parametrize("bias", [3.0, 10.0, 30.0])
@@ -164,3 +140,23 @@ def test_gates_gradients_where_every_term_decays_are_exact_relatively(dt, L, fla
         w = np.abs(want[0, :, i])
         M = np.concatenate([w[t:t + 32][::-1].cumsum()[::-1] for t in range(0, L, 32)])
         assert np.linalg.norm((got - want)[0, :, i]) <= 3 * (8 + size) * UNIT * np.linalg.norm(M)
+
+
+# --------------------------------------------------------------- states and gates' gradients on every path
+
+CASES = [  # batch, seqlen, qk_heads, heads, N, P: the tensor cores' four kernels, with states and adjoints in one launch and in two
+    (1, 600, 1, 2, 64, 64), (1, 300, 1, 2, 128, 128), (2, 200, 1, 2, 96, 48), (1, 200, 2, 2, 40, 100), (5, 130, 4, 16, 64, 64),
+    (5, 130, 4, 16, 72, 80), (1, 40, 1, 2, 64, 64), (1, 8, 1, 2, 64, 64), (6, 100, 8, 16, 32, 32),
+]
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("c", CASES)
+@pytest.mark.parametrize("bias", [-2.5, -8.0])
+def test_fp32_results_are_exact_to_fp32(c, dt, bias):
+    a, h0 = delta_case(c, dt, bias=bias)
+    dy, dh = gradients_in(a)
+    y, h, want = backward_oracle(a, h0, dy, dh)
+    got = {n: npy(x) for n, x in (pd.delta_forward(**a, h0=h0) | pd.delta_backward(**a, dy=dy, h0=h0, dh_final=dh)).items()}
+    for n, x in slices_off(got, h, want, gate_terms(a, h0, y, want, dy, dh, 64)).items():
+        assert x <= BOUNDS[n], (n, x)
