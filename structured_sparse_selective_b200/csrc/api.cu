@@ -111,9 +111,14 @@ Workspace carve(const Plan &p, void *ws) {
   return w;
 }
 
-// Makes the device that owns `stream` current for this library's runtime.
+// Makes the device that owns `stream` current for this library's runtime. A capturing stream
+// may not be asked for its device (the question ends the capture): there the caller has that
+// device current, as the capture needs it anyway.
 pdssm_status bind_device(cudaStream_t stream) {
   if (stream == nullptr) return PDSSM_OK;
+  cudaStreamCaptureStatus capturing;
+  if (cudaStreamIsCapturing(stream, &capturing) != cudaSuccess) return PDSSM_ERR_CUDA;
+  if (capturing != cudaStreamCaptureStatusNone) return PDSSM_OK;
   int dev = -1;
   if (cudaStreamGetDevice(stream, &dev) != cudaSuccess) return PDSSM_ERR_CUDA;
   int cur = -1;
