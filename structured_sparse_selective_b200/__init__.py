@@ -27,6 +27,9 @@ The functions keep the C names:
 another, allocate the results and call these. ``forward(...)`` is a convenience wrapper that allocates the outputs and the
 workspace with torch and calls ``pdssm_forward``; ``backward(...)`` does the
 same for ``pdssm_scan_bwd``.
+
+A call runs on its tensors' device, current or not, on ``stream`` (a torch stream of that device or a handle; None: the
+device's current one). What the wrappers allocate for a call on another stream belongs to that stream.
 """
 from __future__ import annotations
 

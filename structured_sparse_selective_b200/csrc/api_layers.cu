@@ -90,7 +90,12 @@ constexpr size_t kErrBytes = 256;
 //   backward  256: 8 steps 56, 56; 16 steps 64, 57; 64 steps 140, 53
 //             2,048: 8 steps 829, 431
 // A chunk costs the same however few of its steps there are; steps cost their number, more
-// where four sequences or more share an SM.
+// where four sequences or more share an SM. The rule does not look at P, nor at N below 64; there it is
+// not always the faster one:
+//   forward   N = P = 32: 256: 64 steps 16, 31; 2,048: 16 steps 35, 151; 64 steps 86, 154
+//             64 x 8: 2,048: 16 steps 35, 151; 64 steps 95, 152.  128 x 128: 256: 16 steps 62, 43; 64 steps 189, 43
+//   backward  N = P = 32: 2,048: 16 steps 198, 321; 32 steps 265, 330.  64 x 8: 2,048: 32 steps 263, 327
+//             128 x 128: 256: 4 steps 174, 108; 32 steps 267, 114
 bool chunks_apply(const pdssm_delta_problem *pb, bool bwd) {
   if (pb->in_t != PDSSM_BF16 || (pb->flags & PDSSM_FLAG_REFERENCE_PATH)) return false;
   if (bwd) return pb->seqlen > 8;
@@ -103,8 +108,13 @@ bool chunks_apply(const pdssm_delta_problem *pb, bool bwd) {
 //             N = 128: S = 64: 64 steps 46, 50; 128 steps 85, 82.  S = 256: 128 steps 308, 240; 512 steps 1205, 864.
 //   backward  N = 64:  S = 64: 64 steps 46, 37; 128 steps 80, 53; 512 steps 268, 151.  S = 256: 512 steps 474, 491.
 //             N = 128: S = 64: 64 steps 92, 80; 512 steps 638, 450.  S = 256: 512 steps 2033, 1433.
+//   forward   N = 32:  S = 8: 128 steps 19, 17; 512 steps 60, 25.  S = 64: 128 steps 19, 21; 512 steps 62, 39.
+//                      S = 256: 512 steps 80, 115.  S = 1024: 512 steps 303, 384.
+//   backward  N = 32:  S = 64: 64 steps 35, 35; 512 steps 179, 129.  S = 256: 512 steps 495, 466.
 // A step's chain of shuffles is what few sequences wait for; many fill the SMs either way, and then
 // steps do fewer FMAs, unless a head is so large that its columns do not fit in a few registers a lane.
+// The rule does not look at P: with N = 128 and P = 8 (S = 256: 512 steps 176, 251; S = 1024: 680, 1084) steps would
+// be the faster ones, with N = 32 and P = 128 (S = 64: 512 steps 80, 86) it is even.
 bool rows_apply(const pdssm_delta_problem *pb, bool bwd) {
   if (pb->in_t != PDSSM_F32 || (pb->flags & PDSSM_FLAG_REFERENCE_PATH)) return false;
   if (pb->N > 64) return pb->seqlen > (bwd ? 64 : 96);
