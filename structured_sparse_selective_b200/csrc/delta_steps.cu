@@ -27,23 +27,21 @@ constexpr int kMaxCols = 64;     // their columns
 constexpr int kLoaders = 4;      // loader w has the tiles w, w + 4, ...
 
 // One tile in shared memory: rows of k and q (padded with zeros to 32 J), of the
-// block's columns of v (or dy), (a, beta), and what the tile's decays lack together,
-// relative to them: the state is multiplied by 1 + that once a tile.
+// block's columns of v (or dy), and (a, beta).
 template <int J>
 struct Tile {
   static constexpr int kRow = 32 * J;
-  float *k, *q, *c, *rest;
+  float *k, *q, *c;
   float2 *ab;
   __device__ Tile(float *base, int cols, int buf) {
-    const int one = kTS * (2 * kRow + cols + 2) + 4;
+    const int one = kTS * (2 * kRow + cols + 2);
     base += buf * one;
     k = base;
     q = base + kTS * kRow;
     c = base + 2 * kTS * kRow;
     ab = reinterpret_cast<float2 *>(c + kTS * cols);
-    rest = reinterpret_cast<float *>(ab + kTS);
   }
-  static size_t bytes(int cols) { return (size_t)2 * (kTS * (2 * kRow + cols + 2) + 4) * 4; }
+  static size_t bytes(int cols) { return (size_t)2 * kTS * (2 * kRow + cols + 2) * 4; }
 };
 
 // A loader warp, with every fourth tile. A tile's values wait in registers: fetch() starts
@@ -61,6 +59,7 @@ struct Loader {
   int64_t rowk, rowc;
   T kv[kTS][J], qv[kTS][J], cv[kTS][M];
   G gv, bv;
+  float place;  // where the lane's step rounds its decay, in (-1/2, 1/2)
 
   // `src`: v forwards, dy backwards.
   __device__ Loader(const DeltaArgs &a_, int64_t b, int64_t h, int p0_, int cols_, const void *src)
@@ -92,6 +91,7 @@ struct Loader {
     const int64_t t = (t0 + min(lane, n - 1)) * a.H;
     gv = g[t];
     bv = beta[t];
+    place = (float)((int)((uint32_t)(t0 + lane) * 2654435769u) >> 8) * 0x1p-24f;
   }
 
   __device__ __forceinline__ void put(const Tile<J> &tile) {
@@ -110,12 +110,11 @@ struct Loader {
         if (i < cols) tile.c[s * cols + i] = p0 + i < a.P ? to_f32(cv[s][j]) : 0.f;
       }
     }
+    // A decay's rest is paid in whole steps of the float (2^-24 below 1), in as many of the steps of the sequence as
+    // makes their product right: step t rounds at a place of its own, t times the golden section, which fills the
+    // interval evenly. A decay without a rest stays as it is.
     const Decay d = decay_of(to_f32(gv));
-    if (lane < kTS) tile.ab[lane] = make_float2(d.a, to_f32(bv));
-    float rest = lane < n && d.rest != 0.f ? d.rest / d.a : 0.f;
-#pragma unroll
-    for (int o = kTS / 2; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
-    if (lane == 0) *tile.rest = rest;
+    if (lane < kTS) tile.ab[lane] = make_float2(fmaf(rintf(fmaf(d.rest, 0x1p24f, place)), 0x1p-24f, d.a), to_f32(bv));
   }
 };
 
@@ -228,11 +227,6 @@ __device__ __forceinline__ void forward(const DeltaArgs &a, int group) {
     const Tile<J> tile(smem, cols, buf), after(smem, cols, buf ^ 1);
     if (SAVE && room && (t0 & (a.C - 1)) == 0)  // a.C is a multiple of kTS
       store_column<J>(st, a.carry + (bh * a.nC + t0 / a.C) * a.N * a.Pp + col, l, N, a.Pp);
-    const pair2 rest = pack2(*tile.rest, *tile.rest);
-#pragma unroll
-    for (int r = 0; r < R; ++r) st[r] = fma2(rest, st[r], st[r]);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) d[r] = fma2(rest, d[r], d[r]);
     const float *kl = tile.k + 4 * l, *ql = tile.q + 4 * l, *cl = tile.c + c;
     // everything a step reads comes ahead of the shuffles that it waits for
     const auto one = [&](int s, bool last, bool has_y) {
@@ -335,9 +329,6 @@ __device__ __forceinline__ void backward(const DeltaArgs &a, int group) {
     const Tile<J> tile(smem, cols, buf), before(smem, cols, buf ^ 1);
     if (room && (i == 0 || ((t0 + kTS) & (a.C - 1)) == 0))  // a.C is a multiple of kTS
       store_column<J>(x, a.xcarry + (bh * a.nC + t0 / a.C) * a.N * a.Pp + col, l, N, a.Pp);
-    const pair2 rest = pack2(*tile.rest, *tile.rest);
-#pragma unroll
-    for (int r = 0; r < R; ++r) x[r] = fma2(rest, x[r], x[r]);
     const float *kl = tile.k + 4 * l, *ql = tile.q + 4 * l, *cl = tile.c + c;
     const auto one = [&](int s) {
       const float2 ab = tile.ab[s];
