@@ -59,7 +59,7 @@ struct Loader {
   int64_t rowk, rowc;
   T kv[kTS][J], qv[kTS][J], cv[kTS][M];
   G gv, bv;
-  float place;  // where the lane's step rounds its decay, in (-1/2, 1/2)
+  uint32_t first, step;  // of the places where decays are rounded: the sequence's, and the lane's step
 
   // `src`: v forwards, dy backwards.
   __device__ Loader(const DeltaArgs &a_, int64_t b, int64_t h, int p0_, int cols_, const void *src)
@@ -70,6 +70,7 @@ struct Loader {
     c = static_cast<const T *>(src) + b * a.L * rowc + h * a.P;
     g = static_cast<const G *>(a.g) + b * a.L * a.H + h;
     beta = static_cast<const G *>(a.beta) + b * a.L * a.H + h;
+    first = live_steps(a.lengths, b, a.L) > 0 ? (__float_as_uint(to_f32(k[0])) * 2654435769u) ^ __float_as_uint(to_f32(c[0])) : 0;
   }
 
   // Steps [t0, t0 + steps), steps <= kTS; nothing for steps <= 0.
@@ -91,7 +92,7 @@ struct Loader {
     const int64_t t = (t0 + min(lane, n - 1)) * a.H;
     gv = g[t];
     bv = beta[t];
-    place = (float)((int)((uint32_t)(t0 + lane) * 2654435769u) >> 8) * 0x1p-24f;
+    step = (uint32_t)(t0 + lane);
   }
 
   __device__ __forceinline__ void put(const Tile<J> &tile) {
@@ -111,8 +112,10 @@ struct Loader {
       }
     }
     // A decay's rest is paid in whole steps of the float (2^-24 below 1), in as many of the steps of the sequence as
-    // makes their product right: step t rounds at a place of its own, t times the golden section, which fills the
-    // interval evenly. A decay without a rest stays as it is.
+    // makes their product right: step t rounds at a place of its own in [-1/2, 1/2), t times the golden section, which
+    // fills the interval evenly, from a first place by the first key and value, so that short calls one after the other
+    // do not all round alike. A decay without a rest stays as it is.
+    const float place = (float)((int)((first + step) * 2654435769u) >> 8) * 0x1p-24f;
     const Decay d = decay_of(to_f32(gv));
     if (lane < kTS) tile.ab[lane] = make_float2(fmaf(rintf(fmaf(d.rest, 0x1p24f, place)), 0x1p-24f, d.a), to_f32(bv));
   }

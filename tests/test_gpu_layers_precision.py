@@ -87,6 +87,18 @@ def test_slow_decays_by_steps(dt, N, P, g):
 
 
 @pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("g", [-1e-4, -1.3e-4, -1.7e-4])
+def test_slow_decays_by_short_segments(dt, g):
+    """Four steps a call, 2,000 calls: eight times 0.6 sqrt(2 x 8,000) as by steps (a rounding that is the same in each call would be
+    off by up to 8,000 units)."""
+    a, h0, _, _ = slow_case(dt, g, 64, 64, L=8000, H=1)
+    state = h0.clone()
+    for t in range(0, 8000, 4):
+        pd.delta_forward(**{n: x[:, t:t + 4].contiguous() for n, x in a.items()}, h0=state, h_final=state)
+    assert off(state, last_state(a, h0)) <= 600
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
 def test_slow_decays_token_by_token(dt):
     """As by steps, 2,000 of them: eight times 0.6 sqrt(2 x 2,000)."""
     a, h0, _, _ = slow_case(dt, -1e-4, 64, 64, L=2000)
