@@ -21,20 +21,25 @@ __device__ __forceinline__ float clamp_gate(float g) { return g < -110.f ? -110.
 // exp(g) as a float and what it lacks: exp(g) = d.a + d.rest, |d.rest| <= 2^-25 (2^-24 above 1). A state of slow decay
 // is multiplied by the same factors thousands of times, so half a step of the float, 2^-25, each time becomes 2^-11 of
 // the state after 2^14 steps. Near 1 the rest is known from exp(g) - 1, by its series (off by less than 2^-33 of 1);
-// what decays by more than exp(-1/8) is forgotten in a few steps.
+// what decays by more than exp(-1/8) is forgotten in a few steps. UNIFORM: all lanes have the same g and go one way
+// (one token of 64 sequences x 32 heads, 128 x 64: 30.5 -> 27.5 us; where lanes have steps of their own the branch makes
+// the chains of steps slower, 338 -> 379 us for 32 sequences of 4,000 steps, 32 x 32).
 struct Decay {
   float a, rest;
 };
+template <bool UNIFORM>
 __device__ __forceinline__ Decay decay_of(float g) {
   g = clamp_gate(g);
+  const bool near = fabsf(g) < 0.125f;
+  if (UNIFORM && !near) return {expf(g), 0.f};
   float m = fmaf(g, 1.f / 6, 1.f);
   m = fmaf(g * (1.f / 5), m, 1.f);
   m = fmaf(g * (1.f / 4), m, 1.f);
   m = fmaf(g * (1.f / 3), m, 1.f);
   m = fmaf(g * (1.f / 2), m, 1.f) * g;
-  const float a = 1.f + m;
-  const bool near = fabsf(g) < 0.125f;
-  return {near ? a : expf(g), near ? m - (a - 1.f) : 0.f};  // exact: |m| < 1
+  const float a = 1.f + m;  // a - 1 and what m has more are exact, |m| < 1
+  if (UNIFORM) return {a, m - (a - 1.f)};
+  return {near ? a : expf(g), near ? m - (a - 1.f) : 0.f};
 }
 
 // Steps of sequence b that count: its length clamped to [0, L], or L.

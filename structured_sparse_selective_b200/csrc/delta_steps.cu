@@ -116,7 +116,7 @@ struct Loader {
     // fills the interval evenly, from a first place by the first key and value, so that short calls one after the other
     // do not all round alike. A decay without a rest stays as it is.
     const float place = (float)((int)((first + step) * 2654435769u) >> 8) * 0x1p-24f;
-    const Decay d = decay_of(to_f32(gv));
+    const Decay d = decay_of<false>(to_f32(gv));
     if (lane < kTS) tile.ab[lane] = make_float2(fmaf(rintf(fmaf(d.rest, 0x1p24f, place)), 0x1p-24f, d.a), to_f32(bv));
   }
 };
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(128) delta_token_kernel(DeltaArgs a) {
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) v[c] = ldf(static_cast<const T *>(a.v) + bh * P + min(col + c, P - 1));
-    const Decay decay = decay_of(ldf(static_cast<const G *>(a.g) + bh));
+    const Decay decay = decay_of<true>(ldf(static_cast<const G *>(a.g) + bh));
     beta = ldf(static_cast<const G *>(a.beta) + bh);
 #pragma unroll
     for (int i = 0; i < 4 * J; ++i) {
